@@ -27,6 +27,9 @@ EXPORTED = (
     "w4a16_matmul", "w4a16_matmul_gemv_cutoff", "w4a16_quantize_act_i8", "w4a16_gemm_w4a8",
     "w4a16_matmul_w4a8", "w4a16_check_weights", "w4a16_matmul_noalloc", "w4a16_matmul_noalloc_max_scratch_bytes",
     "w4a16_prepared_bytes", "w4a16_prepare", "w4a16_gemv_prepared",
+    "w4a16_quantize_rows_i8", "w4a16_gemm_w8a8", "w4a16_matmul_w8a8", "w4a16_w8a8_workspace_bytes",
+    "w4a16_gemm_w8a8_experts", "w4a16_max_experts", "w4a16_expert_sort", "w4a16_expert_sort_workspace_bytes",
+    "w4a16_expert_gather", "w4a16_expert_gather_i8", "w4a16_expert_combine", "w4a16_expert_combine_backward",
 )
 
 
@@ -68,6 +71,22 @@ def _load() -> ctypes.CDLL:
     L.w4a16_quantize_act_i8.argtypes = [P, I64, I64, P, P, P, P]
     L.w4a16_gemm_w4a8.argtypes = [I, P, P, P, I64, P, P, P, I64, I64, P, P]
     L.w4a16_matmul_w4a8.argtypes = [I, P, I64, P, P, P, I64, I64, P, P]
+    L.w4a16_quantize_rows_i8.argtypes = [I, P, I64, I64, P, P, P]
+    L.w4a16_gemm_w8a8.argtypes = [I, I, P, P, I64, P, P, P, I64, I64, P, P]
+    L.w4a16_matmul_w8a8.argtypes = [I, I, P, I64, P, P, P, I64, I64, P, P, SZ, P]
+    L.w4a16_w8a8_workspace_bytes.argtypes, L.w4a16_w8a8_workspace_bytes.restype = [I, I64, I64, I64], SZ
+    L.w4a16_gemm_w8a8_experts.argtypes = [I, I, P, P, I64, P, I64, P, P, P, I64, I64, P, P]
+    L.w4a16_max_experts.argtypes, L.w4a16_max_experts.restype = [], I64
+    L.w4a16_expert_sort.argtypes = [P, I64, I64, I64, I64, P, P, P, P, SZ, P]
+    L.w4a16_expert_sort_workspace_bytes.argtypes, L.w4a16_expert_sort_workspace_bytes.restype = [I64, I64, I64], SZ
+    L.w4a16_expert_gather.argtypes = [I, P, I64, I64, P, I64, P, P]
+    L.w4a16_expert_gather_i8.argtypes = [I, P, I64, I64, P, I64, P, P, P]
+    L.w4a16_expert_combine.argtypes = [I, P, I64, I64, P, P, I64, P, P]
+    L.w4a16_expert_combine_backward.argtypes = [I, P, P, I64, I64, P, P, I64, P, P, P]
+    for name in ("w4a16_quantize_rows_i8", "w4a16_gemm_w8a8", "w4a16_matmul_w8a8", "w4a16_gemm_w8a8_experts",
+                 "w4a16_expert_sort", "w4a16_expert_gather", "w4a16_expert_gather_i8", "w4a16_expert_combine",
+                 "w4a16_expert_combine_backward"):
+        getattr(L, name).restype = I
     for name in ("w4a16_packed_sizes", "w4a16_quantize_pack", "w4a16_check_weights", "w4a16_dequant", "w4a16_gemv",
                  "w4a16_gemm", "w4a16_matmul", "w4a16_matmul_noalloc", "w4a16_quantize_act_i8", "w4a16_gemm_w4a8",
                  "w4a16_matmul_w4a8", "w4a16_prepare", "w4a16_gemv_prepared"):
@@ -200,6 +219,109 @@ def w4a16_matmul_w4a8(fmt: int, x, M: int, codes, scales, mins, N: int, K: int, 
         "w4a16_matmul_w4a8")
 
 
+# ---- W8A8 and the experts' operators --------------------------------------------------------------
+# Tensors given to these must be on one GPU, contiguous and at least as large as the call reads or
+# writes (W4A16_ERR_INVALID otherwise); the launch goes to that GPU's current stream, whichever GPU is
+# current.  Raw addresses are passed as they are.
+
+_ELEMENT = {W4A16_BF16: 2, W4A16_FP16: 2, W4A16_FP32: 4}
+
+
+def _element(dtype: int) -> int:
+    return _ELEMENT.get(dtype, 0)  # an unknown type is refused by the library
+
+
+def _call(name: str, args, arrays, stream) -> None:
+    """lib.<name>(*args): ``arrays`` gives the array arguments' places in ``args`` and the bytes each
+    must hold."""
+    import torch
+    device = None
+    args = list(args)
+    for at, nbytes in arrays:
+        t = args[at]
+        if isinstance(t, torch.Tensor):
+            d = t.get_device()
+            if d < 0 or (device is not None and d != device) or not t.is_contiguous() or t.nbytes < nbytes:
+                raise W4A16Error(W4A16_ERR_INVALID, name)
+            device = d
+            args[at] = t.data_ptr()
+    fn = getattr(lib, name)
+    if stream is not None or device is None or device == torch.cuda.current_device():
+        status = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _stream(None))
+    if status != W4A16_OK:
+        raise W4A16Error(status, name)
+
+
+def w4a16_quantize_rows_i8(act: int, x, M: int, K: int, xq, ascale, stream=None) -> None:
+    _call("w4a16_quantize_rows_i8", (act, x, M, K, xq, ascale),
+          ((1, M * K * _element(act)), (4, M * K), (5, 4 * M)), stream)
+
+
+def w4a16_gemm_w8a8(fmt: int, out: int, xq, ascale, M: int, codes, scales, mins, N: int, K: int, y, stream=None) -> None:
+    _call("w4a16_gemm_w8a8", (fmt, out, xq, ascale, M, codes, scales, mins, N, K, y),
+          ((2, M * K), (3, 4 * M), (5, N * K), (6, 4 * N), (7, 0), (10, M * N * _element(out))), stream)
+
+
+def w4a16_matmul_w8a8(fmt: int, act: int, x, M: int, codes, scales, mins, N: int, K: int, y, workspace,
+                      workspace_bytes: int, stream=None) -> None:
+    b = _element(act)
+    _call("w4a16_matmul_w8a8", (fmt, act, x, M, codes, scales, mins, N, K, y, workspace, workspace_bytes),
+          ((2, M * K * b), (4, N * K), (5, 4 * N), (6, 0), (9, M * N * b), (10, workspace_bytes)), stream)
+
+
+def w4a16_w8a8_workspace_bytes(fmt: int, M: int, N: int, K: int) -> int:
+    return int(lib.w4a16_w8a8_workspace_bytes(fmt, M, N, K))
+
+
+def w4a16_gemm_w8a8_experts(fmt: int, out: int, xq, ascale, R: int, offsets, E: int, codes, scales, mins, N: int, K: int,
+                            y, stream=None) -> None:
+    _call("w4a16_gemm_w8a8_experts", (fmt, out, xq, ascale, R, offsets, E, codes, scales, mins, N, K, y),
+          ((2, R * K), (3, 4 * R), (5, 4 * (E + 1)), (7, E * N * K), (8, 4 * E * N), (9, 0),
+           (12, R * N * _element(out))), stream)
+
+
+def w4a16_max_experts() -> int:
+    return int(lib.w4a16_max_experts())
+
+
+def w4a16_expert_sort_workspace_bytes(T: int, topk: int, E: int) -> int:
+    return int(lib.w4a16_expert_sort_workspace_bytes(T, topk, E))
+
+
+def w4a16_expert_sort(ids, id_bits: int, T: int, topk: int, E: int, offsets, pos, src, workspace=None,
+                      workspace_bytes: int = 0, stream=None) -> None:
+    P = T * topk
+    _call("w4a16_expert_sort", (ids, id_bits, T, topk, E, offsets, pos, src, workspace, workspace_bytes),
+          ((0, P * id_bits // 8), (5, 4 * (E + 1)), (6, 4 * P), (7, 4 * P), (8, workspace_bytes)), stream)
+
+
+def w4a16_expert_gather(act: int, x, T: int, topk: int, pos, K: int, xs, stream=None) -> None:
+    b = K * _element(act)
+    _call("w4a16_expert_gather", (act, x, T, topk, pos, K, xs), ((1, T * b), (4, 4 * T * topk), (6, T * topk * b)), stream)
+
+
+def w4a16_expert_gather_i8(act: int, x, T: int, topk: int, pos, K: int, xq, ascale, stream=None) -> None:
+    P = T * topk
+    _call("w4a16_expert_gather_i8", (act, x, T, topk, pos, K, xq, ascale),
+          ((1, T * K * _element(act)), (4, 4 * P), (6, P * K), (7, 4 * P)), stream)
+
+
+def w4a16_expert_combine(act: int, ys, T: int, topk: int, pos, weights, N: int, y, stream=None) -> None:
+    P, b = T * topk, N * _element(act)
+    _call("w4a16_expert_combine", (act, ys, T, topk, pos, weights, N, y), ((1, P * b), (4, 4 * P), (5, 4 * P), (7, T * b)),
+          stream)
+
+
+def w4a16_expert_combine_backward(act: int, dy, ys, T: int, topk: int, pos, weights, N: int, dys, dweights,
+                                  stream=None) -> None:
+    P, b = T * topk, N * _element(act)
+    _call("w4a16_expert_combine_backward", (act, dy, ys, T, topk, pos, weights, N, dys, dweights),
+          ((1, T * b), (2, P * b), (5, 4 * P), (6, 4 * P), (8, P * b), (9, 4 * P)), stream)
+
+
 # ---- memory plumbing (torch allocations with the ABI's shapes and dtypes) ------------------------
 
 def alloc_packed(fmt: int, N: int, K: int, device="cuda"):
@@ -242,3 +364,20 @@ def alloc_workspace(fmt: int, M: int, N: int, K: int, device="cuda"):
     if nbytes == 0:
         return None, 0
     return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
+
+
+def alloc_w8a8_workspace(fmt: int, M: int, N: int, K: int, device="cuda"):
+    """(tensor, bytes) sized for w4a16_matmul_w8a8 on this shape."""
+    import torch
+    nbytes = w4a16_w8a8_workspace_bytes(fmt, M, N, K)
+    return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
+
+
+def alloc_expert_sort(T: int, topk: int, E: int, device="cuda"):
+    """Empty (offsets [E + 1], pos [T][topk], src [T * topk], workspace or None, its bytes) for
+    w4a16_expert_sort."""
+    import torch
+    nbytes = w4a16_expert_sort_workspace_bytes(T, topk, E)
+    i32 = lambda *shape: torch.empty(shape, dtype=torch.int32, device=device)
+    return (i32(E + 1), i32(T, topk), i32(T * topk),
+            torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None, nbytes)

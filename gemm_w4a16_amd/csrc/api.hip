@@ -67,6 +67,8 @@ w4a16_status_t check_act(w4a16_format_t fmt, w4a16_dtype_t act) {
     return W4A16_OK;
 }
 
+bool valid_dtype(w4a16_dtype_t t) { return t == W4A16_BF16 || t == W4A16_FP16 || t == W4A16_FP32; }
+
 w4a16_status_t from_hip(hipError_t e) { return e == hipSuccess ? W4A16_OK : W4A16_ERR_DEVICE; }
 
 // Largest fp32 values that still round to a finite 16-bit value under round-to-nearest-even: the
@@ -114,6 +116,37 @@ w4a16_status_t launch_rowmajor_rows(w4a16_format_t fmt, const void* x, int64_t M
                                                     static_cast<const uint16_t*>(mins), N, K, ya, stream));
     return from_hip(w4a16::launch_rowmma_w8row(xa, M, static_cast<const int8_t*>(codes),
                                                static_cast<const float*>(scales), N, K, ya, stream));
+}
+
+// ---- W8A8 and the experts' operators -----------------------------------------------------------
+// K below 2^17 keeps a sum of products of two int8 codes (at most 2^14 each) below 2^31.
+constexpr int64_t kMaxKInt8 = ((int64_t)1 << 17) - 1;
+
+w4a16_status_t check_w8a8(w4a16_format_t fmt, w4a16_dtype_t out, int64_t M, const void* codes, const void* scales,
+                          const void* mins, int64_t N, int64_t K, const void* y) {
+    if (w4a16_status_t st = check_shape(fmt, N, K); st != W4A16_OK) return st;
+    if (M <= 0 || M > kMaxDim || !valid_dtype(out) || !aligned16(y)) return W4A16_ERR_INVALID;
+    if (w4a16_status_t st = check_packed(fmt, codes, scales, mins); st != W4A16_OK) return st;
+    if (fmt != W4A16_FMT_W8_ROW_FP32 || K > kMaxKInt8) return W4A16_ERR_UNSUPPORTED;
+    return W4A16_OK;
+}
+
+// T tokens of `topk` pairs each, and rows of `width` elements.
+w4a16_status_t check_pairs(int64_t T, int64_t topk, int64_t width) {
+    if (T <= 0 || T > kMaxDim || topk <= 0 || topk > kMaxDim || width <= 0 || width > kMaxDim) return W4A16_ERR_INVALID;
+    if (topk > w4a16::kMaxExperts || T * topk > kMaxDim || width > kMaxK) return W4A16_ERR_UNSUPPORTED;
+    return W4A16_OK;
+}
+
+// matmul_w8a8's workspace: the codes of x, then its row scales.
+struct W8A8Workspace {
+    size_t ascale, total;
+};
+W8A8Workspace w8a8_workspace(int64_t M, int64_t K) {
+    W8A8Workspace w;
+    w.ascale = (size_t)M * (size_t)K;  // K % 16 == 0: 16-byte aligned
+    w.total = w.ascale + (size_t)M * 4;
+    return w;
 }
 
 // ---- The no-allocation entry point's scratch buffer -------------------------------------------
@@ -493,6 +526,127 @@ w4a16_status_t w4a16_matmul_w4a8(w4a16_format_t fmt, const void* x, int64_t M, c
                                                     static_cast<const uint16_t*>(scales),
                                                     static_cast<const uint16_t*>(mins), N, K, static_cast<uint16_t*>(y),
                                                     stream));
+}
+
+w4a16_status_t w4a16_quantize_rows_i8(w4a16_dtype_t act, const void* x, int64_t M, int64_t K, int8_t* xq, float* ascale,
+                                      hipStream_t stream) {
+    if (!valid_dtype(act) || M <= 0 || M > kMaxDim || K <= 0 || K > kMaxDim || K % kW8RowAlign != 0)
+        return W4A16_ERR_INVALID;
+    if (!aligned16(x) || !aligned16(xq) || !aligned16(ascale)) return W4A16_ERR_INVALID;
+    if (K > kMaxK) return W4A16_ERR_UNSUPPORTED;
+    w4a16::clear_stale_error();
+    return from_hip(w4a16::launch_quant_rows_i8((int)act, x, M, K, xq, ascale, stream));
+}
+
+w4a16_status_t w4a16_gemm_w8a8(w4a16_format_t fmt, w4a16_dtype_t out, const int8_t* xq, const float* ascale, int64_t M,
+                               const void* codes, const void* scales, const void* mins, int64_t N, int64_t K, void* y,
+                               hipStream_t stream) {
+    if (w4a16_status_t st = check_w8a8(fmt, out, M, codes, scales, mins, N, K, y); st != W4A16_OK) return st;
+    if (!aligned16(xq) || !aligned16(ascale)) return W4A16_ERR_INVALID;
+    if (!w4a16::w8a8_fits_grid(M, N, 1)) return W4A16_ERR_UNSUPPORTED;
+    w4a16::clear_stale_error();
+    return from_hip(w4a16::launch_gemm_w8a8((int)out, xq, ascale, M, static_cast<const int8_t*>(codes),
+                                            static_cast<const float*>(scales), N, K, y, nullptr, 1, stream));
+}
+
+size_t w4a16_w8a8_workspace_bytes(w4a16_format_t fmt, int64_t M, int64_t N, int64_t K) {
+    if (fmt != W4A16_FMT_W8_ROW_FP32 || check_shape(fmt, N, K) != W4A16_OK || M <= 0 || M > kMaxDim) return 0;
+    return w8a8_workspace(M, K).total;
+}
+
+w4a16_status_t w4a16_matmul_w8a8(w4a16_format_t fmt, w4a16_dtype_t act, const void* x, int64_t M, const void* codes,
+                                 const void* scales, const void* mins, int64_t N, int64_t K, void* y, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream) {
+    if (w4a16_status_t st = check_w8a8(fmt, act, M, codes, scales, mins, N, K, y); st != W4A16_OK) return st;
+    const W8A8Workspace w = w8a8_workspace(M, K);
+    if (!aligned16(x) || !aligned16(workspace) || workspace_bytes < w.total) return W4A16_ERR_INVALID;
+    if (!w4a16::w8a8_fits_grid(M, N, 1)) return W4A16_ERR_UNSUPPORTED;
+    int8_t* xq = static_cast<int8_t*>(workspace);
+    float* ascale = reinterpret_cast<float*>(xq + w.ascale);
+    w4a16::clear_stale_error();
+    const w4a16_status_t st = from_hip(w4a16::launch_quant_rows_i8((int)act, x, M, K, xq, ascale, stream));
+    if (st != W4A16_OK) return st;
+    return from_hip(w4a16::launch_gemm_w8a8((int)act, xq, ascale, M, static_cast<const int8_t*>(codes),
+                                            static_cast<const float*>(scales), N, K, y, nullptr, 1, stream));
+}
+
+w4a16_status_t w4a16_gemm_w8a8_experts(w4a16_format_t fmt, w4a16_dtype_t out, const int8_t* xq, const float* ascale,
+                                       int64_t R, const int32_t* offsets, int64_t E, const void* codes, const void* scales,
+                                       const void* mins, int64_t N, int64_t K, void* y, hipStream_t stream) {
+    if (w4a16_status_t st = check_w8a8(fmt, out, R, codes, scales, mins, N, K, y); st != W4A16_OK) return st;
+    if (E <= 0 || E > kMaxDim || !aligned16(xq) || !aligned16(ascale) || !aligned16(offsets)) return W4A16_ERR_INVALID;
+    if (E > w4a16::kMaxExperts || !w4a16::w8a8_fits_grid(R, N, E)) return W4A16_ERR_UNSUPPORTED;
+    w4a16::clear_stale_error();
+    return from_hip(w4a16::launch_gemm_w8a8((int)out, xq, ascale, R, static_cast<const int8_t*>(codes),
+                                            static_cast<const float*>(scales), N, K, y, offsets, E, stream));
+}
+
+int64_t w4a16_max_experts(void) { return w4a16::kMaxExperts; }
+
+size_t w4a16_expert_sort_workspace_bytes(int64_t T, int64_t topk, int64_t E) {
+    if (check_pairs(T, topk, 1) != W4A16_OK || E <= 0 || E > w4a16::kMaxExperts) return 0;
+    return w4a16::expert_sort_workspace_bytes(T * topk, E);
+}
+
+w4a16_status_t w4a16_expert_sort(const void* ids, int64_t id_bits, int64_t T, int64_t topk, int64_t E, int32_t* offsets,
+                                 int32_t* pos, int32_t* src, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    const w4a16_status_t st = check_pairs(T, topk, 1);
+    if (st == W4A16_ERR_INVALID || E <= 0 || E > kMaxDim || (id_bits != 32 && id_bits != 64)) return W4A16_ERR_INVALID;
+    if (!aligned16(ids) || !aligned16(offsets) || !aligned16(pos) || (src != nullptr && !aligned16(src)))
+        return W4A16_ERR_INVALID;
+    if (st != W4A16_OK) return st;
+    if (E > w4a16::kMaxExperts) return W4A16_ERR_UNSUPPORTED;
+    const size_t need = w4a16::expert_sort_workspace_bytes(T * topk, E);
+    if (need > 0 && (workspace_bytes < need || !aligned16(workspace))) return W4A16_ERR_INVALID;
+    w4a16::clear_stale_error();
+    return from_hip(w4a16::launch_expert_sort(ids, (int)id_bits, T * topk, E, offsets, pos, src,
+                                              static_cast<int32_t*>(workspace), stream));
+}
+
+w4a16_status_t w4a16_expert_gather(w4a16_dtype_t act, const void* x, int64_t T, int64_t topk, const int32_t* pos, int64_t K,
+                                   void* xs, hipStream_t stream) {
+    const w4a16_status_t st = check_pairs(T, topk, K);
+    if (st == W4A16_ERR_INVALID || !valid_dtype(act) || !aligned16(x) || !aligned16(pos) || !aligned16(xs))
+        return W4A16_ERR_INVALID;
+    if (st != W4A16_OK) return st;
+    w4a16::clear_stale_error();
+    return from_hip(w4a16::launch_expert_gather((int)act, x, T, topk, pos, K, xs, stream));
+}
+
+w4a16_status_t w4a16_expert_gather_i8(w4a16_dtype_t act, const void* x, int64_t T, int64_t topk, const int32_t* pos,
+                                      int64_t K, int8_t* xq, float* ascale, hipStream_t stream) {
+    const w4a16_status_t st = check_pairs(T, topk, K);
+    if (st == W4A16_ERR_INVALID || !valid_dtype(act) || K % kW8RowAlign != 0) return W4A16_ERR_INVALID;
+    if (!aligned16(x) || !aligned16(pos) || !aligned16(xq) || !aligned16(ascale)) return W4A16_ERR_INVALID;
+    if (st != W4A16_OK) return st;
+    w4a16::clear_stale_error();
+    return from_hip(w4a16::launch_expert_gather_i8((int)act, x, T, topk, pos, K, xq, ascale, stream));
+}
+
+w4a16_status_t w4a16_expert_combine(w4a16_dtype_t act, const void* ys, int64_t T, int64_t topk, const int32_t* pos,
+                                    const float* weights, int64_t N, void* y, hipStream_t stream) {
+    const w4a16_status_t st = check_pairs(T, topk, N);
+    if (st == W4A16_ERR_INVALID || !valid_dtype(act) || !aligned16(ys) || !aligned16(pos) || !aligned16(y))
+        return W4A16_ERR_INVALID;
+    if (weights != nullptr && !aligned16(weights)) return W4A16_ERR_INVALID;
+    if (st != W4A16_OK) return st;
+    w4a16::clear_stale_error();
+    return from_hip(w4a16::launch_expert_combine((int)act, ys, T, topk, pos, weights, N, y, stream));
+}
+
+w4a16_status_t w4a16_expert_combine_backward(w4a16_dtype_t act, const void* dy, const void* ys, int64_t T, int64_t topk,
+                                             const int32_t* pos, const float* weights, int64_t N, void* dys,
+                                             float* dweights, hipStream_t stream) {
+    const w4a16_status_t st = check_pairs(T, topk, N);
+    if (st == W4A16_ERR_INVALID || !valid_dtype(act) || !aligned16(dy) || !aligned16(pos)) return W4A16_ERR_INVALID;
+    if (weights != nullptr && !aligned16(weights)) return W4A16_ERR_INVALID;
+    if (dys == nullptr && dweights == nullptr) return W4A16_ERR_INVALID;
+    if (dys != nullptr && !aligned16(dys)) return W4A16_ERR_INVALID;
+    if (dweights != nullptr && (!aligned16(dweights) || !aligned16(ys))) return W4A16_ERR_INVALID;
+    if (st != W4A16_OK) return st;
+    w4a16::clear_stale_error();
+    return from_hip(w4a16::launch_expert_combine_backward((int)act, dy, ys, T, topk, pos, weights, N, dys, dweights,
+                                                          stream));
 }
 
 }  // extern "C"

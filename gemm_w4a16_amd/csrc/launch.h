@@ -153,4 +153,29 @@ hipError_t launch_gemm_w4a8(const int8_t* xq, const float* ascale, const float* 
 hipError_t launch_matmul_w4a8_fused(const uint16_t* x, int64_t M, const uint32_t* codes, const uint16_t* scales,
                                     const uint16_t* mins, int64_t N, int64_t K, uint16_t* y, hipStream_t stream);
 
+// W8A8: int8 rows (dtype: 0 bf16, 1 fp16, 2 fp32 activations) and their product with W8 weights, in
+// that output type; offsets null for one matrix, else E + 1 first rows of E experts' matrices.
+hipError_t launch_quant_rows_i8(int dtype, const void* x, int64_t M, int64_t K, int8_t* xq, float* ascale,
+                                hipStream_t stream);
+bool w8a8_fits_grid(int64_t M, int64_t N, int64_t E);
+hipError_t launch_gemm_w8a8(int dtype, const int8_t* xq, const float* ascale, int64_t M, const int8_t* codes,
+                            const float* scales, int64_t N, int64_t K, void* y, const int32_t* offsets, int64_t E,
+                            hipStream_t stream);
+
+// Tokens sorted by expert and back (P = T * topk pairs); widths in elements of dtype.
+constexpr int64_t kMaxExperts = 512;    // the sort keeps a count per wave and expert in LDS
+constexpr int64_t kSortOneBlock = 8192;  // pairs that one block sorts in one launch, with no workspace
+size_t expert_sort_workspace_bytes(int64_t P, int64_t E);
+hipError_t launch_expert_sort(const void* ids, int id_bits, int64_t P, int64_t E, int32_t* offsets, int32_t* pos,
+                              int32_t* src, int32_t* ws, hipStream_t stream);
+hipError_t launch_expert_gather(int dtype, const void* x, int64_t T, int64_t topk, const int32_t* pos, int64_t K, void* xs,
+                                hipStream_t stream);
+hipError_t launch_expert_gather_i8(int dtype, const void* x, int64_t T, int64_t topk, const int32_t* pos, int64_t K,
+                                   int8_t* xq, float* ascale, hipStream_t stream);
+hipError_t launch_expert_combine(int dtype, const void* ys, int64_t T, int64_t topk, const int32_t* pos,
+                                 const float* weights, int64_t N, void* y, hipStream_t stream);
+hipError_t launch_expert_combine_backward(int dtype, const void* dy, const void* ys, int64_t T, int64_t topk,
+                                          const int32_t* pos, const float* weights, int64_t N, void* dys, float* dweights,
+                                          hipStream_t stream);
+
 }  // namespace w4a16

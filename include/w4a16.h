@@ -312,6 +312,101 @@ w4a16_status_t w4a16_gemm_w4a8(w4a16_format_t fmt, const int8_t* xq, const float
 w4a16_status_t w4a16_matmul_w4a8(w4a16_format_t fmt, const void* x, int64_t M, const void* codes, const void* scales,
                                  const void* mins, int64_t N, int64_t K, void* y, hipStream_t stream);
 
+/* ---- W8A8: int8 activations against the W8 format's int8 weights ---------------------------------
+ * The same two steps with 8-bit weights: each row of x gets one scale, each output column has its
+ * own (the W8 row scale), and y[m][n] = a_m s_n sum_k xq[m][k] codes[n][k], the integer sum exact
+ * on the int8 matrix cores and the scales applied to it in fp32.  Activations and outputs may be
+ * bf16, fp16 or fp32. */
+
+/* Per-row symmetric int8 quantization of x [M][K] (type `act`, K % 16 == 0):
+ *   ascale [M]       a_m = max_k |x[m][k]| / 127 in fp32 (IEEE division); 1.0 where that is zero
+ *   xq     [M][K]    clamp(rint(x / a_m), -127, 127), ties to even (IEEE division)
+ * A row that holds an infinity or NaN gets the scale NaN and codes 0, so that its products are NaN
+ * and other rows are not touched.  Bit-identical to the definition.  ERR_INVALID: type, sizes,
+ * alignment; ERR_UNSUPPORTED: K above 2^22. */
+w4a16_status_t w4a16_quantize_rows_i8(w4a16_dtype_t act, const void* x, int64_t M, int64_t K, int8_t* xq, float* ascale,
+                                      hipStream_t stream);
+
+/* y [M][N] (type `out`) from int8 rows xq [M][K] and their scales, against W8 weights.  K at most
+ * 2^17 - 16, so that no sum of int8 products passes 32 bits.  W8 only.  No workspace; bitwise
+ * reproducible.  ERR_INVALID: type, sizes, alignment, mins not NULL; ERR_UNSUPPORTED: another
+ * format, K or N past the limits, M and N too large for one launch. */
+w4a16_status_t w4a16_gemm_w8a8(w4a16_format_t fmt, w4a16_dtype_t out, const int8_t* xq, const float* ascale, int64_t M,
+                               const void* codes, const void* scales, const void* mins, int64_t N, int64_t K, void* y,
+                               hipStream_t stream);
+
+/* y [M][N] = x [M][K] . W_hat^T with x quantized on the way: bit for bit w4a16_quantize_rows_i8
+ * followed by w4a16_gemm_w8a8 with out = act.  workspace (w4a16_w8a8_workspace_bytes, 16-byte
+ * aligned) holds the codes and scales of x; it needs no initialisation and must not be shared by
+ * calls, or graphs of calls, that may run at the same time.  Errors as for the two calls, and
+ * ERR_INVALID for a workspace that is NULL or too small. */
+w4a16_status_t w4a16_matmul_w8a8(w4a16_format_t fmt, w4a16_dtype_t act, const void* x, int64_t M, const void* codes,
+                                 const void* scales, const void* mins, int64_t N, int64_t K, void* y, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace w4a16_matmul_w8a8 needs (0 for a bad shape or another format). */
+size_t w4a16_w8a8_workspace_bytes(w4a16_format_t fmt, int64_t M, int64_t N, int64_t K);
+
+/* ---- Experts: tokens sorted by expert, the experts' products, and back -----------------------------
+ * A router gives each of T tokens `topk` expert numbers, ids [T][topk]; pair p = t * topk + j is token
+ * t's j-th choice.  The pairs are sorted by expert, stably (pairs of one expert in order of p); a
+ * pair whose id is outside [0, E) -- a padding token's, say -1 -- goes to no expert and gets no row.
+ * The same expert may appear twice among a token's choices.  Sorted arrays have T * topk rows; the
+ * experts' rows are the first offsets[E] of them, and rows behind those are neither read nor
+ * written by any call.  A serving pass is w4a16_expert_sort, w4a16_expert_gather_i8,
+ * w4a16_gemm_w8a8_experts, w4a16_expert_combine; none of them waits for the host, so the pass can be
+ * captured into a graph.
+ * T, topk and E at least 1; topk and E at most w4a16_max_experts(), T * topk at most 2^30 and rows
+ * at most 2^22 wide (ERR_UNSUPPORTED above).  Outputs may not overlap inputs. */
+
+/* Largest E and topk the experts' calls accept. */
+int64_t w4a16_max_experts(void);
+
+/* Bytes of workspace w4a16_expert_sort needs (0 up to 8192 pairs, and for bad sizes). */
+size_t w4a16_expert_sort_workspace_bytes(int64_t T, int64_t topk, int64_t E);
+
+/* The sorted order.  ids [T][topk]: int32 (id_bits 32) or int64 (id_bits 64).  Writes
+ *   offsets int32 [E + 1]     expert e's rows are offsets[e] .. offsets[e + 1] - 1; offsets[0] = 0
+ *   pos     int32 [T][topk]   a pair's sorted row, -1 for a pair with no expert
+ *   src     int32 [T * topk]  a sorted row's pair, -1 for the rows from offsets[E] on; may be NULL
+ * workspace may be NULL if w4a16_expert_sort_workspace_bytes is 0; it needs no initialisation and
+ * must not be shared by calls that may run at the same time. */
+w4a16_status_t w4a16_expert_sort(const void* ids, int64_t id_bits, int64_t T, int64_t topk, int64_t E, int32_t* offsets,
+                                 int32_t* pos, int32_t* src, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Rows in sorted order: xs[pos[t][j]] = x[t], x [T][K], xs [T * topk][K] of type `act`.  pos as
+ * w4a16_expert_sort wrote it; entries outside [0, T * topk) are skipped.  Its gradient is
+ * w4a16_expert_combine with weights NULL. */
+w4a16_status_t w4a16_expert_gather(w4a16_dtype_t act, const void* x, int64_t T, int64_t topk, const int32_t* pos, int64_t K,
+                                   void* xs, hipStream_t stream);
+
+/* The same with each row quantized on the way as w4a16_quantize_rows_i8 does it: xq int8
+ * [T * topk][K] and ascale [T * topk], K % 16 == 0. */
+w4a16_status_t w4a16_expert_gather_i8(w4a16_dtype_t act, const void* x, int64_t T, int64_t topk, const int32_t* pos,
+                                      int64_t K, int8_t* xq, float* ascale, hipStream_t stream);
+
+/* w4a16_gemm_w8a8 with one weight matrix per expert: codes [E][N][K] and scales [E][N], each expert's
+ * part as w4a16_quantize_pack writes it; y[r] for the rows r of expert e (offsets[e] <= r <
+ * offsets[e + 1]) is multiplied by that expert's weights.  R: rows that xq, ascale and y have.
+ * Experts with no rows cost no work.  offsets are read on the device and clamped to [0, R]. */
+w4a16_status_t w4a16_gemm_w8a8_experts(w4a16_format_t fmt, w4a16_dtype_t out, const int8_t* xq, const float* ascale,
+                                       int64_t R, const int32_t* offsets, int64_t E, const void* codes, const void* scales,
+                                       const void* mins, int64_t N, int64_t K, void* y, hipStream_t stream);
+
+/* Back to the tokens: y[t] = sum_j weights[t][j] ys[pos[t][j]], in order of j in fp32, rounded once to
+ * `act`; ys [T * topk][N], y [T][N]; weights fp32 [T][topk], or NULL for ones.  Pairs with no row add
+ * nothing (their weights are not read into the sum); a token with none gets zeros. */
+w4a16_status_t w4a16_expert_combine(w4a16_dtype_t act, const void* ys, int64_t T, int64_t topk, const int32_t* pos,
+                                    const float* weights, int64_t N, void* y, hipStream_t stream);
+
+/* Gradients of w4a16_expert_combine: dys[pos[t][j]] = weights[t][j] dy[t] (type `act`) and
+ * dweights[t][j] = sum_n dy[t][n] ys[pos[t][j]][n] (fp32, summed in a fixed order; 0 for a pair with no
+ * row).  dys or dweights may be NULL (not wanted), not both; ys is read for dweights only and may
+ * be NULL without it; weights may be NULL for ones. */
+w4a16_status_t w4a16_expert_combine_backward(w4a16_dtype_t act, const void* dy, const void* ys, int64_t T, int64_t topk,
+                                             const int32_t* pos, const float* weights, int64_t N, void* dys,
+                                             float* dweights, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -135,6 +135,19 @@ __device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int R
     hi = min(max(offsets[e + 1], lo), R);
 }
 
+// Row tiles of all experts; every wave counts for itself.
+__device__ __forceinline__ int count_expert_tiles(const int32_t* __restrict__ offsets, int E, int R, int tile) {
+    int n = 0;
+    for (int e = lane_id(); e < E; e += kWave) {
+        int lo, hi;
+        expert_rows(offsets, e, R, lo, hi);
+        n += (hi - lo + tile - 1) / tile;
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) n += __shfl_xor(n, off);
+    return __builtin_amdgcn_readfirstlane(n);
+}
+
 // The expert and first row of row tile `t`, counting tiles expert by expert.  Each wave looks for
 // itself, 64 experts at a time: the lanes' tile counts are summed over the lanes, and the lane whose
 // range of tiles holds t is the expert.  Every lane returns the same.

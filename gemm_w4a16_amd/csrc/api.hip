@@ -564,10 +564,8 @@ w4a16_status_t w4a16_matmul_w8a8(w4a16_format_t fmt, w4a16_dtype_t act, const vo
     int8_t* xq = static_cast<int8_t*>(workspace);
     float* ascale = reinterpret_cast<float*>(xq + w.ascale);
     w4a16::clear_stale_error();
-    const w4a16_status_t st = from_hip(w4a16::launch_quant_rows_i8((int)act, x, M, K, xq, ascale, stream));
-    if (st != W4A16_OK) return st;
-    return from_hip(w4a16::launch_gemm_w8a8((int)act, xq, ascale, M, static_cast<const int8_t*>(codes),
-                                            static_cast<const float*>(scales), N, K, y, nullptr, 1, stream));
+    return from_hip(w4a16::launch_matmul_w8a8((int)act, x, M, static_cast<const int8_t*>(codes),
+                                              static_cast<const float*>(scales), N, K, y, xq, ascale, stream));
 }
 
 w4a16_status_t w4a16_gemm_w8a8_experts(w4a16_format_t fmt, w4a16_dtype_t out, const int8_t* xq, const float* ascale,

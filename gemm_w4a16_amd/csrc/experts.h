@@ -53,6 +53,24 @@ struct alignas(V * sizeof(T)) Pack {
     T v[V];
 };
 
+// A unit read or written once: with kStream past the caches' usual order (non-temporal), which large arrays
+// gain by and arrays that the caches hold lose by.
+typedef uint32_t unit16_t __attribute__((ext_vector_type(4)));
+template <bool kStream, typename U>
+__device__ __forceinline__ U load_unit(const U* p) {
+    if constexpr (kStream && sizeof(U) == 16)
+        return __builtin_bit_cast(U, __builtin_nontemporal_load(reinterpret_cast<const unit16_t*>(p)));
+    else
+        return *p;
+}
+template <bool kStream, typename U>
+__device__ __forceinline__ void store_unit(U* p, const U& u) {
+    if constexpr (kStream && sizeof(U) == 16)
+        __builtin_nontemporal_store(__builtin_bit_cast(unit16_t, u), reinterpret_cast<unit16_t*>(p));
+    else
+        *p = u;
+}
+
 // ---- int8 quantization of a row -------------------------------------------------------------------
 
 // Bits of |v| as an unsigned integer of the type's own width: these order like the magnitudes, with
@@ -78,34 +96,58 @@ __device__ __forceinline__ uint32_t code_i8(float v, float a) {
     return (uint32_t)(int)fminf(fmaxf(r, -127.0f), 127.0f) & 0xFFu;
 }
 
-// 16 consecutive activations (16-byte aligned) to 16 codes.
+// 16 consecutive activations (16-byte aligned), their largest magnitude's bits, and their codes.
 template <typename T>
-__device__ __forceinline__ uint4 quant16(const T* p, float a) {
-    constexpr int V = 16 / sizeof(T);
+struct alignas(16) Act16 {
+    T v[16];
+};
+template <typename T>
+__device__ __forceinline__ uint32_t max_bits(const Act16<T>& x, uint32_t m) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) m = max(m, abs_bits(x.v[j]));
+    return m;
+}
+// The codes by a product with r = 1 / a where that cannot differ: r and the product are each off by at most
+// 2^-24 of their value, so for |v / a| <= 127 the product is within 127.5 * 2^-23 < 1.6e-5 of v / a, and the
+// division's own rounding within 0.8e-5; with the product at least 1e-4 from a midpoint both round to the
+// same code.  Else (and for scales whose reciprocal is not a normal number) the 16 are divided.
+template <typename T>
+__device__ __forceinline__ uint4 codes16(const Act16<T>& x, float a, float r) {
     uint32_t w[4] = {};
+    float far = a >= 0x1p-100f ? 0.0f : 1.0f;  // largest distance from a code (NaN scales come here too)
 #pragma unroll
-    for (int i = 0; i < 16 / V; ++i) {
-        const Pack<T, V> c = reinterpret_cast<const Pack<T, V>*>(p)[i];
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int at = V * i + j;
-            w[at / 4] |= code_i8(to_f32(c.v[j]), a) << (8 * (at % 4));
-        }
+    for (int j = 0; j < 16; ++j) {
+        const float t = to_f32(x.v[j]) * r, q = rintf(t);
+        far = fmaxf(far, fabsf(t - q));
+        w[j / 4] |= ((uint32_t)(int)fminf(fmaxf(q, -127.0f), 127.0f) & 0xFFu) << (8 * (j % 4));
     }
-    if (a != a) return make_uint4(0, 0, 0, 0);
+    if (far > 0.4999f) {
+        w[0] = w[1] = w[2] = w[3] = 0;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) w[j / 4] |= code_i8(to_f32(x.v[j]), a) << (8 * (j % 4));
+        if (a != a) return make_uint4(0, 0, 0, 0);
+    }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The scale of row[0 .. K) (K % 16 == 0), by a block of kThreads; red: one word per wave.
-template <int kThreads, typename T>
-__device__ __forceinline__ float row_scale_i8(const T* row, int K, uint32_t* red) {
-    constexpr int V = 16 / sizeof(T);
+// row[0 .. K) (K % 16 == 0) quantized by a block of kThreads: store(c, codes) for each 16 codes c; the row's
+// scale is returned.  A thread's first activations stay in registers between the two passes.  red: one word
+// per wave of LDS.
+template <int kThreads, typename T, typename F>
+__device__ __forceinline__ float quantize_row(const T* row, int K, uint32_t* red, F store) {
+    constexpr int kKeep = 2;
+    const Act16<T>* in = reinterpret_cast<const Act16<T>*>(row);
+    Act16<T> keep[kKeep];
     uint32_t m = 0;
-    for (int c = threadIdx.x; c < K / V; c += kThreads) {
-        const Pack<T, V> v = reinterpret_cast<const Pack<T, V>*>(row)[c];
 #pragma unroll
-        for (int j = 0; j < V; ++j) m = max(m, abs_bits(v.v[j]));
+    for (int i = 0; i < kKeep; ++i) {
+        const int c = threadIdx.x + kThreads * i;
+        if (c < K / 16) {
+            keep[i] = in[c];
+            m = max_bits(keep[i], m);
+        }
     }
+    for (int c = threadIdx.x + kThreads * kKeep; c < K / 16; c += kThreads) m = max_bits(in[c], m);
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off));
     __syncthreads();  // red may still be read from the row before
@@ -113,7 +155,14 @@ __device__ __forceinline__ float row_scale_i8(const T* row, int K, uint32_t* red
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kThreads / kWave; ++w) m = max(m, red[w]);
-    return scale_i8(from_abs_bits(m, T{}));
+    const float a = scale_i8(from_abs_bits(m, T{})), r = 1.0f / a;
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) {
+        const int c = threadIdx.x + kThreads * i;
+        if (c < K / 16) store(c, codes16(keep[i], a, r));
+    }
+    for (int c = threadIdx.x + kThreads * kKeep; c < K / 16; c += kThreads) store(c, codes16(in[c], a, r));
+    return a;
 }
 
 // ---- row tiles of experts ----------------------------------------------------------------------

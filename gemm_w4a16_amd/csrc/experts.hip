@@ -56,74 +56,109 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const TI* __re
     for (int e = threadIdx.x; e <= E; e += kSortThreads) ws[(size_t)blockIdx.x * (E + 1) + e] = lds[e];
 }
 
-// Ranks and output.  ws: the blocks' counts (null where there is one block).
-template <typename TI>
+// Ranks and output.  kBlocks: the run is one of several, whose counts are in ws.  kPer > 0: the run is at most kPer
+// pairs a thread, whose keys and ranks stay in registers; else a wave walks its pairs twice.
+template <typename TI, bool kBlocks, int kPer>
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const TI* __restrict__ ids, int64_t P, int E, int64_t run,
                                                                   const int32_t* __restrict__ ws, int bits,
                                                                   int32_t* __restrict__ offsets, int32_t* __restrict__ pos,
                                                                   int32_t* __restrict__ src) {
-    extern __shared__ int32_t lds[];  // [kSortWaves][E + 1] counts, then next rows; [kSortWaves] sums
-    int32_t* cnt = lds;
-    int32_t* sums = lds + kSortWaves * (E + 1);
+    extern __shared__ int32_t lds[];
+    const int keys = E + 1;
+    int32_t* cnt = lds;                        // [kSortWaves][keys] counts, then the next rows
+    int32_t* sums = lds + kSortWaves * keys;   // [kSortWaves]
+    int32_t* all = sums + kSortWaves;          // [2][keys] pairs in all blocks, and in the blocks before (kBlocks)
     const int t = threadIdx.x, lane = lane_id(), wave = wave_id();
-    for (int i = t; i < kSortWaves * (E + 1); i += kSortThreads) cnt[i] = 0;
-    __syncthreads();
     const int64_t p0 = blockIdx.x * run;
     const int64_t wrun = run / kSortWaves;  // a multiple of 64
     const int64_t w0 = p0 + wave * wrun, w1 = min(w0 + wrun, P);
-    for (int64_t p = w0 + lane; p < w1; p += kWave) atomicAdd(&cnt[wave * (E + 1) + sort_key(ids, p, P, E)], 1);
-    __syncthreads();
-    // first rows of every (wave, key): keys 0..E, one per thread
-    static_assert(kMaxExperts < kSortThreads, "a thread per key");
-    {
-        const int e = t;
-        int total = 0, before = 0;
-        if (e <= E) {
-            if (ws != nullptr) {
-                for (int b = 0; b < (int)gridDim.x; ++b) {
-                    const int c = ws[(size_t)b * (E + 1) + e];
-                    total += c;
-                    if (b < (int)blockIdx.x) before += c;
-                }
-            }
-            int s = 0;
-            for (int w = 0; w < kSortWaves; ++w) {
-                const int c = cnt[w * (E + 1) + e];
-                cnt[w * (E + 1) + e] = before + s;
-                s += c;
-            }
-            if (ws == nullptr) total = s;
-        }
-        int end = total;  // inclusive sum over the block's keys
+    int32_t* mine = cnt + wave * keys;
+
+    for (int i = t; i < (kSortWaves + (kBlocks ? 2 : 0)) * keys + kSortWaves; i += kSortThreads) cnt[i] = 0;
+    int key[kPer > 0 ? kPer : 1], rank[kPer > 0 ? kPer : 1];
+    if constexpr (kPer > 0) {
 #pragma unroll
-        for (int off = 1; off < kWave; off <<= 1) {
-            const int v = __shfl_up(end, off);
-            if (lane >= off) end += v;
+        for (int i = 0; i < kPer; ++i) key[i] = sort_key(ids, w0 + kWave * i + lane, w1, E);
+    }
+    __syncthreads();
+
+    // a chunk of 64 pairs: a pair's rank among its key in this wave so far, counting it
+    auto rank_chunk = [&](int64_t p, int key) __attribute__((always_inline)) {
+        const uint64_t same = same_key(key, bits);
+        const int below = __popcll(same & ((1ull << lane) - 1));
+        int rank = 0;
+        if (p < w1) {
+            rank = mine[key] + below;
+            wave_lds_sync();
+            if (below == 0) mine[key] = rank + __popcll(same);
         }
-        if (lane == kWave - 1) sums[wave] = end;
-        __syncthreads();
-        int base = 0;
-        for (int w = 0; w < wave; ++w) base += sums[w];
-        if (e <= E) {
-            const int first = base + end - total;
-            for (int w = 0; w < kSortWaves; ++w) cnt[w * (E + 1) + e] += first;
-            if (blockIdx.x == 0) offsets[e] = first;  // key E's first row is offsets[E]
+        wave_lds_sync();
+        return rank;
+    };
+    if constexpr (kPer > 0) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (w0 + kWave * i < w1) rank[i] = rank_chunk(w0 + kWave * i + lane, key[i]);
+    } else {
+        for (int64_t p = w0 + lane; p < w1; p += kWave) atomicAdd(&mine[sort_key(ids, p, P, E)], 1);
+    }
+    if constexpr (kBlocks) {  // the blocks' counts, over all threads
+        const int rows = kSortThreads / keys, r = t / keys, e = t % keys;  // keys <= kMaxExperts + 1 < kSortThreads
+        if (r < rows) {
+            int total = 0, before = 0;
+            for (int b = r; b < (int)gridDim.x; b += rows) {
+                const int c = ws[(size_t)b * keys + e];
+                total += c;
+                if (b < (int)blockIdx.x) before += c;
+            }
+            atomicAdd(&all[e], total);
+            atomicAdd(&all[keys + e], before);
         }
     }
     __syncthreads();
-    for (int64_t p = w0 + lane; p - lane < w1; p += kWave) {
-        const int key = p < w1 ? sort_key(ids, p, P, E) : E + 1;
-        const uint64_t same = same_key(key, bits);
-        if (p < w1) {
-            const int rank = __popcll(same & ((1ull << lane) - 1));
-            int32_t* next = &cnt[wave * (E + 1) + key];
-            const int row = *next + rank;
-            wave_lds_sync();
-            if (rank == 0) *next = row + __popcll(same);
-            pos[p] = key < E ? row : -1;
-            if (src != nullptr) src[row] = key < E ? (int32_t)p : -1;
+    // first rows of every (wave, key): one key per thread
+    static_assert(kMaxExperts < kSortThreads, "a thread per key");
+    int total = 0;
+    if (t < keys) {
+        int s = kBlocks ? all[keys + t] : 0;
+        for (int w = 0; w < kSortWaves; ++w) {
+            const int c = cnt[w * keys + t];
+            cnt[w * keys + t] = s;
+            s += c;
         }
-        wave_lds_sync();
+        total = kBlocks ? all[t] : s;
+    }
+    int end = total;  // inclusive sum over the keys
+#pragma unroll
+    for (int off = 1; off < kWave; off <<= 1) {
+        const int v = __shfl_up(end, off);
+        if (lane >= off) end += v;
+    }
+    if (lane == kWave - 1) sums[wave] = end;
+    __syncthreads();
+    if (t < keys) {
+        int first = end - total;
+        for (int w = 0; w < wave; ++w) first += sums[w];
+        for (int w = 0; w < kSortWaves; ++w) cnt[w * keys + t] += first;
+        if (blockIdx.x == 0) offsets[t] = first;  // key E's first row is offsets[E]
+    }
+    __syncthreads();
+    auto place = [&](int64_t p, int key, int row) __attribute__((always_inline)) {
+        pos[p] = key < E ? row : -1;
+        if (src != nullptr) src[row] = key < E ? (int32_t)p : -1;
+    };
+    if constexpr (kPer > 0) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int64_t p = w0 + kWave * i + lane;
+            if (p < w1) place(p, key[i], mine[key[i]] + rank[i]);
+        }
+    } else {
+        for (int64_t p = w0 + lane; p - lane < w1; p += kWave) {
+            const int key = p < w1 ? sort_key(ids, p, P, E) : keys;
+            const int row = rank_chunk(p, key);  // (mine holds the next rows now)
+            if (p < w1) place(p, key, row);
+        }
     }
 }
 
@@ -135,20 +170,37 @@ __device__ __forceinline__ int64_t pair_row(const int32_t* pos, int64_t p, int64
     return r >= 0 && r < P ? r : -1;
 }
 
-// One unit U (16 bytes, or one element) of a row per thread, stored once for each of the token's pairs.
-template <typename U>
-__global__ __launch_bounds__(256) void gather_kernel(const U* __restrict__ x, int64_t T, int topk,
-                                                     const int32_t* __restrict__ pos, int units, int blocks_per_row,
+// The token and unit of a row (16 bytes, or one element) that a thread moves: a block takes 256 units of a row,
+// or (kShort) `tokens` whole rows where a row has at most 64.
+struct RowShape {
+    int units, tokens, blocks_per_row;
+};
+template <bool kShort>
+__device__ __forceinline__ bool row_place(const RowShape& s, int64_t b, int64_t Tn, int64_t& t, int& c) {
+    if constexpr (kShort) {
+        const int i = threadIdx.x / s.units;
+        t = b * s.tokens + i, c = threadIdx.x - i * s.units;
+        return i < s.tokens && t < Tn;
+    } else {
+        t = b / s.blocks_per_row, c = (int)(b - t * s.blocks_per_row) * 256 + threadIdx.x;
+        return c < s.units;
+    }
+}
+
+// A unit is read once and stored for each of the token's pairs.
+template <typename U, bool kStream, bool kShort>
+__global__ __launch_bounds__(256) void gather_kernel(const U* __restrict__ x, int64_t Tn, int topk,
+                                                     const int32_t* __restrict__ pos, RowShape s, int64_t blocks,
                                                      U* __restrict__ xs) {
-    const int64_t P = T * topk;
-    for (int64_t b = blockIdx.x; b < T * blocks_per_row; b += gridDim.x) {
-        const int64_t t = b / blocks_per_row;
-        const int c = (int)(b % blocks_per_row) * 256 + threadIdx.x;
-        if (c >= units) continue;
-        const U v = x[t * units + c];
+    const int64_t P = Tn * topk;
+    for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
+        int64_t t;
+        int c;
+        if (!row_place<kShort>(s, b, Tn, t, c)) continue;
+        const U v = x[t * s.units + c];
         for (int j = 0; j < topk; ++j) {
             const int64_t r = pair_row(pos, t * topk + j, P);
-            if (r >= 0) xs[r * units + c] = v;
+            if (r >= 0) store_unit<kStream>(&xs[r * s.units + c], v);
         }
     }
 }
@@ -160,85 +212,126 @@ __global__ __launch_bounds__(256) void gather_i8_kernel(const T* __restrict__ x,
     __shared__ uint32_t red[4];
     const int64_t P = Tn * topk;
     for (int64_t t = blockIdx.x; t < Tn; t += gridDim.x) {
-        const T* row = x + t * K;
-        const float a = row_scale_i8<256>(row, K, red);
-        for (int j = threadIdx.x; j < topk; j += 256) {
-            const int64_t r = pair_row(pos, t * topk + j, P);
-            if (r >= 0) ascale[r] = a;
-        }
-        for (int c = threadIdx.x; c < K / 16; c += 256) {
-            const uint4 q = quant16(row + 16 * c, a);
+        const float a = quantize_row<256>(x + t * K, K, red, [&](int c, uint4 q) __attribute__((always_inline)) {
             for (int j = 0; j < topk; ++j) {
                 const int64_t r = pair_row(pos, t * topk + j, P);
                 if (r >= 0) *reinterpret_cast<uint4*>(xq + r * K + 16 * c) = q;
             }
+        });
+        for (int j = threadIdx.x; j < topk; j += 256) {
+            const int64_t r = pair_row(pos, t * topk + j, P);
+            if (r >= 0) ascale[r] = a;
         }
     }
 }
 
-template <typename T, int V>
+// The rows of kAhead pairs from j0 on, one unit of each: all requested before the first is used (a pair with no
+// row reads row 0 and is left out by `live`).
+template <bool kStream, int kAhead, typename U>
+__device__ __forceinline__ void load_pairs(const U* ys, const int32_t* pos, int64_t t, int topk, int j0, int64_t P, int units,
+                                           int c, U (&v)[kAhead], int64_t (&row)[kAhead]) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+        row[i] = j0 + i < topk ? pair_row(pos, t * topk + j0 + i, P) : -1;
+        v[i] = load_unit<kStream>(&ys[max(row[i], (int64_t)0) * units + c]);
+    }
+}
+
+template <typename T, int V, int kAhead, bool kStream, bool kShort>
 __global__ __launch_bounds__(256) void combine_kernel(const T* __restrict__ ys, int64_t Tn, int topk,
                                                       const int32_t* __restrict__ pos, const float* __restrict__ weights,
-                                                      int units, int blocks_per_row, T* __restrict__ y) {
+                                                      RowShape s, int64_t blocks, T* __restrict__ y) {
     using U = Pack<T, V>;
     const int64_t P = Tn * topk;
-    for (int64_t b = blockIdx.x; b < Tn * blocks_per_row; b += gridDim.x) {
-        const int64_t t = b / blocks_per_row;
-        const int c = (int)(b % blocks_per_row) * 256 + threadIdx.x;
-        if (c >= units) continue;
+    for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
+        int64_t t;
+        int c;
+        if (!row_place<kShort>(s, b, Tn, t, c)) continue;
         float acc[V] = {};
-        for (int j = 0; j < topk; ++j) {
-            const int64_t r = pair_row(pos, t * topk + j, P);
-            if (r < 0) continue;
-            const float w = weights != nullptr ? weights[t * topk + j] : 1.0f;
-            const U v = reinterpret_cast<const U*>(ys)[r * units + c];
+        for (int j0 = 0; j0 < topk; j0 += kAhead) {
+            U v[kAhead];
+            int64_t row[kAhead];
+            load_pairs<kStream>(reinterpret_cast<const U*>(ys), pos, t, topk, j0, P, s.units, c, v, row);
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(w, to_f32(v.v[i]), acc[i]);
+            for (int i = 0; i < kAhead; ++i)
+                if (row[i] >= 0) {
+                    const float w = weights != nullptr ? weights[t * topk + j0 + i] : 1.0f;
+#pragma unroll
+                    for (int k = 0; k < V; ++k) acc[k] = __builtin_fmaf(w, to_f32(v[i].v[k]), acc[k]);
+                }
         }
         U o;
 #pragma unroll
         for (int i = 0; i < V; ++i) o.v[i] = from_f32<T>(acc[i]);
-        reinterpret_cast<U*>(y)[t * units + c] = o;
+        store_unit<kStream>(reinterpret_cast<U*>(y) + t * s.units + c, o);
     }
 }
 
-// One block per token; a thread's partial dot products are summed over the block in a fixed order.
-template <typename T, int V>
+// Pairs that the backward takes at a time: two (one, four and eight took 66, 50 and 50 us against 51 at 4096 tokens of
+// 8 rows of 2048 bf16, 31, 32 and 38 against 29 at 4096 of 2 rows of 4096, and 5.5, 5.2 and 6.0 against 4.2 at 333
+// of 3 rows of 1000: more rows in flight cost registers, and so waves).
+constexpr int kBackwardAhead = 2;
+
+// kWaves waves per token (one, four tokens a block, for short rows); kAhead pairs at a time.  A thread's partial
+// dot products are summed over the wave, then over the waves, in a fixed order.
+template <typename T, int V, int kAhead, int kWaves, bool kStream>
 __global__ __launch_bounds__(256) void combine_backward_kernel(const T* __restrict__ dy, const T* __restrict__ ys, int64_t Tn,
                                                                int topk, const int32_t* __restrict__ pos,
                                                                const float* __restrict__ weights, int units,
                                                                T* __restrict__ dys, float* __restrict__ dweights) {
     using U = Pack<T, V>;
-    __shared__ float red[4];
+    constexpr int kTokens = 4 / kWaves, kThreads = kWave * kWaves;
+    __shared__ float red[4][kAhead];
     const int64_t P = Tn * topk;
-    for (int64_t t = blockIdx.x; t < Tn; t += gridDim.x) {
-        for (int j = 0; j < topk; ++j) {
-            const int64_t r = pair_row(pos, t * topk + j, P);
-            const float w = weights != nullptr ? weights[t * topk + j] : 1.0f;
-            float dot = 0.0f;
-            if (r >= 0) {
-                for (int c = threadIdx.x; c < units; c += 256) {
-                    const U g = reinterpret_cast<const U*>(dy)[t * units + c];
-                    if (dweights != nullptr) {
-                        const U v = reinterpret_cast<const U*>(ys)[r * units + c];
+    const int lane = threadIdx.x % kThreads;
+    for (int64_t b = blockIdx.x; b * kTokens < Tn; b += gridDim.x) {
+        const int64_t t = kWaves > 1 ? b : b * kTokens + wave_id();
+        if (kWaves == 1 && t >= Tn) continue;
+        for (int j0 = 0; j0 < topk; j0 += kAhead) {
+            float dot[kAhead] = {};
+            for (int c = lane; c < units; c += kThreads) {
+                const U g = reinterpret_cast<const U*>(dy)[t * units + c];
+                U v[kAhead];
+                int64_t row[kAhead];
+                if (dweights != nullptr) {
+                    load_pairs<kStream>(reinterpret_cast<const U*>(ys), pos, t, topk, j0, P, units, c, v, row);
+                } else {
 #pragma unroll
-                        for (int i = 0; i < V; ++i) dot = __builtin_fmaf(to_f32(g.v[i]), to_f32(v.v[i]), dot);
+                    for (int i = 0; i < kAhead; ++i) row[i] = j0 + i < topk ? pair_row(pos, t * topk + j0 + i, P) : -1;
+                }
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    if (row[i] < 0) continue;
+                    if (dweights != nullptr) {
+#pragma unroll
+                        for (int k = 0; k < V; ++k) dot[i] = __builtin_fmaf(to_f32(g.v[k]), to_f32(v[i].v[k]), dot[i]);
                     }
                     if (dys != nullptr) {
+                        const float w = weights != nullptr ? weights[t * topk + j0 + i] : 1.0f;
                         U o;
 #pragma unroll
-                        for (int i = 0; i < V; ++i) o.v[i] = from_f32<T>(w * to_f32(g.v[i]));
-                        reinterpret_cast<U*>(dys)[r * units + c] = o;
+                        for (int k = 0; k < V; ++k) o.v[k] = from_f32<T>(w * to_f32(g.v[k]));
+                        store_unit<kStream>(reinterpret_cast<U*>(dys) + row[i] * units + c, o);
                     }
                 }
             }
-            if (dweights != nullptr) {
-                dot = wave_sum(dot);
-                __syncthreads();
-                if (lane_id() == 0) red[wave_id()] = dot;
-                __syncthreads();
-                if (threadIdx.x == 0) dweights[t * topk + j] = (red[0] + red[1]) + (red[2] + red[3]);
+            if (dweights == nullptr) continue;
+            if constexpr (kWaves > 1) __syncthreads();  // red may still be read
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const float sum = wave_sum(dot[i]);
+                if (lane_id() == 0) red[wave_id()][i] = sum;
             }
+            if constexpr (kWaves > 1)
+                __syncthreads();
+            else
+                wave_lds_sync();
+            if (lane < kAhead && j0 + lane < topk) {
+                float sum = red[wave_id()][lane];
+                if constexpr (kWaves > 1) sum = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+                dweights[t * topk + j0 + lane] = sum;
+            }
+            if constexpr (kWaves == 1) wave_lds_sync();
         }
     }
 }
@@ -267,16 +360,23 @@ static hipError_t launch_sort(const TI* ids, int64_t P, int E, int32_t* offsets,
     const dim3 grid((unsigned)ceil_div(P, run));
     int bits = 1;  // keys 0..E + 1
     while ((E + 1) >> bits) ++bits;
-    const size_t lds = (size_t)(kSortWaves * (E + 1) + kSortWaves) * 4;
-    if (P > kSortOneBlock) {
-        hipLaunchKernelGGL((sort_count_kernel<TI>), grid, dim3(kSortThreads), (E + 1) * 4, stream, ids, P, E, run, ws);
-        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    } else {
-        ws = nullptr;
-    }
-    hipLaunchKernelGGL((sort_place_kernel<TI>), grid, dim3(kSortThreads), lds, stream, ids, P, E, run, ws, bits, offsets, pos,
-                       src);
-    return hipGetLastError();
+    auto place = [&](auto blocks, auto per) {
+        constexpr bool kBlocks = decltype(blocks)::value;
+        constexpr int kPer = decltype(per)::value;
+        const size_t lds = (size_t)((kSortWaves + (kBlocks ? 2 : 0)) * (E + 1) + kSortWaves) * 4;
+        hipLaunchKernelGGL((sort_place_kernel<TI, kBlocks, kPer>), grid, dim3(kSortThreads), lds, stream, ids, P, E, run, ws,
+                           bits, offsets, pos, src);
+        return hipGetLastError();
+    };
+    using std::false_type;
+    using std::integral_constant;
+    using std::true_type;
+    constexpr int kPerBlock = kSortOneBlock / kSortThreads;
+    if (P <= kSortThreads) return place(false_type{}, integral_constant<int, 1>{});
+    if (P <= kSortOneBlock) return place(false_type{}, integral_constant<int, kPerBlock>{});
+    hipLaunchKernelGGL((sort_count_kernel<TI>), grid, dim3(kSortThreads), (E + 1) * 4, stream, ids, P, E, run, ws);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    return run == kSortThreads ? place(true_type{}, integral_constant<int, 1>{}) : place(true_type{}, integral_constant<int, 0>{});
 }
 
 hipError_t launch_expert_sort(const void* ids, int id_bits, int64_t P, int64_t E, int32_t* offsets, int32_t* pos,
@@ -285,18 +385,33 @@ hipError_t launch_expert_sort(const void* ids, int id_bits, int64_t P, int64_t E
     return launch_sort(static_cast<const int32_t*>(ids), P, (int)E, offsets, pos, src, ws, stream);
 }
 
+// Arrays of sorted rows from this size on are streamed (more than the L2s hold, 8 x 4 MiB): 4096 tokens of 2 rows of
+// 8 KiB are gathered in 16.1 us against 20.5, 333 of 3 rows of 2 KB in 2.8 against 2.5.
+static bool streams(int64_t rows, int64_t row_bytes) { return rows * row_bytes >= ((int64_t)32 << 20); }
+
+static RowShape row_shape(int64_t units) {
+    return RowShape{(int)units, units <= 64 ? (int)(256 / units) : 1, (int)ceil_div(units, 256)};
+}
+static int64_t row_blocks(const RowShape& s, int64_t T) { return s.tokens > 1 ? ceil_div(T, s.tokens) : T * s.blocks_per_row; }
+
 hipError_t launch_expert_gather(int dtype, const void* x, int64_t T, int64_t topk, const int32_t* pos, int64_t K, void* xs,
                                 hipStream_t stream) {
     return with_act_type(dtype, [&](auto t) {
         using E = decltype(t);
-        auto run = [&](auto unit) {
+        auto run = [&](auto unit, auto stream_rows) {
             using U = decltype(unit);
-            const int units = (int)(K * sizeof(E) / sizeof(U)), bpr = (int)ceil_div(units, 256);
-            hipLaunchKernelGGL((gather_kernel<U>), row_grid(T * bpr), dim3(256), 0, stream, static_cast<const U*>(x), T,
-                               (int)topk, pos, units, bpr, static_cast<U*>(xs));
-            return hipGetLastError();
+            const RowShape s = row_shape(K * sizeof(E) / sizeof(U));
+            const int64_t blocks = row_blocks(s, T);
+            auto launch = [&](auto is_short) {
+                hipLaunchKernelGGL((gather_kernel<U, decltype(stream_rows)::value, decltype(is_short)::value>),
+                                   row_grid(blocks), dim3(256), 0, stream, static_cast<const U*>(x), T, (int)topk, pos, s,
+                                   blocks, static_cast<U*>(xs));
+                return hipGetLastError();
+            };
+            return s.tokens > 1 ? launch(std::true_type{}) : launch(std::false_type{});
         };
-        return K * sizeof(E) % 16 == 0 ? run(uint4{}) : run(E{});
+        if (K * sizeof(E) % 16 != 0) return run(E{}, std::false_type{});
+        return streams(T * topk, K * sizeof(E)) ? run(uint4{}, std::true_type{}) : run(uint4{}, std::false_type{});
     });
 }
 
@@ -310,37 +425,57 @@ hipError_t launch_expert_gather_i8(int dtype, const void* x, int64_t T, int64_t 
     });
 }
 
+// f(an element, the elements of a unit, whether rows are streamed) as constants.
 template <typename F>
-static hipError_t with_row_unit(int dtype, int64_t N, F f) {
+static hipError_t with_row_unit(int dtype, int64_t T, int64_t topk, int64_t N, F f) {
+    using std::integral_constant;
     return with_act_type(dtype, [&](auto t) {
         using E = decltype(t);
         constexpr int V = 16 / sizeof(E);
-        return N % V == 0 ? f(t, std::integral_constant<int, V>{}) : f(t, std::integral_constant<int, 1>{});
+        if (N % V != 0) return f(t, integral_constant<int, 1>{}, std::false_type{});
+        if (streams(T * topk, N * sizeof(E))) return f(t, integral_constant<int, V>{}, std::true_type{});
+        return f(t, integral_constant<int, V>{}, std::false_type{});
     });
 }
 
 hipError_t launch_expert_combine(int dtype, const void* ys, int64_t T, int64_t topk, const int32_t* pos,
                                  const float* weights, int64_t N, void* y, hipStream_t stream) {
-    return with_row_unit(dtype, N, [&](auto t, auto v) {
+    return with_row_unit(dtype, T, topk, N, [&](auto t, auto v, auto stream_rows) {
         using E = decltype(t);
         constexpr int V = decltype(v)::value;
-        const int units = (int)(N / V), bpr = (int)ceil_div(units, 256);
-        hipLaunchKernelGGL((combine_kernel<E, V>), row_grid(T * bpr), dim3(256), 0, stream, static_cast<const E*>(ys), T,
-                           (int)topk, pos, weights, units, bpr, static_cast<E*>(y));
-        return hipGetLastError();
+        const RowShape s = row_shape(N / V);
+        const int64_t blocks = row_blocks(s, T);
+        auto launch = [&](auto ahead, auto is_short) {
+            hipLaunchKernelGGL((combine_kernel<E, V, decltype(ahead)::value, decltype(stream_rows)::value,
+                                               decltype(is_short)::value>),
+                               row_grid(blocks), dim3(256), 0, stream, static_cast<const E*>(ys), T, (int)topk, pos, weights, s,
+                               blocks, static_cast<E*>(y));
+            return hipGetLastError();
+        };
+        using std::integral_constant;  // (eight pairs at a time take as long as four)
+        auto pairs = [&](auto is_short) {
+            return topk <= 2 ? launch(integral_constant<int, 2>{}, is_short) : launch(integral_constant<int, 4>{}, is_short);
+        };
+        return s.tokens > 1 ? pairs(std::true_type{}) : pairs(std::false_type{});
     });
 }
 
 hipError_t launch_expert_combine_backward(int dtype, const void* dy, const void* ys, int64_t T, int64_t topk,
                                           const int32_t* pos, const float* weights, int64_t N, void* dys, float* dweights,
                                           hipStream_t stream) {
-    return with_row_unit(dtype, N, [&](auto t, auto v) {
+    return with_row_unit(dtype, T, topk, N, [&](auto t, auto v, auto stream_rows) {
         using E = decltype(t);
         constexpr int V = decltype(v)::value;
-        hipLaunchKernelGGL((combine_backward_kernel<E, V>), row_grid(T), dim3(256), 0, stream, static_cast<const E*>(dy),
-                           static_cast<const E*>(ys), T, (int)topk, pos, weights, (int)(N / V), static_cast<E*>(dys),
-                           dweights);
-        return hipGetLastError();
+        constexpr bool kStream = decltype(stream_rows)::value;
+        const int64_t units = N / V;
+        auto run = [&](auto waves) {
+            constexpr int kWaves = decltype(waves)::value;
+            hipLaunchKernelGGL((combine_backward_kernel<E, V, kBackwardAhead, kWaves, kStream>), row_grid(ceil_div(T, 4 / kWaves)),
+                               dim3(256), 0, stream, static_cast<const E*>(dy), static_cast<const E*>(ys), T, (int)topk, pos,
+                               weights, (int)units, static_cast<E*>(dys), dweights);
+            return hipGetLastError();
+        };
+        return units <= 64 ? run(std::integral_constant<int, 1>{}) : run(std::integral_constant<int, 4>{});
     });
 }
 

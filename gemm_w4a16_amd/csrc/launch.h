@@ -161,6 +161,9 @@ bool w8a8_fits_grid(int64_t M, int64_t N, int64_t E);
 hipError_t launch_gemm_w8a8(int dtype, const int8_t* xq, const float* ascale, int64_t M, const int8_t* codes,
                             const float* scales, int64_t N, int64_t K, void* y, const int32_t* offsets, int64_t E,
                             hipStream_t stream);
+// The product of activations x quantized on the way (xq and ascale hold them where a launch of its own does).
+hipError_t launch_matmul_w8a8(int dtype, const void* x, int64_t M, const int8_t* codes, const float* scales, int64_t N,
+                              int64_t K, void* y, int8_t* xq, float* ascale, hipStream_t stream);
 
 // Tokens sorted by expert and back (P = T * topk pairs); widths in elements of dtype.
 constexpr int64_t kMaxExperts = 512;    // the sort keeps a count per wave and expert in LDS

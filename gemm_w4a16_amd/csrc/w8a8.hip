@@ -10,6 +10,7 @@
 // With experts the rows are sorted by expert (offsets[e] is the first row of expert e) and row r of
 // expert e is multiplied by that expert's weights.
 #include <cmath>
+#include <cstddef>
 #include <type_traits>
 
 #include "device_common.h"
@@ -30,10 +31,10 @@ __global__ __launch_bounds__(256) void quant_rows_i8_kernel(const T* __restrict_
                                                             int8_t* __restrict__ xq, float* __restrict__ ascale) {
     __shared__ uint32_t red[4];
     for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
-        const T* row = x + m * K;
-        const float a = row_scale_i8<256>(row, K, red);
+        const float a = quantize_row<256>(x + m * K, K, red, [&](int c, uint4 q) __attribute__((always_inline)) {
+            *reinterpret_cast<uint4*>(xq + m * K + 16 * c) = q;
+        });
         if (threadIdx.x == 0) ascale[m] = a;
-        for (int c = threadIdx.x; c < K / 16; c += 256) *reinterpret_cast<uint4*>(xq + m * K + 16 * c) = quant16(row + 16 * c, a);
     }
 }
 
@@ -43,12 +44,14 @@ __global__ __launch_bounds__(256) void quant_rows_i8_kernel(const T* __restrict_
 // along K.  K is taken in stages of WK k-tiles of 128; the waves of index wk along K multiply k-tile wk of a
 // stage, and their sums are added at the end.  Operands reach LDS by direct copies into a ring of R
 // units: a unit is a whole stage (U = 1), or a stage's weights or its rows of x (U = 2, BM = BN).
-template <int WM_, int WN_, int WK_, int TM_, int TN_, int R_, int U_ = 1>
+// kX = false: x is not staged (the ring holds weights alone).
+template <int WM_, int WN_, int WK_, int TM_, int TN_, int R_, int U_ = 1, bool kX = true>
 struct Tiling {
     static constexpr int WM = WM_, WN = WN_, WK = WK_, TM = TM_, TN = TN_, R = R_, U = U_;
     static constexpr int BM = 16 * TM * WM, BN = 16 * TN * WN, NW = WM * WN * WK;
     static_assert(U == 1 || (U == 2 && WK == 1 && BM == BN), "units of one size");
-    static constexpr int kTileBytes = (BM + BN) * 128;     // one k-tile: BN rows of weights, then BM rows of x
+    static constexpr int kXRows = kX ? BM : 0;
+    static constexpr int kTileBytes = (kXRows + BN) * 128;  // one k-tile: BN rows of weights, then BM rows of x
     static constexpr int kUnitBytes = WK * kTileBytes / U;
     static constexpr int kCopies = kUnitBytes / 1024;      // of 8 rows x 128 bytes
     static constexpr int kWaveCopies = (kCopies + NW - 1) / NW;  // (the last ones may be made twice)
@@ -79,15 +82,32 @@ __device__ __forceinline__ void store_rows(const char* buf, TO* y, int N, int m0
     }
 }
 
-template <typename TO, bool kExperts, typename C>
-__global__ __launch_bounds__(64 * C::NW) void w8a8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ ascale,
+// What x is: int8 rows; int8 rows sorted by expert; or a few rows of activations (TO) that every block
+// quantizes for itself (kFused: no other launch, and x stays in LDS whole, behind the ring).
+enum XKind { kRows, kExpertRows, kFused };
+
+// LDS behind the ring for kFused: M rows of codes, Kp (K up to whole stages) bytes each, and the activations as
+// they are, in whole 1-KB copies.
+__host__ __device__ constexpr int64_t fused_codes_bytes(int64_t M, int64_t K, int wk) {
+    return M * ((K + 128 * wk - 1) / (128 * wk) * (128 * wk));
+}
+constexpr int64_t fused_raw_bytes(int64_t M, int64_t K, int element) {
+    return (M * K * element + 1023) / 1024 * 1024;
+}
+
+template <typename TO, XKind kX, typename C>
+__global__ __launch_bounds__(64 * C::NW) void w8a8_tile_kernel(const void* __restrict__ x, const float* __restrict__ ascale,
                                                                const int8_t* __restrict__ codes,
                                                                const float* __restrict__ scales, TO* __restrict__ y, int M,
                                                                int N, int K, const int32_t* __restrict__ offsets, int E,
                                                                int n_tiles, int group) {
     constexpr int TM = C::TM, TN = C::TN, R = C::R, U = C::U, BM = C::BM, BN = C::BN, CW = C::kWaveCopies;
     constexpr int kTileCopies = C::kTileBytes / 1024 / U;  // of a unit's part of one k-tile
+    constexpr bool kExperts = kX == kExpertRows, kFuse = kX == kFused;
+    static_assert(!kFuse || (U == 1 && BM == 16 && C::kXRows == 0), "a fused ring holds weights alone");
     __shared__ __attribute__((aligned(1024))) char smem[R * C::kUnitBytes];
+    extern __shared__ __attribute__((aligned(1024))) char fused_lds[];
+    const int8_t* xq = static_cast<const int8_t*>(x);
     const int lane = lane_id(), wave = wave_id();
     const int l16 = lane & 15, kg = lane >> 4;
     const int wn = wave % C::WN, wk = wave / C::WN % C::WK, wm = wave / (C::WN * C::WK);
@@ -185,8 +205,13 @@ __global__ __launch_bounds__(64 * C::NW) void w8a8_tile_kernel(const int8_t* __r
             if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
         }
     };
-    auto read_step = [&](int slot, int ks, int u) __attribute__((always_inline)) {
-        if (u < TM)
+    const int Kp = T * C::WK * 128;
+    const char* fused_x = fused_lds + min(l16, M - 1) * Kp + wk * 128 + 16 * kg;  // (kFuse)
+    // read u of stage t (in ring slot `slot`)
+    auto read_step = [&](int t, int slot, int ks, int u) __attribute__((always_inline)) {
+        if (kFuse && u < TM)
+            xf[ks][u] = *reinterpret_cast<const i32x4_t*>(fused_x + t * (C::WK * 128) + 64 * ks);
+        else if (u < TM)
             xf[ks][u] = read(U == 2 ? next_slot(slot, 1) : slot, ks, x_rt + u);
         else
             wf[ks][u - TM] = read(slot, ks, w_rt + u - TM);
@@ -202,13 +227,32 @@ __global__ __launch_bounds__(64 * C::NW) void w8a8_tile_kernel(const int8_t* __r
     using None = std::integral_constant<int, 0>;
     auto none = [](int) {};
 
+    static_assert(R * CW < 64, "the wait counts");
+    char* raw = fused_lds + fused_codes_bytes(M, K, C::WK);
+    if constexpr (kFuse) {  // all of x, ahead of the weights
+        const int last = M * K * (int)sizeof(TO) - 16, copies = (last + 16 + 1023) / 1024;
+        for (int c = wave; c < copies; c += C::NW)
+            dma16((uint32_t)min(1024 * c + 16 * lane, last), x, lds_addr(raw) + (uint32_t)(1024 * c));
+    }
 #pragma unroll
     for (int u = 0; u < R * CW - kLate; ++u) copy(u / CW / U, u / CW % U, u / CW, u % CW);
-    static_assert((R - U) * CW < 64, "the wait counts");
+    __shared__ float fused_scale[kFuse ? 16 : 1];
+    if constexpr (kFuse) {  // codes and scales, while the first weights are on their way
+        __shared__ uint32_t red[C::NW];
+        wait_vm<R * CW - kLate>();
+        __syncthreads();
+        for (int m = 0; m < M; ++m) {
+            const float a = quantize_row<64 * C::NW>(reinterpret_cast<const TO*>(raw) + m * K, K, red,
+                                                     [&](int c, uint4 q) __attribute__((always_inline)) {
+                                                         *reinterpret_cast<uint4*>(fused_lds + m * Kp + 16 * c) = q;
+                                                     });
+            if (threadIdx.x == 0) fused_scale[m] = a;
+        }
+    }
     wait_vm<(R - U) * CW - kLate>();
     __syncthreads();
 #pragma unroll
-    for (int u = 0; u < kReads; ++u) read_step(0, 0, u);
+    for (int u = 0; u < kReads; ++u) read_step(0, 0, 0, u);
 
     // Stage t: its first k-step's fragments are in registers.  The second's are read under the first's
     // products; then stage t's units are no longer needed: behind the barrier, which also waits for stage
@@ -226,17 +270,17 @@ __global__ __launch_bounds__(64 * C::NW) void w8a8_tile_kernel(const int8_t* __r
     if (row0 + 16 * TM * wm < row_end) {
         for (int t = 0; t + 1 < T; ++t) {
             const int next = next_slot(slot, U);
-            multiply(0, NReads{}, [&](int u) __attribute__((always_inline)) { read_step(slot, 1, u); }, NLate{},
+            multiply(0, NReads{}, [&](int u) __attribute__((always_inline)) { read_step(t, slot, 1, u); }, NLate{},
                      [&](int u) __attribute__((always_inline)) { late(t, slot, u); });
             wait_vm<(R - 2 * U) * CW>();
             __syncthreads();
-            multiply(1, NReads{}, [&](int u) __attribute__((always_inline)) { read_step(next, 0, u); }, NEarly{},
+            multiply(1, NReads{}, [&](int u) __attribute__((always_inline)) { read_step(t + 1, next, 0, u); }, NEarly{},
                      [&](int u) __attribute__((always_inline)) { early(t, slot, u); });
             slot = next;
         }
         // the last stage: chunks past K (and k-tiles past the last) count as zero
 #pragma unroll
-        for (int u = 0; u < kReads; ++u) read_step(slot, 1, u);
+        for (int u = 0; u < kReads; ++u) read_step(T - 1, slot, 1, u);
         const int chunks = (K - ((T - 1) * C::WK + wk) * 128) / 16;
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
@@ -293,7 +337,7 @@ __global__ __launch_bounds__(64 * C::NW) void w8a8_tile_kernel(const int8_t* __r
     for (int b = 0; b < TM; ++b) {
         const int mb = row0 + 16 * (TM * wm + b);
         if (mb >= row_end) break;
-        const float am = ascale[min(mb + l16, row_end - 1)];
+        const float am = kFuse ? fused_scale[min(l16, M - 1)] : ascale[min(mb + l16, row_end - 1)];
 #pragma unroll
         for (int a = 0; a < TN; ++a) {
             Pack<TO, 4> o;
@@ -308,7 +352,7 @@ __global__ __launch_bounds__(64 * C::NW) void w8a8_tile_kernel(const int8_t* __r
 }
 
 struct Product {
-    const int8_t* xq;
+    const void* x;  // int8 rows, or activations (fused)
     const float* ascale;
     const int8_t* codes;
     const float* scales;
@@ -324,32 +368,36 @@ hipError_t launch_tiles(const Product& p, TO* y) {
     const dim3 grid((unsigned)(tn * tm)), block(64 * C::NW);
     constexpr int kGroup = C::BM < 256 ? 1024 / C::BM : 4;  // row tiles walked together: about 1024 rows
     if (p.offsets)
-        hipLaunchKernelGGL((w8a8_tile_kernel<TO, true, C>), grid, block, 0, p.stream, p.xq, p.ascale, p.codes, p.scales, y,
+        hipLaunchKernelGGL((w8a8_tile_kernel<TO, kExpertRows, C>), grid, block, 0, p.stream, p.x, p.ascale, p.codes, p.scales, y,
                            (int)p.M, (int)p.N, (int)p.K, p.offsets, (int)p.E, (int)tn, kGroup);
     else
-        hipLaunchKernelGGL((w8a8_tile_kernel<TO, false, C>), grid, block, 0, p.stream, p.xq, p.ascale, p.codes, p.scales, y,
+        hipLaunchKernelGGL((w8a8_tile_kernel<TO, kRows, C>), grid, block, 0, p.stream, p.x, p.ascale, p.codes, p.scales, y,
                            (int)p.M, (int)p.N, (int)p.K, nullptr, 1, (int)tn, kGroup);
     return hipGetLastError();
 }
 
-// The tilings, and what one costs: a block takes `us_ktile` for each 128 of K (measured where every block has
+// The tilings, and what one costs.  A block takes `us_ktile` for each 128 of K (measured where every block has
 // a CU to itself: 4096 columns, K = 4096 and 14336) and `us_block` besides; `blocks` of them fit a CU,
-// which runs them at the same rate in all.  The choice by that sum is within 2% of the fastest of these
-// in 31 of 33 shapes of 1 to 2048 rows, within 13% in the others.
-template <int BM, int BN>
+// which runs them at the same rate in all.  Few rows wait for the weights instead, which arrive at `tbs` TB/s
+// (measured on eight matrices of 14336 x 4096 and 64 of 1024 x 2048).  The choice by this is within 2% of
+// the fastest in 31 of 33 shapes of 1 to 2048 rows of one matrix, within 13% in the others; of experts,
+// whose row counts are not known here, within 10%.
 struct Cost {
     double us_ktile, us_block;
     int blocks;
-    double of(int64_t row_tiles, int64_t N, int64_t K) const {
-        const double waves = (double)(row_tiles * ((N + BN - 1) / BN)) / 256, up = std::ceil(waves);
+    double tbs;
+    double us(int64_t tiles, int64_t K, double weight_bytes) const {
+        const double waves = (double)tiles / 256, up = std::ceil(waves);
         const double rounds = blocks == 1 ? up : waves <= 1 ? 1.0 : std::max(waves, 0.9 * up);
-        return 2.6 + rounds * ((double)((K + 127) / 128) * us_ktile + us_block);
+        const double work = rounds * ((double)((K + 127) / 128) * us_ktile + us_block);
+        return 2.6 + std::max(work, weight_bytes / tbs * 1e-6) + 0.03 * work;  // (of two that wait, the idler one)
     }
 };
 using T256x256 = Tiling<2, 4, 1, 8, 4, 5, 2>;
 using T128x256 = Tiling<2, 4, 1, 4, 4, 3>;
 using T128x128 = Tiling<2, 4, 1, 4, 2, 5, 2>;
 using T64x128 = Tiling<2, 4, 1, 2, 2, 3>;
+using T32x128 = Tiling<2, 4, 1, 1, 2, 4>;
 using T64x64 = Tiling<2, 2, 1, 2, 2, 4>;
 using T32x32 = Tiling<2, 2, 2, 1, 1, 4>;
 using T16x64 = Tiling<1, 4, 1, 1, 1, 4>;
@@ -358,25 +406,56 @@ using T16x16 = Tiling<1, 1, 4, 1, 1, 6>;
 
 template <typename TO>
 hipError_t launch_product(const Product& p, TO* y) {
+    // an even share of the rows for each expert that can have any
+    const int64_t used = std::min(p.M, p.E), each = (p.M + used - 1) / used;
+    const double weight_bytes = (double)used * (double)p.N * (double)p.K;
     hipError_t (*best)(const Product&, TO*) = nullptr;
     double least = 0;
-    auto consider = [&](auto tiling, double us_ktile, double us_block, int blocks) {
+    auto consider = [&](auto tiling, Cost cost) {
         using C = decltype(tiling);
-        // row tiles: of experts, as many as an even share of the rows takes
-        const int64_t used = std::min(p.M, p.E), each = (p.M + used - 1) / used;
-        const double us = Cost<C::BM, C::BN>{us_ktile, us_block, blocks}.of(used * ((each + C::BM - 1) / C::BM), p.N, p.K);
+        const int64_t tiles = used * ((each + C::BM - 1) / C::BM) * ((p.N + C::BN - 1) / C::BN);
+        const double us = cost.us(tiles, p.K, weight_bytes);
         if (best == nullptr || us < least) best = launch_tiles<C, TO>, least = us;
     };
-    consider(T256x256{}, 1.25, 4.0, 1);
-    consider(T128x256{}, 0.72, 2.0, 1);
-    consider(T128x128{}, 0.43, 1.0, 2);
-    consider(T64x128{}, 0.33, 1.0, 2);
-    consider(T64x64{}, 0.25, 0.6, 2);
-    consider(T32x32{}, 0.13, 0.4, 2);
-    consider(T16x64{}, 0.19, 0.3, 4);
-    consider(T16x32{}, 0.098, 0.3, 3);
-    consider(T16x16{}, 0.07, 0.3, 1);
+    consider(T256x256{}, {1.25, 4.0, 1, 5.0});
+    consider(T128x256{}, {0.72, 2.0, 1, 5.0});
+    consider(T128x128{}, {0.43, 1.0, 2, 5.2});
+    consider(T64x128{}, {0.33, 1.0, 2, 5.3});
+    consider(T32x128{}, {0.30, 1.0, 2, 5.5});
+    consider(T64x64{}, {0.25, 0.6, 2, 5.2});
+    consider(T32x32{}, {0.13, 0.4, 2, 5.3});
+    consider(T16x64{}, {0.19, 0.3, 4, 5.8});
+    consider(T16x32{}, {0.098, 0.3, 3, 5.8});
+    consider(T16x16{}, {0.07, 0.3, 1, 5.2});
     return best(p, y);
+}
+
+// x quantized by every block for itself.
+template <typename C, typename TO>
+hipError_t launch_fused_tiles(const Product& p, TO* y) {
+    const int64_t tn = (p.N + C::BN - 1) / C::BN;
+    const size_t lds = (size_t)(fused_codes_bytes(p.M, p.K, C::WK) + fused_raw_bytes(p.M, p.K, sizeof(TO)));
+    hipLaunchKernelGGL((w8a8_tile_kernel<TO, kFused, C>), dim3((unsigned)tn), dim3(64 * C::NW), lds, p.stream, p.x, nullptr,
+                       p.codes, p.scales, y, (int)p.M, (int)p.N, (int)p.K, nullptr, 1, (int)tn, 1);
+    return hipGetLastError();
+}
+using F16x32 = Tiling<1, 2, 2, 1, 1, 4, 1, false>;
+using F16x16 = Tiling<1, 1, 4, 1, 1, 6, 1, false>;
+
+// Rows that the product quantizes itself: two at most (each block quantizes all of x, so the work grows with
+// every row: at K = 4096, N = 14336 one row takes 10.7 us against 13.5 in two launches, two rows 11.8
+// against 13.8, four 14.7 against 14.0), and as long as they fit LDS beside the weights.
+constexpr int64_t kFusedRows = 2;
+constexpr int64_t kFusedBytes = 48 << 10;
+template <typename TO>
+bool fused_fits(const Product& p) {
+    return p.M <= kFusedRows && fused_codes_bytes(p.M, p.K, 4) + fused_raw_bytes(p.M, p.K, sizeof(TO)) <= kFusedBytes;
+}
+// 16 columns a block where that leaves no CU more than one block (4096 columns of K = 4096 / 14336: 5.7 / 13.0
+// us against 6.7 / 15.3), else 32 (14336 columns of K = 4096: 10.7 us against 13.2).
+template <typename TO>
+hipError_t launch_fused(const Product& p, TO* y) {
+    return p.N <= 16 * 256 ? launch_fused_tiles<F16x16>(p, y) : launch_fused_tiles<F16x32>(p, y);
 }
 
 }  // namespace
@@ -394,6 +473,17 @@ hipError_t launch_quant_rows_i8(int dtype, const void* x, int64_t M, int64_t K, 
 
 bool w8a8_fits_grid(int64_t M, int64_t N, int64_t E) {
     return ((N + 15) / 16) * expert_tiles(M, E, 16) <= (int64_t)1 << 30 && M * N <= (int64_t)1 << 36;
+}
+
+hipError_t launch_matmul_w8a8(int dtype, const void* x, int64_t M, const int8_t* codes, const float* scales, int64_t N,
+                              int64_t K, void* y, int8_t* xq, float* ascale, hipStream_t stream) {
+    return with_act_type(dtype, [&](auto t) {
+        using T = decltype(t);
+        const Product fused{x, nullptr, codes, scales, M, N, K, nullptr, 1, stream};
+        if (fused_fits<T>(fused)) return launch_fused(fused, static_cast<T*>(y));
+        if (const hipError_t e = launch_quant_rows_i8(dtype, x, M, K, xq, ascale, stream); e != hipSuccess) return e;
+        return launch_product<T>(Product{xq, ascale, codes, scales, M, N, K, nullptr, 1, stream}, static_cast<T*>(y));
+    });
 }
 
 hipError_t launch_gemm_w8a8(int dtype, const int8_t* xq, const float* ascale, int64_t M, const int8_t* codes,

@@ -118,15 +118,16 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const TI* __re
     __syncthreads();
     // first rows of every (wave, key): one key per thread
     static_assert(kMaxExperts < kSortThreads, "a thread per key");
-    int total = 0;
+    int c[kSortWaves] = {}, total = 0;
     if (t < keys) {
-        int s = kBlocks ? all[keys + t] : 0;
-        for (int w = 0; w < kSortWaves; ++w) {
-            const int c = cnt[w * keys + t];
-            cnt[w * keys + t] = s;
-            s += c;
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) c[w] = cnt[w * keys + t];
+        if constexpr (kBlocks) {
+            total = all[t];
+        } else {
+#pragma unroll
+            for (int w = 0; w < kSortWaves; ++w) total += c[w];
         }
-        total = kBlocks ? all[t] : s;
     }
     int end = total;  // inclusive sum over the keys
 #pragma unroll
@@ -137,10 +138,15 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const TI* __re
     if (lane == kWave - 1) sums[wave] = end;
     __syncthreads();
     if (t < keys) {
-        int first = end - total;
-        for (int w = 0; w < wave; ++w) first += sums[w];
-        for (int w = 0; w < kSortWaves; ++w) cnt[w * keys + t] += first;
-        if (blockIdx.x == 0) offsets[t] = first;  // key E's first row is offsets[E]
+        int next = end - total;
+        for (int w = 0; w < wave; ++w) next += sums[w];
+        if (blockIdx.x == 0) offsets[t] = next;  // key E's first row is offsets[E]
+        if constexpr (kBlocks) next += all[keys + t];
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) {
+            cnt[w * keys + t] = next;
+            next += c[w];
+        }
     }
     __syncthreads();
     auto place = [&](int64_t p, int key, int row) __attribute__((always_inline)) {
@@ -210,18 +216,17 @@ __global__ __launch_bounds__(256) void gather_i8_kernel(const T* __restrict__ x,
                                                         const int32_t* __restrict__ pos, int K, int8_t* __restrict__ xq,
                                                         float* __restrict__ ascale) {
     __shared__ uint32_t red[4];
+    __shared__ int32_t rows[kMaxExperts];  // the token's, fetched beside its activations (topk <= kMaxExperts)
     const int64_t P = Tn * topk;
     for (int64_t t = blockIdx.x; t < Tn; t += gridDim.x) {
+        __syncthreads();  // rows may still be read
+        for (int j = threadIdx.x; j < topk; j += 256) rows[j] = (int32_t)pair_row(pos, t * topk + j, P);
         const float a = quantize_row<256>(x + t * K, K, red, [&](int c, uint4 q) __attribute__((always_inline)) {
-            for (int j = 0; j < topk; ++j) {
-                const int64_t r = pair_row(pos, t * topk + j, P);
-                if (r >= 0) *reinterpret_cast<uint4*>(xq + r * K + 16 * c) = q;
-            }
+            for (int j = 0; j < topk; ++j)
+                if (rows[j] >= 0) *reinterpret_cast<uint4*>(xq + (int64_t)rows[j] * K + 16 * c) = q;
         });
-        for (int j = threadIdx.x; j < topk; j += 256) {
-            const int64_t r = pair_row(pos, t * topk + j, P);
-            if (r >= 0) ascale[r] = a;
-        }
+        for (int j = threadIdx.x; j < topk; j += 256)
+            if (rows[j] >= 0) ascale[rows[j]] = a;
     }
 }
 

@@ -238,9 +238,9 @@ def w4a16_matmul_w4a8(fmt: int, x, M: int, codes, scales, mins, N: int, K: int, 
 
 
 # ---- W8A8 and the experts' operators --------------------------------------------------------------
-# Tensors given to these must be on one GPU, contiguous and at least as large as the call reads or
-# writes (W4A16_ERR_INVALID otherwise); the launch goes to that GPU's current stream, whichever GPU is
-# current.  Raw addresses are passed as they are.
+# Tensors given to these must be on one GPU, contiguous, of elements as wide as the call takes them and at
+# least as large as it reads or writes (W4A16_ERR_INVALID otherwise); the launch goes to that GPU's current
+# stream, whichever GPU is current.  Raw addresses are passed as they are.
 
 _ELEMENT = {W4A16_BF16: 2, W4A16_FP16: 2, W4A16_FP32: 4}
 
@@ -250,46 +250,46 @@ def _element(dtype: int) -> int:
 
 
 def _call(name: str, args, arrays, stream) -> None:
-    """lib.<name>(*args, stream): ``arrays`` gives the array arguments' places in ``args`` and the bytes
-    each must hold."""
+    """lib.<name>(*args, stream): ``arrays`` gives the array arguments' places in ``args``, the elements
+    each must hold and their bytes (0: any)."""
     device = None
     args = list(args)
-    for at, nbytes in arrays:
+    for at, count, width in arrays:
         t = args[at]
         if t is None or isinstance(t, int):
             continue
         d = t.get_device()
-        if d != device and (d < 0 or device is not None) or t.nbytes < nbytes or not t.is_contiguous():
+        if (d != device and (d < 0 or device is not None) or t.nbytes < count * (width or 1)
+                or (width and t.element_size() != width) or not t.is_contiguous()):
             raise W4A16Error(W4A16_ERR_INVALID, name)
         device = d
         args[at] = t.data_ptr()
-    if stream is not None:
-        status = getattr(lib, name)(*args, _stream(stream))
-    elif device is None or device == _current_device():
-        status = getattr(lib, name)(*args, _current_stream(_current_device() if device is None else device))
+    fn = getattr(lib, name)
+    if device is None or device == _current_device():
+        status = fn(*args, _stream(stream))
     else:
         import torch
         with torch.cuda.device(device):
-            status = getattr(lib, name)(*args, _current_stream(device))
+            status = fn(*args, _stream(stream))
     if status != W4A16_OK:
         raise W4A16Error(status, name)
 
 
 def w4a16_quantize_rows_i8(act: int, x, M: int, K: int, xq, ascale, stream=None) -> None:
     _call("w4a16_quantize_rows_i8", (act, x, M, K, xq, ascale),
-          ((1, M * K * _element(act)), (4, M * K), (5, 4 * M)), stream)
+          ((1, M * K, _element(act)), (4, M * K, 1), (5, M, 4)), stream)
 
 
 def w4a16_gemm_w8a8(fmt: int, out: int, xq, ascale, M: int, codes, scales, mins, N: int, K: int, y, stream=None) -> None:
     _call("w4a16_gemm_w8a8", (fmt, out, xq, ascale, M, codes, scales, mins, N, K, y),
-          ((2, M * K), (3, 4 * M), (5, N * K), (6, 4 * N), (7, 0), (10, M * N * _element(out))), stream)
+          ((2, M * K, 1), (3, M, 4), (5, N * K, 1), (6, N, 4), (7, 0, 0), (10, M * N, _element(out))), stream)
 
 
 def w4a16_matmul_w8a8(fmt: int, act: int, x, M: int, codes, scales, mins, N: int, K: int, y, workspace,
                       workspace_bytes: int, stream=None) -> None:
     b = _element(act)
     _call("w4a16_matmul_w8a8", (fmt, act, x, M, codes, scales, mins, N, K, y, workspace, workspace_bytes),
-          ((2, M * K * b), (4, N * K), (5, 4 * N), (6, 0), (9, M * N * b), (10, workspace_bytes)), stream)
+          ((2, M * K, b), (4, N * K, 1), (5, N, 4), (6, 0, 0), (9, M * N, b), (10, workspace_bytes, 0)), stream)
 
 
 def w4a16_w8a8_workspace_bytes(fmt: int, M: int, N: int, K: int) -> int:
@@ -299,8 +299,8 @@ def w4a16_w8a8_workspace_bytes(fmt: int, M: int, N: int, K: int) -> int:
 def w4a16_gemm_w8a8_experts(fmt: int, out: int, xq, ascale, R: int, offsets, E: int, codes, scales, mins, N: int, K: int,
                             y, stream=None) -> None:
     _call("w4a16_gemm_w8a8_experts", (fmt, out, xq, ascale, R, offsets, E, codes, scales, mins, N, K, y),
-          ((2, R * K), (3, 4 * R), (5, 4 * (E + 1)), (7, E * N * K), (8, 4 * E * N), (9, 0),
-           (12, R * N * _element(out))), stream)
+          ((2, R * K, 1), (3, R, 4), (5, E + 1, 4), (7, E * N * K, 1), (8, E * N, 4), (9, 0, 0),
+           (12, R * N, _element(out))), stream)
 
 
 def w4a16_max_experts() -> int:
@@ -315,31 +315,31 @@ def w4a16_expert_sort(ids, id_bits: int, T: int, topk: int, E: int, offsets, pos
                       workspace_bytes: int = 0, stream=None) -> None:
     P = T * topk
     _call("w4a16_expert_sort", (ids, id_bits, T, topk, E, offsets, pos, src, workspace, workspace_bytes),
-          ((0, P * id_bits // 8), (5, 4 * (E + 1)), (6, 4 * P), (7, 4 * P), (8, workspace_bytes)), stream)
+          ((0, P, id_bits // 8), (5, E + 1, 4), (6, P, 4), (7, P, 4), (8, workspace_bytes, 0)), stream)
 
 
 def w4a16_expert_gather(act: int, x, T: int, topk: int, pos, K: int, xs, stream=None) -> None:
-    b = K * _element(act)
-    _call("w4a16_expert_gather", (act, x, T, topk, pos, K, xs), ((1, T * b), (4, 4 * T * topk), (6, T * topk * b)), stream)
+    P, b = T * topk, _element(act)
+    _call("w4a16_expert_gather", (act, x, T, topk, pos, K, xs), ((1, T * K, b), (4, P, 4), (6, P * K, b)), stream)
 
 
 def w4a16_expert_gather_i8(act: int, x, T: int, topk: int, pos, K: int, xq, ascale, stream=None) -> None:
     P = T * topk
     _call("w4a16_expert_gather_i8", (act, x, T, topk, pos, K, xq, ascale),
-          ((1, T * K * _element(act)), (4, 4 * P), (6, P * K), (7, 4 * P)), stream)
+          ((1, T * K, _element(act)), (4, P, 4), (6, P * K, 1), (7, P, 4)), stream)
 
 
 def w4a16_expert_combine(act: int, ys, T: int, topk: int, pos, weights, N: int, y, stream=None) -> None:
-    P, b = T * topk, N * _element(act)
-    _call("w4a16_expert_combine", (act, ys, T, topk, pos, weights, N, y), ((1, P * b), (4, 4 * P), (5, 4 * P), (7, T * b)),
-          stream)
+    P, b = T * topk, _element(act)
+    _call("w4a16_expert_combine", (act, ys, T, topk, pos, weights, N, y),
+          ((1, P * N, b), (4, P, 4), (5, P, 4), (7, T * N, b)), stream)
 
 
 def w4a16_expert_combine_backward(act: int, dy, ys, T: int, topk: int, pos, weights, N: int, dys, dweights,
                                   stream=None) -> None:
-    P, b = T * topk, N * _element(act)
+    P, b = T * topk, _element(act)
     _call("w4a16_expert_combine_backward", (act, dy, ys, T, topk, pos, weights, N, dys, dweights),
-          ((1, T * b), (2, P * b), (5, 4 * P), (6, 4 * P), (8, P * b), (9, 4 * P)), stream)
+          ((1, T * N, b), (2, P * N, b), (5, P, 4), (6, P, 4), (8, P * N, b), (9, P, 4)), stream)
 
 
 # ---- memory plumbing (torch allocations with the ABI's shapes and dtypes) ------------------------

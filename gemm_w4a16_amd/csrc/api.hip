@@ -543,7 +543,7 @@ w4a16_status_t w4a16_gemm_w8a8(w4a16_format_t fmt, w4a16_dtype_t out, const int8
                                hipStream_t stream) {
     if (w4a16_status_t st = check_w8a8(fmt, out, M, codes, scales, mins, N, K, y); st != W4A16_OK) return st;
     if (!aligned16(xq) || !aligned16(ascale)) return W4A16_ERR_INVALID;
-    if (!w4a16::w8a8_fits_grid(M, N, 1)) return W4A16_ERR_UNSUPPORTED;
+    if (!w4a16::w8a8_fits_grid(M, N, false, 1)) return W4A16_ERR_UNSUPPORTED;
     w4a16::clear_stale_error();
     return from_hip(w4a16::launch_gemm_w8a8((int)out, xq, ascale, M, static_cast<const int8_t*>(codes),
                                             static_cast<const float*>(scales), N, K, y, nullptr, 1, stream));
@@ -560,7 +560,7 @@ w4a16_status_t w4a16_matmul_w8a8(w4a16_format_t fmt, w4a16_dtype_t act, const vo
     if (w4a16_status_t st = check_w8a8(fmt, act, M, codes, scales, mins, N, K, y); st != W4A16_OK) return st;
     const W8A8Workspace w = w8a8_workspace(M, K);
     if (!aligned16(x) || !aligned16(workspace) || workspace_bytes < w.total) return W4A16_ERR_INVALID;
-    if (!w4a16::w8a8_fits_grid(M, N, 1)) return W4A16_ERR_UNSUPPORTED;
+    if (!w4a16::w8a8_fits_grid(M, N, false, 1)) return W4A16_ERR_UNSUPPORTED;
     int8_t* xq = static_cast<int8_t*>(workspace);
     float* ascale = reinterpret_cast<float*>(xq + w.ascale);
     w4a16::clear_stale_error();
@@ -573,7 +573,7 @@ w4a16_status_t w4a16_gemm_w8a8_experts(w4a16_format_t fmt, w4a16_dtype_t out, co
                                        const void* mins, int64_t N, int64_t K, void* y, hipStream_t stream) {
     if (w4a16_status_t st = check_w8a8(fmt, out, R, codes, scales, mins, N, K, y); st != W4A16_OK) return st;
     if (E <= 0 || E > kMaxDim || !aligned16(xq) || !aligned16(ascale) || !aligned16(offsets)) return W4A16_ERR_INVALID;
-    if (E > w4a16::kMaxExperts || !w4a16::w8a8_fits_grid(R, N, E)) return W4A16_ERR_UNSUPPORTED;
+    if (E > w4a16::kMaxExperts || !w4a16::w8a8_fits_grid(R, N, true, E)) return W4A16_ERR_UNSUPPORTED;
     w4a16::clear_stale_error();
     return from_hip(w4a16::launch_gemm_w8a8((int)out, xq, ascale, R, static_cast<const int8_t*>(codes),
                                             static_cast<const float*>(scales), N, K, y, offsets, E, stream));

@@ -157,7 +157,7 @@ hipError_t launch_matmul_w4a8_fused(const uint16_t* x, int64_t M, const uint32_t
 // that output type; offsets null for one matrix, else E + 1 first rows of E experts' matrices.
 hipError_t launch_quant_rows_i8(int dtype, const void* x, int64_t M, int64_t K, int8_t* xq, float* ascale,
                                 hipStream_t stream);
-bool w8a8_fits_grid(int64_t M, int64_t N, int64_t E);
+bool w8a8_fits_grid(int64_t M, int64_t N, bool experts, int64_t E);
 hipError_t launch_gemm_w8a8(int dtype, const int8_t* xq, const float* ascale, int64_t M, const int8_t* codes,
                             const float* scales, int64_t N, int64_t K, void* y, const int32_t* offsets, int64_t E,
                             hipStream_t stream);

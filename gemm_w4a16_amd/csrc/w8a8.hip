@@ -365,10 +365,20 @@ struct Product {
     hipStream_t stream;
 };
 
+// Blocks of a launch: the experts' row tiles are counted on the device, at most this many.
+template <typename C>
+int64_t launch_blocks(int64_t M, int64_t N, bool experts, int64_t E) {
+    return ((N + C::BN - 1) / C::BN) * (experts ? expert_tiles(M, E, C::BM) : (M + C::BM - 1) / C::BM);
+}
+template <typename C>
+bool fits_grid(int64_t M, int64_t N, bool experts, int64_t E) {
+    return launch_blocks<C>(M, N, experts, E) < ((int64_t)1 << 31) / (64 * C::NW);  // the grid's threads
+}
+
 template <typename C, typename TO>
 hipError_t launch_tiles(const Product& p, TO* y) {
-    const int64_t tn = (p.N + C::BN - 1) / C::BN, tm = p.offsets ? expert_tiles(p.M, p.E, C::BM) : (p.M + C::BM - 1) / C::BM;
-    const dim3 grid((unsigned)(tn * tm)), block(64 * C::NW);
+    const int64_t tn = (p.N + C::BN - 1) / C::BN;
+    const dim3 grid((unsigned)launch_blocks<C>(p.M, p.N, p.offsets != nullptr, p.E)), block(64 * C::NW);
     constexpr int kGroup = C::BM < 256 ? 1024 / C::BM : 4;  // row tiles walked together: about 1024 rows
     if (p.offsets)
         hipLaunchKernelGGL((w8a8_tile_kernel<TO, kExpertRows, C>), grid, block, 0, p.stream, p.x, p.ascale, p.codes, p.scales, y,
@@ -418,6 +428,7 @@ hipError_t launch_product(const Product& p, TO* y) {
         using C = decltype(tiling);
         const int64_t tiles = used * ((each + C::BM - 1) / C::BM) * ((p.N + C::BN - 1) / C::BN);
         const double us = cost.us(tiles, p.K, weight_bytes);
+        if (!fits_grid<C>(p.M, p.N, p.offsets != nullptr, p.E)) return;
         if (best == nullptr || us < least) best = launch_tiles<C, TO>, least = us;
     };
     consider(T256x256{}, {1.25, 4.0, 1, 5.0});
@@ -430,7 +441,7 @@ hipError_t launch_product(const Product& p, TO* y) {
     consider(T16x64{}, {0.19, 0.3, 4, 5.8});
     consider(T16x32{}, {0.098, 0.3, 3, 5.8});
     consider(T16x16{}, {0.07, 0.3, 1, 5.2});
-    return best(p, y);
+    return best != nullptr ? best(p, y) : hipErrorInvalidConfiguration;
 }
 
 // x quantized by every block for itself.
@@ -474,9 +485,7 @@ hipError_t launch_quant_rows_i8(int dtype, const void* x, int64_t M, int64_t K, 
     });
 }
 
-bool w8a8_fits_grid(int64_t M, int64_t N, int64_t E) {
-    return ((N + 15) / 16) * expert_tiles(M, E, 16) <= (int64_t)1 << 30 && M * N <= (int64_t)1 << 36;
-}
+bool w8a8_fits_grid(int64_t M, int64_t N, bool experts, int64_t E) { return fits_grid<T256x256>(M, N, experts, E); }
 
 hipError_t launch_matmul_w8a8(int dtype, const void* x, int64_t M, const int8_t* codes, const float* scales, int64_t N,
                               int64_t K, void* y, int8_t* xq, float* ascale, hipStream_t stream) {

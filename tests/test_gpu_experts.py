@@ -14,7 +14,7 @@ import pytest
 import torch
 
 import gemm_w4a16_amd as w
-from test_gpu_w8a8 import TYPES, W8, check, product, quantized, rows, weights
+from test_gpu_w8a8 import TYPES, W8, check, product, product_on_gpu, quantized, rows, weights
 
 pytestmark = pytest.mark.gpu
 
@@ -59,7 +59,7 @@ def gpu_sort(ids, E, bits=32, src=True):
 
 
 SORTS = [(1, 1, 1), (1, 2, 8), (4, 2, 8), (7, 3, 5), (64, 1, 64), (65, 8, 64), (1000, 8, 128), (333, 3, 512), (1024, 8, 60),
-         (8192, 1, 3), (8193, 1, 3), (4097, 2, 512), (5000, 7, 33), (70000, 4, 256), (3000, 100, 16)]
+         (8192, 1, 3), (8193, 1, 3), (2048, 1, 512), (1025, 1, 2), (4097, 2, 512), (5000, 7, 33), (70000, 4, 256), (3000, 100, 16)]
 
 
 @pytest.mark.parametrize("T,topk,E", SORTS)
@@ -289,6 +289,46 @@ def test_experts_products(counts, behind, N, K, kind):
     assert (y[n:] == 7).all()
 
 
+WIDE = [([520, 1, 700], 7, 61, 1040), ([2] * 9, 4, 1001, 1040), ([260] * 8, 0, 61, 1040), ([130, 0, 128, 257], 3, 515, 144),
+        ([17] * 20, 0, 1001, 1040), ([40] * 32, 11, 520, 1040), ([260] * 8, 1, 1001, 1040), ([1030, 900], 0, 2056, 400),
+        ([520, 1, 700], 300, 8200, 1040), ([0, 0, 900, 0, 300, 1], 2, 8200, 144)]
+
+
+@pytest.mark.parametrize("counts,behind,N,K", WIDE)
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_experts_products_wide(counts, behind, N, K, kind):
+    """Each size of tile, with experts that end inside one and rows behind them."""
+    E, n = len(counts), sum(counts)
+    R = n + behind
+    act, dt = TYPES[kind][:2]
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    q, a = quantized(rows(R, K, dt, 63))
+    codes, scales = weights(N, K, 64, E)
+    y = torch.full((R, N), 7.0, dtype=dt, device="cuda")
+    w.w4a16_gemm_w8a8_experts(W8, act, torch.from_numpy(q).cuda(), torch.from_numpy(a).cuda(), R, torch.from_numpy(offsets).cuda(),
+                              E, codes.cuda(), scales.cuda(), None, N, K, y)
+    for e in range(E):
+        lo, hi = offsets[e], offsets[e + 1]
+        if hi > lo:
+            check(y[lo:hi], product_on_gpu(q[lo:hi], a[lo:hi], codes.view(E, N, K)[e], scales.view(E, N)[e]), kind)
+    assert (y[n:] == 7).all()
+
+
+def test_offsets_out_of_range():
+    """Offsets that fall, pass R or are negative stay inside the buffers: rows behind R are not written."""
+    E, R, N, K = 5, 200, 70, 64
+    buf = torch.full((R + 600, N), 7.0, device="cuda")
+    xq = torch.ones((R, K), dtype=torch.int8, device="cuda")
+    codes, scales = torch.ones((E, N, K), dtype=torch.int8, device="cuda"), torch.ones((E, N), device="cuda")
+    for offsets in ([0, 150, 20, 180, 10, 200], [0, 500, 900, 10 ** 9, 10 ** 9, 2 ** 31 - 1], [-5, -1, 30, -2 ** 31, 90, 200],
+                    [200, 100, 50, 20, 10, 0]):
+        buf.fill_(7.0)
+        o = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+        w.w4a16_gemm_w8a8_experts(W8, w.W4A16_FP32, xq, torch.ones(R, device="cuda"), R, o, E, codes, scales, None, N, K, buf[:R])
+        got = buf.cpu()
+        assert (got[R:] == 7).all() and ((got[:R] == 7) | (got[:R] == K)).all()
+
+
 def test_no_expert_has_rows():
     y = torch.full((5, 32), 7.0, device="cuda")
     z = torch.zeros(8, dtype=torch.int32, device="cuda")
@@ -425,7 +465,12 @@ def test_training_step():
 def test_binding_checks_tensors():
     T, topk, N = 4, 2, 8
     x, pos, xs = torch.zeros((T, N), device="cuda"), torch.zeros((T, topk), dtype=torch.int32, device="cuda"), torch.zeros((T * topk, N), device="cuda")
-    for bad in [(x.cpu(), pos, xs), (x, pos[:3], xs), (x, pos, xs[:-1]), (x.t(), pos, xs), (x.half(), pos, xs)]:
+    for bad in [(x.cpu(), pos, xs), (x, pos[:3], xs), (x, pos, xs[:-1]), (x.t(), pos, xs), (x.half(), pos, xs), (x, pos.long(), xs), (x.double(), pos, xs)]:
         with pytest.raises(w.W4A16Error) as e:
             w.w4a16_expert_gather(w.W4A16_FP32, bad[0], T, topk, bad[1], N, bad[2])
+        assert e.value.status == w.W4A16_ERR_INVALID
+    o, p, s, ws, nb = w.alloc_expert_sort(T, topk, 3)
+    for ids, bits in [(pos.long(), 32), (pos, 64)]:
+        with pytest.raises(w.W4A16Error) as e:
+            w.w4a16_expert_sort(ids, bits, T, topk, 3, o, p, s, ws, nb)
         assert e.value.status == w.W4A16_ERR_INVALID

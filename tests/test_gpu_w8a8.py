@@ -124,6 +124,29 @@ def test_gemm_w8a8(M, N, K, kind):
     assert torch.equal(y, gpu_product(q, a, codes, scales, kind))  # bit for bit again
 
 
+def product_on_gpu(q, a, codes, scales):
+    """product() by torch's fp64 on the GPU, for larger shapes."""
+    s = torch.from_numpy(q).cuda().double() @ codes.cuda().double().t()
+    return (s * torch.from_numpy(a).cuda().double()[:, None] * scales.cuda().double()[None]).cpu()
+
+
+# wide products, ragged in every direction: few rows against many columns up to several rounds of the
+# largest tiles, rows of y that are whole 16-byte chunks and rows that are not
+WIDE = [(17, 2050, 1040), (16, 8200, 1040), (17, 4100, 1040), (40, 8200, 1040), (17, 16500, 1040), (33, 16512, 1040),
+        (33, 16500, 144), (65, 16500, 1040), (130, 16512, 144), (200, 16500, 1040), (200, 16512, 400), (780, 14350, 1040),
+        (1030, 14352, 144), (515, 14352, 1168), (2050, 3000, 1040), (1030, 2051, 528)]
+
+
+@pytest.mark.parametrize("M,N,K", WIDE)
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_gemm_w8a8_wide(M, N, K, kind):
+    q, a = quantized(rows(M, K, TYPES[kind][1], 23))
+    codes, scales = weights(N, K, 24)
+    y = gpu_product(q, a, codes, scales, kind)
+    check(y, product_on_gpu(q, a, codes, scales), kind)
+    assert torch.equal(y, gpu_product(q, a, codes, scales, kind))
+
+
 @pytest.mark.parametrize("M", [1, 40, 300])
 def test_largest_sums(M):
     """Codes of -128 everywhere at the largest K: sums of 2^14 K, just below 2^31."""
@@ -136,7 +159,10 @@ def test_largest_sums(M):
 
 
 @pytest.mark.parametrize("M,N,K,kind", [(1, 300, 512, "bf16"), (1, 2048, 8192, "f16"), (3, 61, 80, "f16"), (16, 64, 4096, "f32"),
-                                        (70, 260, 1040, "bf16"), (260, 300, 512, "f16")])
+                                        (70, 260, 1040, "bf16"), (260, 300, 512, "f16"), (1, 1, 16, "f32"),
+                                        (2, 5003, 2064, "f32"), (2, 700, 8192, "bf16"), (2, 700, 8208, "bf16"),
+                                        (1, 4100, 20000, "f16"), (2, 4099, 1008, "f16"), (1, 100, 12288, "f32"),
+                                        (2, 4096, 4096, "bf16"), (3, 8200, 144, "bf16")])
 def test_matmul_is_the_two_calls(M, N, K, kind):
     act, dt = TYPES[kind][:2]
     x = rows(M, K, dt, 31)
@@ -149,19 +175,21 @@ def test_matmul_is_the_two_calls(M, N, K, kind):
     assert torch.equal(y, gpu_product(q, a, codes, scales, kind))
 
 
-def test_nonfinite_rows_stay_their_own():
+@pytest.mark.parametrize("M,N,K", [(20, 130, 256), (2, 5000, 528), (1100, 300, 256)])
+def test_nonfinite_rows_stay_their_own(M, N, K):
     """A row with an infinity or NaN gives NaN outputs; every other row is what it is without it."""
-    M, N, K = 20, 130, 256
     x = rows(M, K, torch.bfloat16, 41)
     codes, scales = weights(N, K, 42)
     ws, nb = w.alloc_w8a8_workspace(W8, M, N, K)
     y = [torch.empty((M, N), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
     args = (codes.cuda(), scales.cuda(), None, N, K)
     w.w4a16_matmul_w8a8(W8, w.W4A16_BF16, x.cuda(), M, *args, y[0], ws, nb)
-    x[7, 3], x[12, 250] = float("inf"), float("nan")
+    hurt = [M // 2, M // 3] if M > 2 else [1]
+    x[hurt[0], 3] = float("inf")
+    x[hurt[-1], 250] = float("nan")
     w.w4a16_matmul_w8a8(W8, w.W4A16_BF16, x.cuda(), M, *args, y[1], ws, nb)
     bad = torch.zeros(M, dtype=torch.bool, device="cuda")
-    bad[[7, 12]] = True
+    bad[hurt] = True
     assert y[1][bad].isnan().all() and torch.equal(y[0][~bad], y[1][~bad])
 
 
@@ -232,7 +260,7 @@ def test_binding_checks_tensors():
 
     call()
     for change in [dict(xq=xq.cpu()), dict(codes=torch.zeros((K, N), dtype=torch.int8, device="cuda").t()),
-                   dict(y=y[:3]), dict(scales=scales[:7]), dict(y=y.bfloat16()),
+                   dict(y=y[:3]), dict(scales=scales[:7]), dict(y=y.bfloat16()), dict(xq=xq.float()),
                    dict(xq=torch.zeros((M, 2 * K), dtype=torch.int8, device="cuda")[:, ::2])]:
         with pytest.raises(w.W4A16Error) as e:
             call(**change)

@@ -130,38 +130,41 @@ __device__ __forceinline__ uint4 codes16(const Act16<T>& x, float a, float r) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// row[0 .. K) (K % 16 == 0) quantized by a block of kThreads: store(c, codes) for each 16 codes c; the row's
-// scale is returned.  A thread's first activations stay in registers between the two passes.  red: one word
-// per wave of LDS.
+// row[0 .. K) (K % 16 == 0) quantized by a block of kThreads, or by one wave (kThreads = 64, red unused): store(c,
+// codes) for each 16 codes c; the row's scale is returned.  A thread's first activations stay in registers
+// between the two passes.  red: one word per wave of LDS.
 template <int kThreads, typename T, typename F>
 __device__ __forceinline__ float quantize_row(const T* row, int K, uint32_t* red, F store) {
-    constexpr int kKeep = 2;
+    constexpr int kKeep = kThreads == kWave ? 3 : 2;
+    const int tid = kThreads == kWave ? lane_id() : (int)threadIdx.x;
     const Act16<T>* in = reinterpret_cast<const Act16<T>*>(row);
     Act16<T> keep[kKeep];
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < kKeep; ++i) {
-        const int c = threadIdx.x + kThreads * i;
+        const int c = tid + kThreads * i;
         if (c < K / 16) {
             keep[i] = in[c];
             m = max_bits(keep[i], m);
         }
     }
-    for (int c = threadIdx.x + kThreads * kKeep; c < K / 16; c += kThreads) m = max_bits(in[c], m);
+    for (int c = tid + kThreads * kKeep; c < K / 16; c += kThreads) m = max_bits(in[c], m);
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off));
-    __syncthreads();  // red may still be read from the row before
-    if (lane_id() == 0) red[wave_id()] = m;
-    __syncthreads();
+    if constexpr (kThreads > kWave) {
+        __syncthreads();  // red may still be read from the row before
+        if (lane_id() == 0) red[wave_id()] = m;
+        __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kThreads / kWave; ++w) m = max(m, red[w]);
+        for (int w = 0; w < kThreads / kWave; ++w) m = max(m, red[w]);
+    }
     const float a = scale_i8(from_abs_bits(m, T{})), r = 1.0f / a;
 #pragma unroll
     for (int i = 0; i < kKeep; ++i) {
-        const int c = threadIdx.x + kThreads * i;
+        const int c = tid + kThreads * i;
         if (c < K / 16) store(c, codes16(keep[i], a, r));
     }
-    for (int c = threadIdx.x + kThreads * kKeep; c < K / 16; c += kThreads) store(c, codes16(in[c], a, r));
+    for (int c = tid + kThreads * kKeep; c < K / 16; c += kThreads) store(c, codes16(in[c], a, r));
     return a;
 }
 

@@ -86,8 +86,8 @@ __device__ __forceinline__ void store_rows(const char* buf, TO* y, int N, int m0
 // quantizes for itself (kFused: no other launch, and x stays in LDS whole, behind the ring).
 enum XKind { kRows, kExpertRows, kFused };
 
-// LDS behind the ring for kFused: M rows of codes, Kp (K up to whole stages) bytes each, and the activations as
-// they are, in whole 1-KB copies.
+// LDS behind the ring for kFused: the tile's rows (16, or M if fewer) of codes, Kp (K up to whole stages) bytes
+// each, and their activations as they are, in whole 1-KB copies.
 __host__ __device__ constexpr int64_t fused_codes_bytes(int64_t M, int64_t K, int wk) {
     return M * ((K + 128 * wk - 1) / (128 * wk) * (128 * wk));
 }
@@ -208,8 +208,8 @@ __global__ __launch_bounds__(64 * C::NW) void w8a8_tile_kernel(const void* __res
             if (i == H - 1) __builtin_amdgcn_s_setprio(0);
         }
     };
-    const int Kp = T * C::WK * 128;
-    const char* fused_x = fused_lds + min(l16, M - 1) * Kp + wk * 128 + 16 * kg;  // (kFuse)
+    const int Kp = T * C::WK * 128, fm = min(M - row0, 16);  // (kFuse: the tile's rows)
+    const char* fused_x = fused_lds + min(l16, fm - 1) * Kp + wk * 128 + 16 * kg;
     // read u of stage t (in ring slot `slot`)
     auto read_step = [&](int t, int slot, int ks, int u) __attribute__((always_inline)) {
         if (kFuse && u < TM)
@@ -231,11 +231,12 @@ __global__ __launch_bounds__(64 * C::NW) void w8a8_tile_kernel(const void* __res
     auto none = [](int) {};
 
     static_assert(R * CW < 64, "the wait counts");
-    char* raw = fused_lds + fused_codes_bytes(M, K, C::WK);
-    if constexpr (kFuse) {  // all of x, ahead of the weights
-        const int last = M * K * (int)sizeof(TO) - 16, copies = (last + 16 + 1023) / 1024;
+    char* raw = fused_lds + fused_codes_bytes(min(M, 16), K, C::WK);
+    if constexpr (kFuse) {  // the tile's rows of x, ahead of the weights
+        const TO* rows = static_cast<const TO*>(x) + (size_t)row0 * K;
+        const int last = fm * K * (int)sizeof(TO) - 16, copies = (last + 16 + 1023) / 1024;
         for (int c = wave; c < copies; c += C::NW)
-            dma16((uint32_t)min(1024 * c + 16 * lane, last), x, lds_addr(raw) + (uint32_t)(1024 * c));
+            dma16((uint32_t)min(1024 * c + 16 * lane, last), rows, lds_addr(raw) + (uint32_t)(1024 * c));
     }
 #pragma unroll
     for (int u = 0; u < R * CW - kLate; ++u) copy(u / CW / U, u / CW % U, u / CW, u % CW);
@@ -244,12 +245,17 @@ __global__ __launch_bounds__(64 * C::NW) void w8a8_tile_kernel(const void* __res
         __shared__ uint32_t red[C::NW];
         wait_vm<R * CW - kLate>();
         __syncthreads();
-        for (int m = 0; m < M; ++m) {
-            const float a = quantize_row<64 * C::NW>(reinterpret_cast<const TO*>(raw) + m * K, K, red,
-                                                     [&](int c, uint4 q) __attribute__((always_inline)) {
-                                                         *reinterpret_cast<uint4*>(fused_lds + m * Kp + 16 * c) = q;
-                                                     });
-            if (threadIdx.x == 0) fused_scale[m] = a;
+        auto quantize = [&](int m, auto threads) __attribute__((always_inline)) {
+            const float a = quantize_row<decltype(threads)::value>(
+                reinterpret_cast<const TO*>(raw) + m * K, K, red, [&](int c, uint4 q) __attribute__((always_inline)) {
+                    *reinterpret_cast<uint4*>(fused_lds + m * Kp + 16 * c) = q;
+                });
+            if (lane == 0) fused_scale[m] = a;  // (every wave's is the same)
+        };
+        if (fm <= 2) {  // a row by all waves, or each wave its own rows
+            for (int m = 0; m < fm; ++m) quantize(m, std::integral_constant<int, 64 * C::NW>{});
+        } else {
+            for (int m = wave; m < fm; m += C::NW) quantize(m, std::integral_constant<int, kWave>{});
         }
     }
     wait_vm<(R - U) * CW - kLate>();
@@ -340,7 +346,7 @@ __global__ __launch_bounds__(64 * C::NW) void w8a8_tile_kernel(const void* __res
     for (int b = 0; b < TM; ++b) {
         const int mb = row0 + 16 * (TM * wm + b);
         if (mb >= row_end) break;
-        const float am = kFuse ? fused_scale[min(l16, M - 1)] : ascale[min(mb + l16, row_end - 1)];
+        const float am = kFuse ? fused_scale[min(l16, fm - 1)] : ascale[min(mb + l16, row_end - 1)];
 #pragma unroll
         for (int a = 0; a < TN; ++a) {
             Pack<TO, 4> o;
@@ -444,32 +450,45 @@ hipError_t launch_product(const Product& p, TO* y) {
     return best != nullptr ? best(p, y) : hipErrorInvalidConfiguration;
 }
 
-// x quantized by every block for itself.
+// x quantized by every block for itself: its tile's rows.
+template <typename TO>
+size_t fused_bytes(const Product& p, int wk) {
+    const int64_t rows = std::min<int64_t>(p.M, 16);
+    return (size_t)(fused_codes_bytes(rows, p.K, wk) + fused_raw_bytes(rows, p.K, sizeof(TO)));
+}
 template <typename C, typename TO>
 hipError_t launch_fused_tiles(const Product& p, TO* y) {
-    const int64_t tn = (p.N + C::BN - 1) / C::BN;
-    const size_t lds = (size_t)(fused_codes_bytes(p.M, p.K, C::WK) + fused_raw_bytes(p.M, p.K, sizeof(TO)));
-    hipLaunchKernelGGL((w8a8_tile_kernel<TO, kFused, C>), dim3((unsigned)tn), dim3(64 * C::NW), lds, p.stream, p.x, nullptr,
-                       p.codes, p.scales, y, (int)p.M, (int)p.N, (int)p.K, nullptr, 1, (int)tn, 1);
+    const int64_t tn = (p.N + C::BN - 1) / C::BN, tm = (p.M + 15) / 16;
+    hipLaunchKernelGGL((w8a8_tile_kernel<TO, kFused, C>), dim3((unsigned)(tn * tm)), dim3(64 * C::NW),
+                       fused_bytes<TO>(p, C::WK), p.stream, p.x, nullptr, p.codes, p.scales, y, (int)p.M, (int)p.N, (int)p.K,
+                       nullptr, 1, (int)tn, 64);
     return hipGetLastError();
 }
 using F16x32 = Tiling<1, 2, 2, 1, 1, 4, 1, false>;
 using F16x16 = Tiling<1, 1, 4, 1, 1, 6, 1, false>;
+using F16x16K8 = Tiling<1, 1, 8, 1, 1, 2, 1, false>;
 
-// Rows that the product quantizes itself: two at most (each block quantizes all of x, so the work grows with
-// every row: at K = 4096, N = 14336 one row takes 10.7 us against 13.5 in two launches, two rows 11.8
-// against 13.8, four 14.7 against 14.0), and as long as they fit LDS beside the weights.
+// One launch for activations where quantizing them in every block costs less than a launch of its own:
+//  - one or two rows (each block quantizes all of x, so the work grows with every row: at K = 4096, N = 14336 one
+//    row takes 10.6 us against 13.5 in two launches, two rows 11.8 against 13.8, four 16.2 against 13.6), which
+//    take few enough bytes that the blocks of a CU keep their number.  16 columns a block where that leaves
+//    no CU more than one block (4096 columns of K = 4096: 5.8 us against 6.8), else 32 (14336: 10.6 against 13.5);
+//  - up to 256 tiles of 16 rows x 16 columns, a CU each, of few enough activations (8 rows x 4096 columns of K =
+//    2048 5.2 us against 6.9, 37 x 1001 of K = 1024 5.6 against 6.5, 16 x 4096 of K = 2048 7.0 either way,
+//    37 x 1001 of K = 2064 8.4 against 7.5).
 constexpr int64_t kFusedRows = 2;
-constexpr int64_t kFusedBytes = 48 << 10;
+constexpr size_t kFusedBytes = 48 << 10;
+constexpr int64_t kFusedTileActs = 32 << 10;
+constexpr size_t kLdsBytes = (160 << 10) - 1024;  // (1 KB: scales and maxima)
 template <typename TO>
-bool fused_fits(const Product& p) {
-    return p.M <= kFusedRows && fused_codes_bytes(p.M, p.K, 4) + fused_raw_bytes(p.M, p.K, sizeof(TO)) <= kFusedBytes;
-}
-// 16 columns a block where that leaves no CU more than one block (4096 columns of K = 4096 / 14336: 5.7 / 13.0
-// us against 6.7 / 15.3), else 32 (14336 columns of K = 4096: 10.7 us against 13.2).
-template <typename TO>
-hipError_t launch_fused(const Product& p, TO* y) {
-    return p.N <= 16 * 256 ? launch_fused_tiles<F16x16>(p, y) : launch_fused_tiles<F16x32>(p, y);
+auto fused_launch(const Product& p) -> hipError_t (*)(const Product&, TO*) {
+    if (p.M <= kFusedRows && fused_bytes<TO>(p, 4) <= kFusedBytes)
+        return p.N <= 16 * 256 ? launch_fused_tiles<F16x16, TO> : launch_fused_tiles<F16x32, TO>;
+    using C = F16x16K8;
+    if (launch_blocks<C>(p.M, p.N, false, 1) <= 256 && std::min<int64_t>(p.M, 16) * p.K <= kFusedTileActs &&
+        fused_bytes<TO>(p, C::WK) + C::R * C::kUnitBytes <= kLdsBytes)
+        return launch_fused_tiles<C, TO>;
+    return nullptr;
 }
 
 }  // namespace
@@ -492,7 +511,7 @@ hipError_t launch_matmul_w8a8(int dtype, const void* x, int64_t M, const int8_t*
     return with_act_type(dtype, [&](auto t) {
         using T = decltype(t);
         const Product fused{x, nullptr, codes, scales, M, N, K, nullptr, 1, stream};
-        if (fused_fits<T>(fused)) return launch_fused(fused, static_cast<T*>(y));
+        if (const auto launch = fused_launch<T>(fused)) return launch(fused, static_cast<T*>(y));
         if (const hipError_t e = launch_quant_rows_i8(dtype, x, M, K, xq, ascale, stream); e != hipSuccess) return e;
         return launch_product<T>(Product{xq, ascale, codes, scales, M, N, K, nullptr, 1, stream}, static_cast<T*>(y));
     });

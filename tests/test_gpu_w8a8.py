@@ -162,7 +162,10 @@ def test_largest_sums(M):
                                         (70, 260, 1040, "bf16"), (260, 300, 512, "f16"), (1, 1, 16, "f32"),
                                         (2, 5003, 2064, "f32"), (2, 700, 8192, "bf16"), (2, 700, 8208, "bf16"),
                                         (1, 4100, 20000, "f16"), (2, 4099, 1008, "f16"), (1, 100, 12288, "f32"),
-                                        (2, 4096, 4096, "bf16"), (3, 8200, 144, "bf16")])
+                                        (2, 4096, 4096, "bf16"), (3, 8200, 144, "bf16"), (37, 1001, 2064, "f16"),
+                                        (16, 4096, 2048, "bf16"), (16, 4100, 2048, "bf16"), (9, 61, 4096, "bf16"),
+                                        (8, 700, 4608, "f16"), (40, 1300, 1024, "f32"), (16, 200, 1536, "f32"),
+                                        (500, 100, 1040, "bf16"), (17, 33, 48, "f16"), (128, 512, 512, "f32")])
 def test_matmul_is_the_two_calls(M, N, K, kind):
     act, dt = TYPES[kind][:2]
     x = rows(M, K, dt, 31)
@@ -175,7 +178,7 @@ def test_matmul_is_the_two_calls(M, N, K, kind):
     assert torch.equal(y, gpu_product(q, a, codes, scales, kind))
 
 
-@pytest.mark.parametrize("M,N,K", [(20, 130, 256), (2, 5000, 528), (1100, 300, 256)])
+@pytest.mark.parametrize("M,N,K", [(20, 130, 256), (2, 5000, 528), (1100, 300, 256), (20, 5000, 256)])
 def test_nonfinite_rows_stay_their_own(M, N, K):
     """A row with an infinity or NaN gives NaN outputs; every other row is what it is without it."""
     x = rows(M, K, torch.bfloat16, 41)

@@ -72,7 +72,7 @@ def _load() -> ctypes.CDLL:
     L.w4a16_gemm_w4a8.argtypes = [I, P, P, P, I64, P, P, P, I64, I64, P, P]
     L.w4a16_matmul_w4a8.argtypes = [I, P, I64, P, P, P, I64, I64, P, P]
     L.w4a16_quantize_rows_i8.argtypes = [I, P, I64, I64, P, P, P]
-    L.w4a16_gemm_w8a8.argtypes = [I, I, P, P, I64, P, P, P, I64, I64, P, P]
+    L.w4a16_gemm_w8a8.argtypes = [I, I, P, P, I64, P, P, P, I64, I64, P, P, SZ, P]
     L.w4a16_matmul_w8a8.argtypes = [I, I, P, I64, P, P, P, I64, I64, P, P, SZ, P]
     L.w4a16_w8a8_workspace_bytes.argtypes, L.w4a16_w8a8_workspace_bytes.restype = [I, I64, I64, I64], SZ
     L.w4a16_gemm_w8a8_experts.argtypes = [I, I, P, P, I64, P, I64, P, P, P, I64, I64, P, P]
@@ -280,9 +280,11 @@ def w4a16_quantize_rows_i8(act: int, x, M: int, K: int, xq, ascale, stream=None)
           ((1, M * K, _element(act)), (4, M * K, 1), (5, M, 4)), stream)
 
 
-def w4a16_gemm_w8a8(fmt: int, out: int, xq, ascale, M: int, codes, scales, mins, N: int, K: int, y, stream=None) -> None:
-    _call("w4a16_gemm_w8a8", (fmt, out, xq, ascale, M, codes, scales, mins, N, K, y),
-          ((2, M * K, 1), (3, M, 4), (5, N * K, 1), (6, N, 4), (7, 0, 0), (10, M * N, _element(out))), stream)
+def w4a16_gemm_w8a8(fmt: int, out: int, xq, ascale, M: int, codes, scales, mins, N: int, K: int, y, workspace=None,
+                    workspace_bytes: int = 0, stream=None) -> None:
+    _call("w4a16_gemm_w8a8", (fmt, out, xq, ascale, M, codes, scales, mins, N, K, y, workspace, workspace_bytes),
+          ((2, M * K, 1), (3, M, 4), (5, N * K, 1), (6, N, 4), (7, 0, 0), (10, M * N, _element(out)),
+           (11, workspace_bytes, 0)), stream)
 
 
 def w4a16_matmul_w8a8(fmt: int, act: int, x, M: int, codes, scales, mins, N: int, K: int, y, workspace,
@@ -387,7 +389,7 @@ def alloc_workspace(fmt: int, M: int, N: int, K: int, device="cuda"):
 
 
 def alloc_w8a8_workspace(fmt: int, M: int, N: int, K: int, device="cuda"):
-    """(tensor, bytes) sized for w4a16_matmul_w8a8 on this shape."""
+    """(tensor, bytes) sized for w4a16_matmul_w8a8 (and w4a16_gemm_w8a8) on this shape."""
     import torch
     nbytes = w4a16_w8a8_workspace_bytes(fmt, M, N, K)
     return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes

@@ -138,13 +138,16 @@ w4a16_status_t check_pairs(int64_t T, int64_t topk, int64_t width) {
     return W4A16_OK;
 }
 
-// matmul_w8a8's workspace: the codes of x, then its row scales.
+// The W8A8 workspace: the sums of K's parts, then the codes of x and its row scales (matmul_w8a8), each
+// 16-byte aligned.
 struct W8A8Workspace {
-    size_t ascale, total;
+    size_t xq, ascale, total;
 };
-W8A8Workspace w8a8_workspace(int64_t M, int64_t K) {
+W8A8Workspace w8a8_workspace(int64_t M, int64_t N, int64_t K) {
+    auto a16 = [](size_t b) { return (b + 15) & ~(size_t)15; };
     W8A8Workspace w;
-    w.ascale = (size_t)M * (size_t)K;  // K % 16 == 0: 16-byte aligned
+    w.xq = a16(w4a16::w8a8_sums_bytes(M, N, K));
+    w.ascale = w.xq + (size_t)M * (size_t)K;  // K % 16 == 0
     w.total = w.ascale + (size_t)M * 4;
     return w;
 }
@@ -540,32 +543,37 @@ w4a16_status_t w4a16_quantize_rows_i8(w4a16_dtype_t act, const void* x, int64_t 
 
 w4a16_status_t w4a16_gemm_w8a8(w4a16_format_t fmt, w4a16_dtype_t out, const int8_t* xq, const float* ascale, int64_t M,
                                const void* codes, const void* scales, const void* mins, int64_t N, int64_t K, void* y,
-                               hipStream_t stream) {
+                               void* workspace, size_t workspace_bytes, hipStream_t stream) {
     if (w4a16_status_t st = check_w8a8(fmt, out, M, codes, scales, mins, N, K, y); st != W4A16_OK) return st;
-    if (!aligned16(xq) || !aligned16(ascale)) return W4A16_ERR_INVALID;
+    if (!aligned16(xq) || !aligned16(ascale) || (workspace != nullptr && !aligned16(workspace))) return W4A16_ERR_INVALID;
     if (!w4a16::w8a8_fits_grid(M, N, false, 1)) return W4A16_ERR_UNSUPPORTED;
     w4a16::clear_stale_error();
     return from_hip(w4a16::launch_gemm_w8a8((int)out, xq, ascale, M, static_cast<const int8_t*>(codes),
-                                            static_cast<const float*>(scales), N, K, y, nullptr, 1, stream));
+                                            static_cast<const float*>(scales), N, K, y, nullptr, 1,
+                                            static_cast<int32_t*>(workspace), workspace_bytes, stream));
 }
 
 size_t w4a16_w8a8_workspace_bytes(w4a16_format_t fmt, int64_t M, int64_t N, int64_t K) {
-    if (fmt != W4A16_FMT_W8_ROW_FP32 || check_shape(fmt, N, K) != W4A16_OK || M <= 0 || M > kMaxDim) return 0;
-    return w8a8_workspace(M, K).total;
+    if (fmt != W4A16_FMT_W8_ROW_FP32 || check_shape(fmt, N, K) != W4A16_OK || M <= 0 || M > kMaxDim || K > kMaxKInt8 ||
+        !w4a16::w8a8_fits_grid(M, N, false, 1))
+        return 0;
+    return w8a8_workspace(M, N, K).total;
 }
 
 w4a16_status_t w4a16_matmul_w8a8(w4a16_format_t fmt, w4a16_dtype_t act, const void* x, int64_t M, const void* codes,
                                  const void* scales, const void* mins, int64_t N, int64_t K, void* y, void* workspace,
                                  size_t workspace_bytes, hipStream_t stream) {
     if (w4a16_status_t st = check_w8a8(fmt, act, M, codes, scales, mins, N, K, y); st != W4A16_OK) return st;
-    const W8A8Workspace w = w8a8_workspace(M, K);
-    if (!aligned16(x) || !aligned16(workspace) || workspace_bytes < w.total) return W4A16_ERR_INVALID;
+    if (!aligned16(x) || !aligned16(workspace)) return W4A16_ERR_INVALID;
     if (!w4a16::w8a8_fits_grid(M, N, false, 1)) return W4A16_ERR_UNSUPPORTED;
-    int8_t* xq = static_cast<int8_t*>(workspace);
-    float* ascale = reinterpret_cast<float*>(xq + w.ascale);
+    const W8A8Workspace w = w8a8_workspace(M, N, K);
+    if (workspace_bytes < w.total) return W4A16_ERR_INVALID;
+    char* base = static_cast<char*>(workspace);
     w4a16::clear_stale_error();
     return from_hip(w4a16::launch_matmul_w8a8((int)act, x, M, static_cast<const int8_t*>(codes),
-                                              static_cast<const float*>(scales), N, K, y, xq, ascale, stream));
+                                              static_cast<const float*>(scales), N, K, y,
+                                              reinterpret_cast<int8_t*>(base + w.xq), reinterpret_cast<float*>(base + w.ascale),
+                                              reinterpret_cast<int32_t*>(base), w.xq, stream));
 }
 
 w4a16_status_t w4a16_gemm_w8a8_experts(w4a16_format_t fmt, w4a16_dtype_t out, const int8_t* xq, const float* ascale,
@@ -576,7 +584,7 @@ w4a16_status_t w4a16_gemm_w8a8_experts(w4a16_format_t fmt, w4a16_dtype_t out, co
     if (E > w4a16::kMaxExperts || !w4a16::w8a8_fits_grid(R, N, true, E)) return W4A16_ERR_UNSUPPORTED;
     w4a16::clear_stale_error();
     return from_hip(w4a16::launch_gemm_w8a8((int)out, xq, ascale, R, static_cast<const int8_t*>(codes),
-                                            static_cast<const float*>(scales), N, K, y, offsets, E, stream));
+                                            static_cast<const float*>(scales), N, K, y, offsets, E, nullptr, 0, stream));
 }
 
 int64_t w4a16_max_experts(void) { return w4a16::kMaxExperts; }

@@ -154,16 +154,19 @@ hipError_t launch_matmul_w4a8_fused(const uint16_t* x, int64_t M, const uint32_t
                                     const uint16_t* mins, int64_t N, int64_t K, uint16_t* y, hipStream_t stream);
 
 // W8A8: int8 rows (dtype: 0 bf16, 1 fp16, 2 fp32 activations) and their product with W8 weights, in
-// that output type; offsets null for one matrix, else E + 1 first rows of E experts' matrices.
+// that output type; offsets null for one matrix, else E + 1 first rows of E experts' matrices.  sums (or null):
+// room for a product whose K is taken in parts, w8a8_sums_bytes of it to allow what the shape gains by.
 hipError_t launch_quant_rows_i8(int dtype, const void* x, int64_t M, int64_t K, int8_t* xq, float* ascale,
                                 hipStream_t stream);
 bool w8a8_fits_grid(int64_t M, int64_t N, bool experts, int64_t E);
+size_t w8a8_sums_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_w8a8(int dtype, const int8_t* xq, const float* ascale, int64_t M, const int8_t* codes,
                             const float* scales, int64_t N, int64_t K, void* y, const int32_t* offsets, int64_t E,
-                            hipStream_t stream);
+                            int32_t* sums, size_t sums_bytes, hipStream_t stream);
 // The product of activations x quantized on the way (xq and ascale hold them where a launch of its own does).
 hipError_t launch_matmul_w8a8(int dtype, const void* x, int64_t M, const int8_t* codes, const float* scales, int64_t N,
-                              int64_t K, void* y, int8_t* xq, float* ascale, hipStream_t stream);
+                              int64_t K, void* y, int8_t* xq, float* ascale, int32_t* sums, size_t sums_bytes,
+                              hipStream_t stream);
 
 // Tokens sorted by expert and back (P = T * topk pairs); widths in elements of dtype.
 constexpr int64_t kMaxExperts = 512;    // the sort keeps a count per wave and expert in LDS

@@ -82,6 +82,16 @@ __device__ __forceinline__ void store_rows(const char* buf, TO* y, int N, int m0
     }
 }
 
+// An output before its last rounding: the sum times the weight row's scale, then the activation row's, each
+// rounded to fp32.  The empty statement keeps the last product out of an instruction that multiplies and
+// rounds to 16 bits at once, which the compiler would use in some kernels only: every kernel stores the
+// same bits.
+__device__ __forceinline__ float scaled_sum(int32_t sum, float sn, float am) {
+    float v = (float)sum * sn * am;
+    asm("" : "+v"(v));
+    return v;
+}
+
 // What x is: int8 rows; int8 rows sorted by expert; or a few rows of activations (TO) that every block
 // quantizes for itself (kFused: no other launch, and x stays in LDS whole, behind the ring).
 enum XKind { kRows, kExpertRows, kFused };
@@ -95,15 +105,16 @@ constexpr int64_t fused_raw_bytes(int64_t M, int64_t K, int element) {
     return (M * K * element + 1023) / 1024 * 1024;
 }
 
+// TO int32_t: y takes the sums of one part of K (split_k columns of it, a multiple of 128) per block, [parts][M][N].
 template <typename TO, XKind kX, typename C>
 __global__ __launch_bounds__(64 * C::NW) void w8a8_tile_kernel(const void* __restrict__ x, const float* __restrict__ ascale,
                                                                const int8_t* __restrict__ codes,
                                                                const float* __restrict__ scales, TO* __restrict__ y, int M,
-                                                               int N, int K, const int32_t* __restrict__ offsets, int E,
-                                                               int n_tiles, int group) {
+                                                               int N, int stride, const int32_t* __restrict__ offsets, int E,
+                                                               int n_tiles, int group, int split_k) {
     constexpr int TM = C::TM, TN = C::TN, R = C::R, U = C::U, BM = C::BM, BN = C::BN, CW = C::kWaveCopies;
     constexpr int kTileCopies = C::kTileBytes / 1024 / U;  // of a unit's part of one k-tile
-    constexpr bool kExperts = kX == kExpertRows, kFuse = kX == kFused;
+    constexpr bool kExperts = kX == kExpertRows, kFuse = kX == kFused, kSums = std::is_same_v<TO, int32_t>;
     static_assert(!kFuse || (U == 1 && BM == 16 && C::kXRows == 0), "a fused ring holds weights alone");
     __shared__ __attribute__((aligned(1024))) char smem[R * C::kUnitBytes];
     extern __shared__ __attribute__((aligned(1024))) char fused_lds[];
@@ -116,13 +127,20 @@ __global__ __launch_bounds__(64 * C::NW) void w8a8_tile_kernel(const void* __res
     // sequence, which walks `group` row tiles at a time, rows first, so that the blocks of one XCD share
     // operands in its L2.
     int row0, row_end = M, expert = 0, tn;
+    int K = stride, k0 = 0;  // kSums: of this block's part of K
     {
         int m_tiles = (M + BM - 1) / BM;
         if constexpr (kExperts) m_tiles = count_expert_tiles(offsets, E, M, BM);
-        const int total = m_tiles * n_tiles, b = blockIdx.x;
+        const int total = kSums ? gridDim.x : m_tiles * n_tiles, b = blockIdx.x;
         if (b >= total) return;
         const int xcd = b & 7, each = total >> 3, rest = total & 7;
-        const int s = xcd * each + min(xcd, rest) + (b >> 3);
+        int s = xcd * each + min(xcd, rest) + (b >> 3);
+        if constexpr (kSums) {  // the sequence once for each part
+            const int part = s / (m_tiles * n_tiles);
+            s -= part * m_tiles * n_tiles;
+            k0 = part * split_k, K = min(split_k, stride - k0);
+            y += (size_t)part * M * N;
+        }
         const int g = s / (group * n_tiles), in = s - g * group * n_tiles;
         const int rows = min(group, m_tiles - g * group);
         tn = in / rows;
@@ -136,8 +154,8 @@ __global__ __launch_bounds__(64 * C::NW) void w8a8_tile_kernel(const void* __res
     }
     const int n0 = tn * BN;
     const int KT = (K + 127) / 128, T = (KT + C::WK - 1) / C::WK;
-    const int8_t* wbase = codes + (size_t)expert * N * K + (size_t)n0 * K;
-    const int8_t* xbase = xq + (size_t)row0 * K;
+    const int8_t* wbase = codes + ((size_t)expert * N + n0) * stride + k0;
+    const int8_t* xbase = xq + (size_t)row0 * stride + k0;
     const uint32_t lds0 = lds_addr(smem);
 
     // This wave's copies j = CW wave + i of a unit: copy jj = j % kTileCopies of k-tile j / kTileCopies, rows
@@ -153,7 +171,7 @@ __global__ __launch_bounds__(64 * C::NW) void w8a8_tile_kernel(const void* __res
             const int jj = min(CW * wave + i, C::kCopies - 1) % kTileCopies;
             const int r = 8 * jj + lane / 8, chunk = (lane % 8) ^ ((r >> 1) & 7);
             const int row = is_w(part, jj) ? min(r, N - 1 - n0) : min(U == 2 ? r : r - BN, row_end - 1 - row0);
-            voff[part][i] = (uint32_t)row * (uint32_t)K + 16u * chunk;
+            voff[part][i] = (uint32_t)row * (uint32_t)stride + 16u * chunk;
         }
     // copy i of stage t's unit `part` into ring slot `slot`; the last k-tile's chunks past K, and k-tiles past the
     // last, read what is there (their products are masked).  Stages past the last read one line over
@@ -338,25 +356,55 @@ __global__ __launch_bounds__(64 * C::NW) void w8a8_tile_kernel(const void* __res
     char* buf = smem + kOut0 + (wm * C::WN + wn) * 16 * kPitch;
     const int nw = n0 + 16 * TN * wn;
     float sn[TN][4];
+    if constexpr (!kSums) {
 #pragma unroll
-    for (int a = 0; a < TN; ++a)
+        for (int a = 0; a < TN; ++a)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sn[a][e] = scales[(size_t)expert * N + min(nw + 16 * a + 4 * kg + e, N - 1)];
+            for (int e = 0; e < 4; ++e) sn[a][e] = scales[(size_t)expert * N + min(nw + 16 * a + 4 * kg + e, N - 1)];
+    }
 #pragma unroll
     for (int b = 0; b < TM; ++b) {
         const int mb = row0 + 16 * (TM * wm + b);
         if (mb >= row_end) break;
-        const float am = kFuse ? fused_scale[min(l16, fm - 1)] : ascale[min(mb + l16, row_end - 1)];
+        float am = 1.0f;
+        if constexpr (!kSums) am = kFuse ? fused_scale[min(l16, fm - 1)] : ascale[min(mb + l16, row_end - 1)];
 #pragma unroll
         for (int a = 0; a < TN; ++a) {
             Pack<TO, 4> o;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o.v[e] = from_f32<TO>((float)acc[a][b][e] * sn[a][e] * am);
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (kSums)
+                    o.v[e] = acc[a][b][e];
+                else
+                    o.v[e] = from_f32<TO>(scaled_sum(acc[a][b][e], sn[a][e], am));
+            }
             *reinterpret_cast<Pack<TO, 4>*>(buf + l16 * kPitch + (16 * a + 4 * kg) * sizeof(TO)) = o;
         }
         wave_lds_sync();
         store_rows<TO, TN>(buf, y, N, mb, nw, row_end);
         wave_lds_sync();
+    }
+}
+
+// y = (the parts' sums, [parts][M N]) * s_n * a_m: exactly what the unsplit product stores.  V columns a thread.
+template <typename TO, int V>
+__global__ __launch_bounds__(256) void w8a8_join_kernel(const int32_t* __restrict__ sums, int parts,
+                                                        const float* __restrict__ ascale, const float* __restrict__ scales,
+                                                        int64_t M, int N, TO* __restrict__ y) {
+    const int64_t units = M * N / V, step = (int64_t)gridDim.x * 256;
+    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += step) {
+        Pack<int32_t, V> sum = load_unit<true>(reinterpret_cast<const Pack<int32_t, V>*>(sums) + u);
+        for (int p = 1; p < parts; ++p) {
+            const Pack<int32_t, V> more = load_unit<true>(reinterpret_cast<const Pack<int32_t, V>*>(sums) + p * units + u);
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum.v[i] += more.v[i];
+        }
+        const int64_t m = V * u / N;
+        const int n = (int)(V * u - m * N);
+        Pack<TO, V> o;
+#pragma unroll
+        for (int i = 0; i < V; ++i) o.v[i] = from_f32<TO>(scaled_sum(sum.v[i], scales[n + i], ascale[m]));
+        reinterpret_cast<Pack<TO, V>*>(y)[u] = o;
     }
 }
 
@@ -369,6 +417,8 @@ struct Product {
     const int32_t* offsets;
     int64_t E;
     hipStream_t stream;
+    int32_t* sums = nullptr;  // for K in parts, or null
+    size_t sums_bytes = 0;
 };
 
 // Blocks of a launch: the experts' row tiles are counted on the device, at most this many.
@@ -388,12 +438,35 @@ hipError_t launch_tiles(const Product& p, TO* y) {
     constexpr int kGroup = C::BM < 256 ? 1024 / C::BM : 4;  // row tiles walked together: about 1024 rows
     if (p.offsets)
         hipLaunchKernelGGL((w8a8_tile_kernel<TO, kExpertRows, C>), grid, block, 0, p.stream, p.x, p.ascale, p.codes, p.scales, y,
-                           (int)p.M, (int)p.N, (int)p.K, p.offsets, (int)p.E, (int)tn, kGroup);
+                           (int)p.M, (int)p.N, (int)p.K, p.offsets, (int)p.E, (int)tn, kGroup, 0);
     else
         hipLaunchKernelGGL((w8a8_tile_kernel<TO, kRows, C>), grid, block, 0, p.stream, p.x, p.ascale, p.codes, p.scales, y,
-                           (int)p.M, (int)p.N, (int)p.K, nullptr, 1, (int)tn, kGroup);
+                           (int)p.M, (int)p.N, (int)p.K, nullptr, 1, (int)tn, kGroup, 0);
     return hipGetLastError();
 }
+
+// K in `parts`, one launch for the sums and one that joins them.
+template <typename C, typename TO>
+hipError_t launch_parts(const Product& p, TO* y, int parts) {
+    const int64_t tn = (p.N + C::BN - 1) / C::BN;
+    const int64_t split = (p.K + 128 * parts - 1) / (128 * parts) * 128;
+    const dim3 grid((unsigned)(launch_blocks<C>(p.M, p.N, false, 1) * parts)), block(64 * C::NW);
+    constexpr int kGroup = C::BM < 256 ? 1024 / C::BM : 4;
+    hipLaunchKernelGGL((w8a8_tile_kernel<int32_t, kRows, C>), grid, block, 0, p.stream, p.x, nullptr, p.codes, nullptr, p.sums,
+                       (int)p.M, (int)p.N, (int)p.K, nullptr, 1, (int)tn, kGroup, (int)split);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    auto join = [&](auto v) {
+        constexpr int V = decltype(v)::value;
+        const int64_t blocks = (p.M * p.N / V + 255) / 256;
+        hipLaunchKernelGGL((w8a8_join_kernel<TO, V>), dim3((unsigned)std::min<int64_t>(blocks, kMaxGridBlocks)), dim3(256), 0,
+                           p.stream, p.sums, parts, p.ascale, p.scales, p.M, (int)p.N, y);
+        return hipGetLastError();
+    };
+    return p.N % 4 == 0 ? join(std::integral_constant<int, 4>{}) : join(std::integral_constant<int, 1>{});
+}
+
+// A join costs a launch and its bytes.
+constexpr double kJoinUs = 3.0, kJoinBytesPerUs = 5e6;
 
 // The tilings, and what one costs.  A block takes `us_ktile` for each 128 of K (measured where every block has
 // a CU to itself: 4096 columns, K = 4096 and 14336) and `us_block` besides; `blocks` of them fit a CU,
@@ -423,31 +496,66 @@ using T16x64 = Tiling<1, 4, 1, 1, 1, 4>;
 using T16x32 = Tiling<1, 2, 2, 1, 1, 4>;
 using T16x16 = Tiling<1, 1, 4, 1, 1, 6>;
 
+// The tiling for a product and the parts K is taken in (1 where `sums` has no room for more).  Parts are whole
+// k-tiles, none empty, of at least 16.
+struct Plan {
+    int tiling, parts;
+};
+template <typename F>
+void each_tiling(F f) {
+    f(0, T256x256{}, Cost{1.25, 4.0, 1, 5.0});
+    f(1, T128x256{}, Cost{0.72, 2.0, 1, 5.0});
+    f(2, T128x128{}, Cost{0.43, 1.0, 2, 5.2});
+    f(3, T64x128{}, Cost{0.33, 1.0, 2, 5.3});
+    f(4, T32x128{}, Cost{0.30, 1.0, 2, 5.5});
+    f(5, T64x64{}, Cost{0.25, 0.6, 2, 5.2});
+    f(6, T32x32{}, Cost{0.13, 0.4, 2, 5.3});
+    f(7, T16x64{}, Cost{0.19, 0.3, 4, 5.8});
+    f(8, T16x32{}, Cost{0.098, 0.3, 3, 5.8});
+    f(9, T16x16{}, Cost{0.07, 0.3, 1, 5.2});
+}
+size_t sums_bytes(int64_t M, int64_t N, int parts) { return parts > 1 ? (size_t)parts * (size_t)M * (size_t)N * 4 : 0; }
+
+Plan plan_product(int64_t M, int64_t N, int64_t K, bool experts, int64_t E, size_t room) {
+    // an even share of the rows for each expert that can have any
+    const int64_t used = std::min(M, E), each = (M + used - 1) / used, ktiles = (K + 127) / 128;
+    const double weight_bytes = (double)used * (double)N * (double)K;
+    Plan plan{-1, 1};
+    double least = 0;
+    each_tiling([&](int i, auto tiling, Cost cost) {
+        using C = decltype(tiling);
+        if (!fits_grid<C>(M, N, experts, E)) return;
+        const int64_t tiles = used * ((each + C::BM - 1) / C::BM) * ((N + C::BN - 1) / C::BN);
+        for (int parts = 1; parts <= 8; parts *= 2) {
+            const int64_t part = (ktiles + parts - 1) / parts;
+            if (parts > 1 && (experts || C::WK > 1 || C::BM * C::BN < 64 * 64 || tiles * parts > 512 || part < 16 ||
+                              part * (parts - 1) >= ktiles || sums_bytes(M, N, parts) > room))
+                break;
+            // the parts' sums are written and read once, and joined by a second launch
+            const double join = parts > 1 ? kJoinUs + 2.0 * sums_bytes(M, N, parts) / kJoinBytesPerUs : 0.0;
+            const double us = cost.us(tiles * parts, part * 128, weight_bytes) + join;
+            if (plan.tiling < 0 || us < least) plan = Plan{i, parts}, least = us;
+        }
+    });
+    return plan;
+}
+
 template <typename TO>
 hipError_t launch_product(const Product& p, TO* y) {
-    // an even share of the rows for each expert that can have any
-    const int64_t used = std::min(p.M, p.E), each = (p.M + used - 1) / used;
-    const double weight_bytes = (double)used * (double)p.N * (double)p.K;
-    hipError_t (*best)(const Product&, TO*) = nullptr;
-    double least = 0;
-    auto consider = [&](auto tiling, Cost cost) {
+    const Plan plan = plan_product(p.M, p.N, p.K, p.offsets != nullptr, p.E, p.sums != nullptr ? p.sums_bytes : 0);
+    hipError_t e = hipErrorInvalidConfiguration;
+    each_tiling([&](int i, auto tiling, Cost) {
         using C = decltype(tiling);
-        const int64_t tiles = used * ((each + C::BM - 1) / C::BM) * ((p.N + C::BN - 1) / C::BN);
-        const double us = cost.us(tiles, p.K, weight_bytes);
-        if (!fits_grid<C>(p.M, p.N, p.offsets != nullptr, p.E)) return;
-        if (best == nullptr || us < least) best = launch_tiles<C, TO>, least = us;
-    };
-    consider(T256x256{}, {1.25, 4.0, 1, 5.0});
-    consider(T128x256{}, {0.72, 2.0, 1, 5.0});
-    consider(T128x128{}, {0.43, 1.0, 2, 5.2});
-    consider(T64x128{}, {0.33, 1.0, 2, 5.3});
-    consider(T32x128{}, {0.30, 1.0, 2, 5.5});
-    consider(T64x64{}, {0.25, 0.6, 2, 5.2});
-    consider(T32x32{}, {0.13, 0.4, 2, 5.3});
-    consider(T16x64{}, {0.19, 0.3, 4, 5.8});
-    consider(T16x32{}, {0.098, 0.3, 3, 5.8});
-    consider(T16x16{}, {0.07, 0.3, 1, 5.2});
-    return best != nullptr ? best(p, y) : hipErrorInvalidConfiguration;
+        if (i != plan.tiling) return;
+        if constexpr (C::WK == 1 && C::BM * C::BN >= 64 * 64) {
+            if (plan.parts > 1) {
+                e = launch_parts<C>(p, y, plan.parts);
+                return;
+            }
+        }
+        e = launch_tiles<C>(p, y);
+    });
+    return e;
 }
 
 // x quantized by every block for itself: its tile's rows.
@@ -461,7 +569,7 @@ hipError_t launch_fused_tiles(const Product& p, TO* y) {
     const int64_t tn = (p.N + C::BN - 1) / C::BN, tm = (p.M + 15) / 16;
     hipLaunchKernelGGL((w8a8_tile_kernel<TO, kFused, C>), dim3((unsigned)(tn * tm)), dim3(64 * C::NW),
                        fused_bytes<TO>(p, C::WK), p.stream, p.x, nullptr, p.codes, p.scales, y, (int)p.M, (int)p.N, (int)p.K,
-                       nullptr, 1, (int)tn, 64);
+                       nullptr, 1, (int)tn, 64, 0);
     return hipGetLastError();
 }
 using F16x32 = Tiling<1, 2, 2, 1, 1, 4, 1, false>;
@@ -506,23 +614,30 @@ hipError_t launch_quant_rows_i8(int dtype, const void* x, int64_t M, int64_t K, 
 
 bool w8a8_fits_grid(int64_t M, int64_t N, bool experts, int64_t E) { return fits_grid<T256x256>(M, N, experts, E); }
 
+size_t w8a8_sums_bytes(int64_t M, int64_t N, int64_t K) {
+    return sums_bytes(M, N, plan_product(M, N, K, false, 1, ~(size_t)0).parts);
+}
+
 hipError_t launch_matmul_w8a8(int dtype, const void* x, int64_t M, const int8_t* codes, const float* scales, int64_t N,
-                              int64_t K, void* y, int8_t* xq, float* ascale, hipStream_t stream) {
+                              int64_t K, void* y, int8_t* xq, float* ascale, int32_t* sums, size_t sums_bytes,
+                              hipStream_t stream) {
     return with_act_type(dtype, [&](auto t) {
         using T = decltype(t);
         const Product fused{x, nullptr, codes, scales, M, N, K, nullptr, 1, stream};
         if (const auto launch = fused_launch<T>(fused)) return launch(fused, static_cast<T*>(y));
         if (const hipError_t e = launch_quant_rows_i8(dtype, x, M, K, xq, ascale, stream); e != hipSuccess) return e;
-        return launch_product<T>(Product{xq, ascale, codes, scales, M, N, K, nullptr, 1, stream}, static_cast<T*>(y));
+        return launch_product<T>(Product{xq, ascale, codes, scales, M, N, K, nullptr, 1, stream, sums, sums_bytes},
+                                 static_cast<T*>(y));
     });
 }
 
 hipError_t launch_gemm_w8a8(int dtype, const int8_t* xq, const float* ascale, int64_t M, const int8_t* codes,
                             const float* scales, int64_t N, int64_t K, void* y, const int32_t* offsets, int64_t E,
-                            hipStream_t stream) {
+                            int32_t* sums, size_t sums_bytes, hipStream_t stream) {
     return with_act_type(dtype, [&](auto t) {
         using T = decltype(t);
-        return launch_product<T>(Product{xq, ascale, codes, scales, M, N, K, offsets, E, stream}, static_cast<T*>(y));
+        return launch_product<T>(Product{xq, ascale, codes, scales, M, N, K, offsets, E, stream, sums, sums_bytes},
+                                 static_cast<T*>(y));
     });
 }
 

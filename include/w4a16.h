@@ -328,23 +328,26 @@ w4a16_status_t w4a16_quantize_rows_i8(w4a16_dtype_t act, const void* x, int64_t 
                                       hipStream_t stream);
 
 /* y [M][N] (type `out`) from int8 rows xq [M][K] and their scales, against W8 weights.  K at most
- * 2^17 - 16, so that no sum of int8 products passes 32 bits.  W8 only.  No workspace; bitwise
- * reproducible.  ERR_INVALID: type, sizes, alignment, mins not NULL; ERR_UNSUPPORTED: another
- * format, K or N past the limits, M and N too large for one launch. */
+ * 2^17 - 16, so that no sum of int8 products passes 32 bits.  W8 only.  workspace (16-byte aligned, or
+ * NULL): where a shape has too few columns to fill the GPU and K is long, and workspace_bytes holds them
+ * (w4a16_w8a8_workspace_bytes is enough), K is taken in parts whose 32-bit sums are joined by a second
+ * launch; the sums are exact, so the result is the same bits either way.  Bitwise reproducible.
+ * ERR_INVALID: type, sizes, alignment, mins not NULL; ERR_UNSUPPORTED: another format, K or N past the
+ * limits, M and N too large for one launch. */
 w4a16_status_t w4a16_gemm_w8a8(w4a16_format_t fmt, w4a16_dtype_t out, const int8_t* xq, const float* ascale, int64_t M,
                                const void* codes, const void* scales, const void* mins, int64_t N, int64_t K, void* y,
-                               hipStream_t stream);
+                               void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* y [M][N] = x [M][K] . W_hat^T with x quantized on the way: bit for bit w4a16_quantize_rows_i8
  * followed by w4a16_gemm_w8a8 with out = act.  workspace (w4a16_w8a8_workspace_bytes, 16-byte
- * aligned) holds the codes and scales of x; it needs no initialisation and must not be shared by
- * calls, or graphs of calls, that may run at the same time.  Errors as for the two calls, and
- * ERR_INVALID for a workspace that is NULL or too small. */
+ * aligned) holds the codes and scales of x and the parts' sums; it needs no initialisation and must
+ * not be shared by calls, or graphs of calls, that may run at the same time.  Errors as for the two
+ * calls, and ERR_INVALID for a workspace that is NULL or too small. */
 w4a16_status_t w4a16_matmul_w8a8(w4a16_format_t fmt, w4a16_dtype_t act, const void* x, int64_t M, const void* codes,
                                  const void* scales, const void* mins, int64_t N, int64_t K, void* y, void* workspace,
                                  size_t workspace_bytes, hipStream_t stream);
 
-/* Bytes of workspace w4a16_matmul_w8a8 needs (0 for a bad shape or another format). */
+/* Bytes of workspace w4a16_matmul_w8a8 needs (0 for a shape it refuses or another format). */
 size_t w4a16_w8a8_workspace_bytes(w4a16_format_t fmt, int64_t M, int64_t N, int64_t K);
 
 /* ---- Experts: tokens sorted by expert, the experts' products, and back -----------------------------

@@ -28,11 +28,11 @@ CALLS = {
         ({"a0": 7}, INVALID), ({"a1": None}, INVALID), ({"a1": A + 8}, INVALID), ({"a2": 0}, INVALID),
         ({"a2": BIG}, INVALID), ({"a3": 0}, INVALID), ({"a3": 24}, INVALID), ({"a4": A + 4}, INVALID),
         ({"a5": None}, INVALID), ({"a3": (1 << 22) + 16}, UNSUPPORTED)]),
-    "gemm_w8a8": (w.w4a16_gemm_w8a8, (W8, BF16, A, A, 4, A, A, None, 8, 32, A, 0), [
+    "gemm_w8a8": (w.w4a16_gemm_w8a8, (W8, BF16, A, A, 4, A, A, None, 8, 32, A, None, 0, 0), [
         ({"a0": 9}, INVALID), ({"a1": 3}, INVALID), ({"a2": None}, INVALID), ({"a2": A + 1}, INVALID),
         ({"a3": A + 4}, INVALID), ({"a4": 0}, INVALID), ({"a4": -1}, INVALID), ({"a5": A + 8}, INVALID),
         ({"a6": None}, INVALID), ({"a7": A}, INVALID), ({"a8": 0}, INVALID), ({"a9": 40}, INVALID),
-        ({"a10": A + 2}, INVALID), ({"a0": G128, "a7": A, "a9": 128}, UNSUPPORTED),
+        ({"a10": A + 2}, INVALID), ({"a11": A + 8, "a12": 64}, INVALID), ({"a0": G128, "a7": A, "a9": 128}, UNSUPPORTED),
         ({"a9": 1 << 17}, UNSUPPORTED), ({"a8": (1 << 26) + 1}, UNSUPPORTED),
         ({"a4": 1 << 30, "a8": 1 << 26}, UNSUPPORTED)]),
     "matmul_w8a8": (w.w4a16_matmul_w8a8, (W8, F16, A, 4, A, A, None, 8, 32, A, A, 144, 0), [
@@ -71,7 +71,10 @@ def test_refused(call, n):
 
 def test_workspace_sizes():
     assert w.w4a16_w8a8_workspace_bytes(W8, 4, 8, 32) == 4 * 32 + 16
-    for bad in [(G128, 4, 8, 128), (W8, 0, 8, 32), (W8, 4, 8, 40), (W8, 4, 0, 32)]:
+    # few columns and a long K: room for the sums of K's parts besides
+    assert w.w4a16_w8a8_workspace_bytes(W8, 512, 4096, 14336) >= 512 * 14336 + 4 * 512 + 2 * 4 * 512 * 4096
+    for bad in [(G128, 4, 8, 128), (W8, 0, 8, 32), (W8, 4, 8, 40), (W8, 4, 0, 32), (W8, 4, 8, 1 << 17),
+                (W8, 1 << 30, 1 << 26, 32)]:
         assert w.w4a16_w8a8_workspace_bytes(*bad) == 0
     assert w.w4a16_expert_sort_workspace_bytes(4096, 2, 8) == 0       # 8192 pairs: one block
     assert w.w4a16_expert_sort_workspace_bytes(8193, 1, 8) > 0

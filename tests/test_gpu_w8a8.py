@@ -69,7 +69,7 @@ def gpu_product(q, a, codes, scales, kind, stream=None):
     N = codes.shape[0]
     y = torch.full((M, N), float("nan"), dtype=dt, device="cuda")
     w.w4a16_gemm_w8a8(W8, act, torch.from_numpy(q).cuda(), torch.from_numpy(a).cuda(), M, codes.cuda(), scales.cuda(), None,
-                      N, K, y, stream)
+                      N, K, y, stream=stream)
     return y
 
 
@@ -147,6 +147,26 @@ def test_gemm_w8a8_wide(M, N, K, kind):
     assert torch.equal(y, gpu_product(q, a, codes, scales, kind))
 
 
+PARTS = [(128, 4096, 14336), (512, 4096, 14352), (300, 2050, 8208), (2000, 1000, 20000), (200, 1030, 14336), (100, 515, 40000)]
+
+
+@pytest.mark.parametrize("M,N,K", PARTS)
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_k_in_parts_is_the_same_product(M, N, K, kind):
+    """Few columns and a long K, with a workspace for the sums of K's parts and without: the same bits."""
+    act, dt = TYPES[kind][:2]
+    q, a = quantized(rows(M, K, dt, 25))
+    codes, scales = weights(N, K, 26)
+    ws, nb = w.alloc_w8a8_workspace(W8, M, N, K)
+    assert nb > (M * K + 4 * M + 4 * M * N)  # there are parts
+    ws.fill_(0x5A)
+    y = torch.full((M, N), float("nan"), dtype=dt, device="cuda")
+    w.w4a16_gemm_w8a8(W8, act, torch.from_numpy(q).cuda(), torch.from_numpy(a).cuda(), M, codes.cuda(), scales.cuda(), None, N, K,
+                      y, ws, nb)
+    assert torch.equal(y, gpu_product(q, a, codes, scales, kind))
+    check(y, product_on_gpu(q, a, codes, scales), kind)
+
+
 @pytest.mark.parametrize("M", [1, 40, 300])
 def test_largest_sums(M):
     """Codes of -128 everywhere at the largest K: sums of 2^14 K, just below 2^31."""
@@ -165,7 +185,7 @@ def test_largest_sums(M):
                                         (2, 4096, 4096, "bf16"), (3, 8200, 144, "bf16"), (37, 1001, 2064, "f16"),
                                         (16, 4096, 2048, "bf16"), (16, 4100, 2048, "bf16"), (9, 61, 4096, "bf16"),
                                         (8, 700, 4608, "f16"), (40, 1300, 1024, "f32"), (16, 200, 1536, "f32"),
-                                        (500, 100, 1040, "bf16"), (17, 33, 48, "f16"), (128, 512, 512, "f32")])
+                                        (500, 100, 1040, "bf16"), (17, 33, 48, "f16"), (512, 2048, 8192, "bf16"), (200, 1030, 14336, "f16"), (128, 512, 512, "f32")])
 def test_matmul_is_the_two_calls(M, N, K, kind):
     act, dt = TYPES[kind][:2]
     x = rows(M, K, dt, 31)

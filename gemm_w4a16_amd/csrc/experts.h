@@ -101,27 +101,50 @@ template <typename T>
 struct alignas(16) Act16 {
     T v[16];
 };
+// (16-bit types: the two halves of a word at once; fold_max joins them.)
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 template <typename T>
 __device__ __forceinline__ uint32_t max_bits(const Act16<T>& x, uint32_t m) {
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(x.v);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) m = max(m, abs_bits(x.v[j]));
+        for (int j = 0; j < 8; ++j)
+            m = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, m),
+                                                                       __builtin_bit_cast(u16x2_t, w[j] & 0x7FFF7FFFu)));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) m = max(m, abs_bits(x.v[j]));
+    }
     return m;
 }
-// The codes by a product with r = 1 / a where that cannot differ: r and the product are each off by at most
-// 2^-24 of their value, so for |v / a| <= 127 the product is within 127.5 * 2^-23 < 1.6e-5 of v / a, and the
-// division's own rounding within 0.8e-5; with the product at least 1e-4 from a midpoint both round to the
-// same code.  Else (and for scales whose reciprocal is not a normal number) the 16 are divided.
+template <typename T>
+__device__ __forceinline__ uint32_t fold_max(uint32_t m) {
+    return sizeof(T) == 2 ? max(m & 0xFFFFu, m >> 16) : m;
+}
+// The codes by a product with r = 1 / a where that cannot differ from the division.  fma(v, r, 1.5 * 2^23) is the
+// product rounded to an integer, ties to even, in its low mantissa bits, whose lowest byte is the code in two's
+// complement.  r is off by at most 2^-24 of its value, so for |v / a| <= 127.1 the product is within 0.8e-5 of
+// v / a, and the division's own rounding within another 0.8e-5; with the product at least 1e-4 from a midpoint
+// both round to the same code.  Else (and for scales whose reciprocal is not a normal number, or NaN) the 16
+// are divided.
 template <typename T>
 __device__ __forceinline__ uint4 codes16(const Act16<T>& x, float a, float r) {
-    uint32_t w[4] = {};
-    float far = a >= 0x1p-100f ? 0.0f : 1.0f;  // largest distance from a code (NaN scales come here too)
+    constexpr float kMagic = 12582912.0f;
+    uint32_t w[4];
+    float far = a >= 0x1p-100f ? 0.0f : 1.0f;  // largest distance from a code
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        const float t = to_f32(x.v[j]) * r, q = rintf(t);
-        far = fmaxf(far, fabsf(t - q));
-        w[j / 4] |= ((uint32_t)(int)fminf(fmaxf(q, -127.0f), 127.0f) & 0xFFu) << (8 * (j % 4));
+    for (int i = 0; i < 4; ++i) {
+        uint32_t b[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float v = to_f32(x.v[4 * i + j]), t = __builtin_fmaf(v, r, kMagic);
+            far = fmaxf(far, fabsf(__builtin_fmaf(v, r, kMagic - t)));
+            b[j] = __float_as_uint(t);
+        }
+        w[i] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0C0C0400u), __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u),
+                                     0x05040100u);
     }
-    if (far > 0.4999f) {
+    if (!(far <= 0.4999f)) {
         w[0] = w[1] = w[2] = w[3] = 0;
 #pragma unroll
         for (int j = 0; j < 16; ++j) w[j / 4] |= code_i8(to_f32(x.v[j]), a) << (8 * (j % 4));
@@ -135,7 +158,7 @@ __device__ __forceinline__ uint4 codes16(const Act16<T>& x, float a, float r) {
 // between the two passes.  red: one word per wave of LDS.
 template <int kThreads, typename T, typename F>
 __device__ __forceinline__ float quantize_row(const T* row, int K, uint32_t* red, F store) {
-    constexpr int kKeep = kThreads == kWave ? 3 : 2;
+    constexpr int kKeep = 2;
     const int tid = kThreads == kWave ? lane_id() : (int)threadIdx.x;
     const Act16<T>* in = reinterpret_cast<const Act16<T>*>(row);
     Act16<T> keep[kKeep];
@@ -149,6 +172,7 @@ __device__ __forceinline__ float quantize_row(const T* row, int K, uint32_t* red
         }
     }
     for (int c = tid + kThreads * kKeep; c < K / 16; c += kThreads) m = max_bits(in[c], m);
+    m = fold_max<T>(m);
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off));
     if constexpr (kThreads > kWave) {
@@ -167,6 +191,11 @@ __device__ __forceinline__ float quantize_row(const T* row, int K, uint32_t* red
     for (int c = tid + kThreads * kKeep; c < K / 16; c += kThreads) store(c, codes16(in[c], a, r));
     return a;
 }
+
+// Whether a wave quantizes a row by itself, not a block: short rows, which would leave threads of a block idle, and
+// enough of them for every SIMD (16384 rows of 1024 fp16 11.6 us against 21.1, 8192 of 2048 bf16 16.5 against
+// 18.2; of 4096 29.5 against 25.1).
+inline bool row_by_wave(int64_t rows, int64_t K) { return K <= 2048 && rows >= 1024; }
 
 // ---- row tiles of experts ----------------------------------------------------------------------
 
@@ -187,49 +216,53 @@ __device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int R
     hi = min(max(offsets[e + 1], lo), R);
 }
 
-// Row tiles of all experts; every wave counts for itself.
-__device__ __forceinline__ int count_expert_tiles(const int32_t* __restrict__ offsets, int E, int R, int tile) {
-    int n = 0;
-    for (int e = lane_id(); e < E; e += kWave) {
-        int lo, hi;
-        expert_rows(offsets, e, R, lo, hi);
-        n += (hi - lo + tile - 1) / tile;
-    }
+// The experts' row tiles, counted expert by expert; every wave counts for itself.  A lane holds one expert of a
+// run of 64, whose tiles are summed over the lanes.
+struct ExpertRun {
+    int lo, hi, end;  // this lane's expert: its rows, and the run's tiles up to and with it
+    int tiles;        // of the run
+};
+__device__ __forceinline__ ExpertRun expert_run(const int32_t* __restrict__ offsets, int E, int e0, int R, int tile) {
+    ExpertRun r{0, 0, 0, 0};
+    const int lane = lane_id();
+    if (e0 + lane < E) expert_rows(offsets, e0 + lane, R, r.lo, r.hi);
+    r.end = (r.hi - r.lo + tile - 1) / tile;
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) n += __shfl_xor(n, off);
-    return __builtin_amdgcn_readfirstlane(n);
+    for (int off = 1; off < kWave; off <<= 1) {
+        const int v = __shfl_up(r.end, off);
+        if (lane >= off) r.end += v;
+    }
+    r.tiles = __builtin_amdgcn_readlane(r.end, kWave - 1);
+    return r;
 }
 
-// The expert and first row of row tile `t`, counting tiles expert by expert.  Each wave looks for
-// itself, 64 experts at a time: the lanes' tile counts are summed over the lanes, and the lane whose
-// range of tiles holds t is the expert.  Every lane returns the same.
-__device__ __forceinline__ ExpertTile find_expert_tile(const int32_t* __restrict__ offsets, int E, int R, int tile, int t) {
-    const int lane = lane_id();
-    int before = 0;  // tiles of the experts so far
-    for (int e0 = 0; e0 < E; e0 += kWave) {
-        int lo = 0, hi = 0;
-        if (e0 + lane < E) expert_rows(offsets, e0 + lane, R, lo, hi);
-        const int n = (hi - lo + tile - 1) / tile;
-        int end = n;  // inclusive sum over the lanes
-#pragma unroll
-        for (int off = 1; off < kWave; off <<= 1) {
-            const int v = __shfl_up(end, off);
-            if (lane >= off) end += v;
-        }
-        const uint64_t past = __ballot(before + end > t);
+// All tiles, given the first run.
+__device__ __forceinline__ int count_expert_tiles(const ExpertRun& first, const int32_t* __restrict__ offsets, int E, int R,
+                                                  int tile) {
+    int n = first.tiles;
+    for (int e0 = kWave; e0 < E; e0 += kWave) n += expert_run(offsets, E, e0, R, tile).tiles;
+    return n;
+}
+
+// The expert and first row of tile `t`, given the first run: the first lane whose tiles end past t is the expert.
+// Every lane returns the same.
+__device__ __forceinline__ ExpertTile find_expert_tile(const ExpertRun& first, const int32_t* __restrict__ offsets, int E,
+                                                       int R, int tile, int t) {
+    ExpertRun run = first;
+    for (int e0 = 0, before = 0;;) {
+        const uint64_t past = __ballot(before + run.end > t);
         if (past != 0) {
             const int src = __ffsll((unsigned long long)past) - 1;
-            const int first = before + __shfl(end - n, src);
-            ExpertTile r;
-            r.expert = __builtin_amdgcn_readfirstlane(e0 + src);
-            r.row0 = __builtin_amdgcn_readfirstlane(__shfl(lo, src) + (t - first) * tile);
-            r.row_end = __builtin_amdgcn_readfirstlane(__shfl(hi, src));
-            if (r.row0 < __builtin_amdgcn_readfirstlane(__shfl(lo, src))) r.row0 = r.row_end;  // offsets that fall
+            const int lo = __builtin_amdgcn_readlane(run.lo, src), hi = __builtin_amdgcn_readlane(run.hi, src);
+            const int start = before + __builtin_amdgcn_readlane(run.end, src) - (hi - lo + tile - 1) / tile;
+            ExpertTile r{e0 + src, lo + (t - start) * tile, hi};
+            if (r.row0 < lo) r.row0 = hi;  // offsets that fall
             return r;
         }
-        before += __shfl(end, kWave - 1);
+        before += run.tiles, e0 += kWave;
+        if (e0 >= E) return ExpertTile{0, 0, 0};
+        run = expert_run(offsets, E, e0, R, tile);
     }
-    return ExpertTile{0, 0, 0};
 }
 
 }  // namespace w4a16

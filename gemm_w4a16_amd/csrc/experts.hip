@@ -211,22 +211,30 @@ __global__ __launch_bounds__(256) void gather_kernel(const U* __restrict__ x, in
     }
 }
 
-template <typename T>
+// kWaves waves per token, as in the quantizer.
+template <typename T, int kWaves>
 __global__ __launch_bounds__(256) void gather_i8_kernel(const T* __restrict__ x, int64_t Tn, int topk,
                                                         const int32_t* __restrict__ pos, int K, int8_t* __restrict__ xq,
                                                         float* __restrict__ ascale) {
+    constexpr int kTokens = 4 / kWaves, kThreads = 64 * kWaves;
     __shared__ uint32_t red[4];
-    __shared__ int32_t rows[kMaxExperts];  // the token's, fetched beside its activations (topk <= kMaxExperts)
+    __shared__ int32_t all_rows[kTokens][kMaxExperts];  // a token's, fetched beside its activations (topk <= kMaxExperts)
     const int64_t P = Tn * topk;
-    for (int64_t t = blockIdx.x; t < Tn; t += gridDim.x) {
-        __syncthreads();  // rows may still be read
-        for (int j = threadIdx.x; j < topk; j += 256) rows[j] = (int32_t)pair_row(pos, t * topk + j, P);
-        const float a = quantize_row<256>(x + t * K, K, red, [&](int c, uint4 q) __attribute__((always_inline)) {
+    const int tid = threadIdx.x % kThreads;
+    int32_t* rows = all_rows[threadIdx.x / kThreads];
+    for (int64_t t0 = (int64_t)blockIdx.x * kTokens; t0 < Tn; t0 += (int64_t)gridDim.x * kTokens) {
+        const int64_t t = kWaves == 1 ? t0 + wave_id() : t0;
+        if (kWaves == 1 && t >= Tn) continue;
+        if constexpr (kWaves > 1) __syncthreads();  // rows may still be read
+        for (int j = tid; j < topk; j += kThreads) rows[j] = (int32_t)pair_row(pos, t * topk + j, P);
+        if constexpr (kWaves == 1) wave_lds_sync();
+        const float a = quantize_row<kThreads>(x + t * K, K, red, [&](int c, uint4 q) __attribute__((always_inline)) {
             for (int j = 0; j < topk; ++j)
                 if (rows[j] >= 0) *reinterpret_cast<uint4*>(xq + (int64_t)rows[j] * K + 16 * c) = q;
         });
-        for (int j = threadIdx.x; j < topk; j += 256)
+        for (int j = tid; j < topk; j += kThreads)
             if (rows[j] >= 0) ascale[rows[j]] = a;
+        if constexpr (kWaves == 1) wave_lds_sync();
     }
 }
 
@@ -424,9 +432,13 @@ hipError_t launch_expert_gather_i8(int dtype, const void* x, int64_t T, int64_t 
                                    int8_t* xq, float* ascale, hipStream_t stream) {
     return with_act_type(dtype, [&](auto t) {
         using E = decltype(t);
-        hipLaunchKernelGGL((gather_i8_kernel<E>), row_grid(T), dim3(256), 0, stream, static_cast<const E*>(x), T, (int)topk,
-                           pos, (int)K, xq, ascale);
-        return hipGetLastError();
+        auto run = [&](auto waves) {
+            constexpr int kWaves = decltype(waves)::value;
+            hipLaunchKernelGGL((gather_i8_kernel<E, kWaves>), row_grid(ceil_div(T, 4 / kWaves)), dim3(256), 0, stream,
+                               static_cast<const E*>(x), T, (int)topk, pos, (int)K, xq, ascale);
+            return hipGetLastError();
+        };
+        return row_by_wave(T, K) ? run(std::integral_constant<int, 1>{}) : run(std::integral_constant<int, 4>{});
     });
 }
 

@@ -170,7 +170,7 @@ hipError_t launch_matmul_w8a8(int dtype, const void* x, int64_t M, const int8_t*
 
 // Tokens sorted by expert and back (P = T * topk pairs); widths in elements of dtype.
 constexpr int64_t kMaxExperts = 512;    // the sort keeps a count per wave and expert in LDS
-constexpr int64_t kSortOneBlock = 8192;  // pairs that one block sorts in one launch, with no workspace
+constexpr int64_t kSortOneBlock = 4096;  // pairs that one block sorts in one launch, with no workspace
 size_t expert_sort_workspace_bytes(int64_t P, int64_t E);
 hipError_t launch_expert_sort(const void* ids, int id_bits, int64_t P, int64_t E, int32_t* offsets, int32_t* pos,
                               int32_t* src, int32_t* ws, hipStream_t stream);

@@ -26,15 +26,19 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
 // ---- activation quantization ------------------------------------------------------------------
 
-template <typename T>
+// kWaves waves per row (4, or 1: four rows a block).
+template <typename T, int kWaves>
 __global__ __launch_bounds__(256) void quant_rows_i8_kernel(const T* __restrict__ x, int64_t M, int K,
                                                             int8_t* __restrict__ xq, float* __restrict__ ascale) {
+    constexpr int kRows = 4 / kWaves;
     __shared__ uint32_t red[4];
-    for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
-        const float a = quantize_row<256>(x + m * K, K, red, [&](int c, uint4 q) __attribute__((always_inline)) {
+    for (int64_t m0 = (int64_t)blockIdx.x * kRows; m0 < M; m0 += (int64_t)gridDim.x * kRows) {
+        const int64_t m = kWaves == 1 ? m0 + wave_id() : m0;
+        if (kWaves == 1 && m >= M) continue;
+        const float a = quantize_row<64 * kWaves>(x + m * K, K, red, [&](int c, uint4 q) __attribute__((always_inline)) {
             *reinterpret_cast<uint4*>(xq + m * K + 16 * c) = q;
         });
-        if (threadIdx.x == 0) ascale[m] = a;
+        if (lane_id() == 0) ascale[m] = a;
     }
 }
 
@@ -130,7 +134,11 @@ __global__ __launch_bounds__(64 * C::NW) void w8a8_tile_kernel(const void* __res
     int K = stride, k0 = 0;  // kSums: of this block's part of K
     {
         int m_tiles = (M + BM - 1) / BM;
-        if constexpr (kExperts) m_tiles = count_expert_tiles(offsets, E, M, BM);
+        ExpertRun first;
+        if constexpr (kExperts) {
+            first = expert_run(offsets, E, 0, M, BM);
+            m_tiles = count_expert_tiles(first, offsets, E, M, BM);
+        }
         const int total = kSums ? gridDim.x : m_tiles * n_tiles, b = blockIdx.x;
         if (b >= total) return;
         const int xcd = b & 7, each = total >> 3, rest = total & 7;
@@ -147,7 +155,7 @@ __global__ __launch_bounds__(64 * C::NW) void w8a8_tile_kernel(const void* __res
         const int tm = g * group + in - tn * rows;
         row0 = tm * BM;
         if constexpr (kExperts) {
-            const ExpertTile t = find_expert_tile(offsets, E, M, BM, tm);
+            const ExpertTile t = find_expert_tile(first, offsets, E, M, BM, tm);
             if (t.row0 >= t.row_end) return;
             row0 = t.row0, row_end = t.row_end, expert = t.expert;
         }
@@ -603,12 +611,16 @@ auto fused_launch(const Product& p) -> hipError_t (*)(const Product&, TO*) {
 
 hipError_t launch_quant_rows_i8(int dtype, const void* x, int64_t M, int64_t K, int8_t* xq, float* ascale,
                                 hipStream_t stream) {
-    const dim3 grid((unsigned)std::min<int64_t>(M, kMaxGridBlocks));
     return with_act_type(dtype, [&](auto t) {
         using T = decltype(t);
-        hipLaunchKernelGGL((quant_rows_i8_kernel<T>), grid, dim3(256), 0, stream, static_cast<const T*>(x), M, (int)K, xq,
-                           ascale);
-        return hipGetLastError();
+        auto run = [&](auto waves) {
+            constexpr int kWaves = decltype(waves)::value;
+            const dim3 grid((unsigned)std::min<int64_t>((M + 4 / kWaves - 1) / (4 / kWaves), kMaxGridBlocks));
+            hipLaunchKernelGGL((quant_rows_i8_kernel<T, kWaves>), grid, dim3(256), 0, stream, static_cast<const T*>(x), M,
+                               (int)K, xq, ascale);
+            return hipGetLastError();
+        };
+        return row_by_wave(M, K) ? run(std::integral_constant<int, 1>{}) : run(std::integral_constant<int, 4>{});
     });
 }
 

@@ -365,7 +365,7 @@ size_t w4a16_w8a8_workspace_bytes(w4a16_format_t fmt, int64_t M, int64_t N, int6
 /* Largest E and topk the experts' calls accept. */
 int64_t w4a16_max_experts(void);
 
-/* Bytes of workspace w4a16_expert_sort needs (0 up to 8192 pairs, and for bad sizes). */
+/* Bytes of workspace w4a16_expert_sort needs (0 up to 4096 pairs, and for bad sizes). */
 size_t w4a16_expert_sort_workspace_bytes(int64_t T, int64_t topk, int64_t E);
 
 /* The sorted order.  ids [T][topk]: int32 (id_bits 32) or int64 (id_bits 64).  Writes

@@ -76,8 +76,8 @@ def test_workspace_sizes():
     for bad in [(G128, 4, 8, 128), (W8, 0, 8, 32), (W8, 4, 8, 40), (W8, 4, 0, 32), (W8, 4, 8, 1 << 17),
                 (W8, 1 << 30, 1 << 26, 32)]:
         assert w.w4a16_w8a8_workspace_bytes(*bad) == 0
-    assert w.w4a16_expert_sort_workspace_bytes(4096, 2, 8) == 0       # 8192 pairs: one block
-    assert w.w4a16_expert_sort_workspace_bytes(8193, 1, 8) > 0
+    assert w.w4a16_expert_sort_workspace_bytes(2048, 2, 8) == 0       # 4096 pairs: one block
+    assert w.w4a16_expert_sort_workspace_bytes(4097, 1, 8) > 0
     assert w.w4a16_expert_sort_workspace_bytes(8193, 1, w.w4a16_max_experts() + 1) == 0
 
 

@@ -59,7 +59,7 @@ def gpu_sort(ids, E, bits=32, src=True):
 
 
 SORTS = [(1, 1, 1), (1, 2, 8), (4, 2, 8), (7, 3, 5), (64, 1, 64), (65, 8, 64), (1000, 8, 128), (333, 3, 512), (1024, 8, 60),
-         (8192, 1, 3), (8193, 1, 3), (2048, 1, 512), (1025, 1, 2), (4097, 2, 512), (5000, 7, 33), (70000, 4, 256), (3000, 100, 16)]
+         (4096, 1, 3), (4097, 1, 3), (8192, 1, 3), (2048, 1, 512), (1025, 1, 2), (4097, 2, 512), (5000, 7, 33), (70000, 4, 256), (3000, 100, 16)]
 
 
 @pytest.mark.parametrize("T,topk,E", SORTS)
@@ -117,7 +117,8 @@ def test_gather(T, topk, E, N, kind):
     assert (xs[n:] == 7).all()  # rows behind the experts' are left as they were
 
 
-@pytest.mark.parametrize("T,topk,E,K", [(1, 1, 1, 16), (4, 2, 8, 4096), (37, 3, 5, 1008), (200, 8, 64, 2048), (9, 20, 30, 48)])
+@pytest.mark.parametrize("T,topk,E,K", [(1, 1, 1, 16), (4, 2, 8, 4096), (37, 3, 5, 1008), (200, 8, 64, 2048), (9, 20, 30, 48), (1500, 3, 7, 1008),
+                                        (1026, 2, 4, 4096), (1030, 2, 5, 4112)])
 @pytest.mark.parametrize("kind", list(TYPES))
 def test_gather_i8(T, topk, E, K, kind):
     act, dt = TYPES[kind][:2]

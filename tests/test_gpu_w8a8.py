@@ -74,7 +74,8 @@ def gpu_product(q, a, codes, scales, kind, stream=None):
 
 
 @pytest.mark.parametrize("kind", list(TYPES))
-@pytest.mark.parametrize("M,K", [(1, 16), (5, 48), (37, 2064), (300, 4096), (6, 20000), (1, 8192)])
+@pytest.mark.parametrize("M,K", [(1, 16), (5, 48), (37, 2064), (300, 4096), (6, 20000), (1, 8192), (1500, 1040),
+                                 (1027, 4096), (1026, 4112)])
 def test_quantize_rows_bit_exact(M, K, kind):
     act, dt = TYPES[kind][:2]
     x = rows(M, K, dt, 11)

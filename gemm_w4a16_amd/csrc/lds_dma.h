@@ -27,6 +27,10 @@ __device__ __forceinline__ void dma16(uint32_t voff, const void* sbase, uint32_t
                      "n"(kImm)
                      : "memory", "m0", "scc");
 }
+// The same, non-temporal: data read once.
+__device__ __forceinline__ void dma16_once(uint32_t voff, const void* sbase, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(voff), "s"(sbase), "s"(lds) : "memory", "m0");
+}
 template <int kImm = 0>
 __device__ __forceinline__ void dma4(uint32_t voff, const void* sbase, uint32_t lds) {
     if constexpr (kImm == 0)

@@ -96,6 +96,14 @@ __device__ __forceinline__ float scaled_sum(int32_t sum, float sn, float am) {
     return v;
 }
 
+// Weights that one row tile reads (a tile of at most kOnceRows rows holds them all) and that take more than a
+// quarter of the Infinity Cache's 256 MiB, so that they would hardly be there at the next call, are copied
+// past it (`once`): eight matrices of 14336 x 4096 for 16 rows take 63.4 us against 71.5, two of them 23.4
+// against 26.4.  One of them alone (56 MiB), called again while the cache holds it, takes 11.8 us so against
+// 10.5; called when it does not, 12.3 against 14.1.
+constexpr int kOnceRows = 64;
+constexpr double kOnceBytes = 64 << 20;
+
 // What x is: int8 rows; int8 rows sorted by expert; or a few rows of activations (TO) that every block
 // quantizes for itself (kFused: no other launch, and x stays in LDS whole, behind the ring).
 enum XKind { kRows, kExpertRows, kFused };
@@ -115,7 +123,7 @@ __global__ __launch_bounds__(64 * C::NW) void w8a8_tile_kernel(const void* __res
                                                                const int8_t* __restrict__ codes,
                                                                const float* __restrict__ scales, TO* __restrict__ y, int M,
                                                                int N, int stride, const int32_t* __restrict__ offsets, int E,
-                                                               int n_tiles, int group, int split_k) {
+                                                               int n_tiles, int group, int split_k, int once) {
     constexpr int TM = C::TM, TN = C::TN, R = C::R, U = C::U, BM = C::BM, BN = C::BN, CW = C::kWaveCopies;
     constexpr int kTileCopies = C::kTileBytes / 1024 / U;  // of a unit's part of one k-tile
     constexpr bool kExperts = kX == kExpertRows, kFuse = kX == kFused, kSums = std::is_same_v<TO, int32_t>;
@@ -195,7 +203,11 @@ __global__ __launch_bounds__(64 * C::NW) void w8a8_tile_kernel(const void* __res
             off -= (uint32_t)max(16 * chunk - (left - 16), 0);
         }
         if (t >= T) base = wbase, off = 0;
-        dma16(off, base, lds0 + (uint32_t)(slot * C::kUnitBytes + 1024 * j));
+        const uint32_t lds = lds0 + (uint32_t)(slot * C::kUnitBytes + 1024 * j);
+        if (BM <= kOnceRows && once && is_w(part, jj))
+            dma16_once(off, base, lds);
+        else
+            dma16(off, base, lds);
     };
 
     // fragment of row tile rt at k-step ks of a k-tile: chunk 4 ks + kg of row 16 rt + l16 (the unit's own
@@ -439,17 +451,29 @@ bool fits_grid(int64_t M, int64_t N, bool experts, int64_t E) {
     return launch_blocks<C>(M, N, experts, E) < ((int64_t)1 << 31) / (64 * C::NW);  // the grid's threads
 }
 
+// The experts that can have rows, and the rows of each if they share them evenly.
+struct Share {
+    int64_t experts, rows;
+    Share(int64_t M, int64_t E) : experts(std::min(M, E)), rows((M + experts - 1) / experts) {}
+};
+template <typename C>
+bool weights_once(int64_t M, int64_t N, int64_t K, int64_t E) {
+    const Share s(M, E);
+    return C::BM <= kOnceRows && s.rows <= C::BM && (double)s.experts * (double)N * (double)K >= kOnceBytes;
+}
+
 template <typename C, typename TO>
 hipError_t launch_tiles(const Product& p, TO* y) {
     const int64_t tn = (p.N + C::BN - 1) / C::BN;
     const dim3 grid((unsigned)launch_blocks<C>(p.M, p.N, p.offsets != nullptr, p.E)), block(64 * C::NW);
+    const int once = weights_once<C>(p.M, p.N, p.K, p.E);
     constexpr int kGroup = C::BM < 256 ? 1024 / C::BM : 4;  // row tiles walked together: about 1024 rows
     if (p.offsets)
         hipLaunchKernelGGL((w8a8_tile_kernel<TO, kExpertRows, C>), grid, block, 0, p.stream, p.x, p.ascale, p.codes, p.scales, y,
-                           (int)p.M, (int)p.N, (int)p.K, p.offsets, (int)p.E, (int)tn, kGroup, 0);
+                           (int)p.M, (int)p.N, (int)p.K, p.offsets, (int)p.E, (int)tn, kGroup, 0, once);
     else
         hipLaunchKernelGGL((w8a8_tile_kernel<TO, kRows, C>), grid, block, 0, p.stream, p.x, p.ascale, p.codes, p.scales, y,
-                           (int)p.M, (int)p.N, (int)p.K, nullptr, 1, (int)tn, kGroup, 0);
+                           (int)p.M, (int)p.N, (int)p.K, nullptr, 1, (int)tn, kGroup, 0, once);
     return hipGetLastError();
 }
 
@@ -461,7 +485,7 @@ hipError_t launch_parts(const Product& p, TO* y, int parts) {
     const dim3 grid((unsigned)(launch_blocks<C>(p.M, p.N, false, 1) * parts)), block(64 * C::NW);
     constexpr int kGroup = C::BM < 256 ? 1024 / C::BM : 4;
     hipLaunchKernelGGL((w8a8_tile_kernel<int32_t, kRows, C>), grid, block, 0, p.stream, p.x, nullptr, p.codes, nullptr, p.sums,
-                       (int)p.M, (int)p.N, (int)p.K, nullptr, 1, (int)tn, kGroup, (int)split);
+                       (int)p.M, (int)p.N, (int)p.K, nullptr, 1, (int)tn, kGroup, (int)split, 0);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     auto join = [&](auto v) {
         constexpr int V = decltype(v)::value;
@@ -479,18 +503,21 @@ constexpr double kJoinUs = 3.0, kJoinBytesPerUs = 5e6;
 // The tilings, and what one costs.  A block takes `us_ktile` for each 128 of K (measured where every block has
 // a CU to itself: 4096 columns, K = 4096 and 14336) and `us_block` besides; `blocks` of them fit a CU,
 // which runs them at the same rate in all.  Few rows wait for the weights instead, which arrive at `tbs` TB/s
-// (measured on eight matrices of 14336 x 4096 and 64 of 1024 x 2048).  The choice by this is within 2% of
+// (measured on eight matrices of 14336 x 4096 and 64 of 1024 x 2048; any tiling at 7.4 where they are read once).  The choice by this is within 2% of
 // the fastest in 31 of 33 shapes of 1 to 2048 rows of one matrix, within 13% in the others; of experts,
 // whose row counts are not known here, within 10%.
 struct Cost {
     double us_ktile, us_block;
     int blocks;
     double tbs;
-    double us(int64_t tiles, int64_t K, double weight_bytes) const {
-        const double waves = (double)tiles / 256, up = std::ceil(waves);
+    double us(int64_t tiles, int64_t K, double weight_bytes, bool once) const {
+        const double waves = (double)tiles / 256, up = std::ceil(waves), slots = 256.0 * blocks;
         const double rounds = blocks == 1 ? up : waves <= 1 ? 1.0 : std::max(waves, 0.9 * up);
         const double work = rounds * ((double)((K + 127) / 128) * us_ktile + us_block);
-        return 2.6 + std::max(work, weight_bytes / tbs * 1e-6) + 0.03 * work;  // (of two that wait, the idler one)
+        // a stream of more blocks than run at once ends with some of the GPU idle: half a round on average
+        const double tail = tiles > slots ? 1.0 + 0.5 * slots / (double)tiles : 1.0;
+        const double stream = weight_bytes / (once ? 7.4 : tbs) * 1e-6 * tail;
+        return 2.6 + std::max(work, stream) + 0.03 * work;  // (of two that wait, the idler one)
     }
 };
 using T256x256 = Tiling<2, 4, 1, 8, 4, 5, 2>;
@@ -525,15 +552,15 @@ void each_tiling(F f) {
 size_t sums_bytes(int64_t M, int64_t N, int parts) { return parts > 1 ? (size_t)parts * (size_t)M * (size_t)N * 4 : 0; }
 
 Plan plan_product(int64_t M, int64_t N, int64_t K, bool experts, int64_t E, size_t room) {
-    // an even share of the rows for each expert that can have any
-    const int64_t used = std::min(M, E), each = (M + used - 1) / used, ktiles = (K + 127) / 128;
-    const double weight_bytes = (double)used * (double)N * (double)K;
+    const Share share(M, E);
+    const int64_t ktiles = (K + 127) / 128;
+    const double weight_bytes = (double)share.experts * (double)N * (double)K;
     Plan plan{-1, 1};
     double least = 0;
     each_tiling([&](int i, auto tiling, Cost cost) {
         using C = decltype(tiling);
         if (!fits_grid<C>(M, N, experts, E)) return;
-        const int64_t tiles = used * ((each + C::BM - 1) / C::BM) * ((N + C::BN - 1) / C::BN);
+        const int64_t tiles = share.experts * ((share.rows + C::BM - 1) / C::BM) * ((N + C::BN - 1) / C::BN);
         for (int parts = 1; parts <= 8; parts *= 2) {
             const int64_t part = (ktiles + parts - 1) / parts;
             if (parts > 1 && (experts || C::WK > 1 || C::BM * C::BN < 64 * 64 || tiles * parts > 512 || part < 16 ||
@@ -541,7 +568,7 @@ Plan plan_product(int64_t M, int64_t N, int64_t K, bool experts, int64_t E, size
                 break;
             // the parts' sums are written and read once, and joined by a second launch
             const double join = parts > 1 ? kJoinUs + 2.0 * sums_bytes(M, N, parts) / kJoinBytesPerUs : 0.0;
-            const double us = cost.us(tiles * parts, part * 128, weight_bytes) + join;
+            const double us = cost.us(tiles * parts, part * 128, weight_bytes, weights_once<C>(M, N, K, E)) + join;
             if (plan.tiling < 0 || us < least) plan = Plan{i, parts}, least = us;
         }
     });
@@ -577,7 +604,7 @@ hipError_t launch_fused_tiles(const Product& p, TO* y) {
     const int64_t tn = (p.N + C::BN - 1) / C::BN, tm = (p.M + 15) / 16;
     hipLaunchKernelGGL((w8a8_tile_kernel<TO, kFused, C>), dim3((unsigned)(tn * tm)), dim3(64 * C::NW),
                        fused_bytes<TO>(p, C::WK), p.stream, p.x, nullptr, p.codes, p.scales, y, (int)p.M, (int)p.N, (int)p.K,
-                       nullptr, 1, (int)tn, 64, 0);
+                       nullptr, 1, (int)tn, 64, 0, p.M <= 16 && (double)p.N * (double)p.K >= kOnceBytes);
     return hipGetLastError();
 }
 using F16x32 = Tiling<1, 2, 2, 1, 1, 4, 1, false>;

@@ -138,19 +138,14 @@ w4a16_status_t check_pairs(int64_t T, int64_t topk, int64_t width) {
     return W4A16_OK;
 }
 
-// The W8A8 workspace: the sums of K's parts, then the codes of x and its row scales (matmul_w8a8), each
-// 16-byte aligned.
+// The W8A8 workspace: the codes of x and its row scales (matmul_w8a8 needs these), then room for the sums of
+// K's parts, each 16-byte aligned.
 struct W8A8Workspace {
-    size_t xq, ascale, total;
+    size_t ascale, needed, sums;
+    W8A8Workspace(int64_t M, int64_t K)
+        : ascale((size_t)M * (size_t)K),  // K % 16 == 0
+          needed(ascale + (size_t)M * 4), sums((needed + 15) & ~(size_t)15) {}
 };
-W8A8Workspace w8a8_workspace(int64_t M, int64_t N, int64_t K) {
-    auto a16 = [](size_t b) { return (b + 15) & ~(size_t)15; };
-    W8A8Workspace w;
-    w.xq = a16(w4a16::w8a8_sums_bytes(M, N, K));
-    w.ascale = w.xq + (size_t)M * (size_t)K;  // K % 16 == 0
-    w.total = w.ascale + (size_t)M * 4;
-    return w;
-}
 
 // ---- The no-allocation entry point's scratch buffer -------------------------------------------
 // Split-K partial sums of the large-M GEMM for callers that cannot allocate a workspace.  One
@@ -557,7 +552,9 @@ size_t w4a16_w8a8_workspace_bytes(w4a16_format_t fmt, int64_t M, int64_t N, int6
     if (fmt != W4A16_FMT_W8_ROW_FP32 || check_shape(fmt, N, K) != W4A16_OK || M <= 0 || M > kMaxDim || K > kMaxKInt8 ||
         !w4a16::w8a8_fits_grid(M, N, false, 1))
         return 0;
-    return w8a8_workspace(M, N, K).total;
+    const W8A8Workspace w(M, K);
+    const size_t sums = w4a16::w8a8_sums_bytes(M, N, K);
+    return sums > 0 ? w.sums + sums : w.needed;
 }
 
 w4a16_status_t w4a16_matmul_w8a8(w4a16_format_t fmt, w4a16_dtype_t act, const void* x, int64_t M, const void* codes,
@@ -566,14 +563,15 @@ w4a16_status_t w4a16_matmul_w8a8(w4a16_format_t fmt, w4a16_dtype_t act, const vo
     if (w4a16_status_t st = check_w8a8(fmt, act, M, codes, scales, mins, N, K, y); st != W4A16_OK) return st;
     if (!aligned16(x) || !aligned16(workspace)) return W4A16_ERR_INVALID;
     if (!w4a16::w8a8_fits_grid(M, N, false, 1)) return W4A16_ERR_UNSUPPORTED;
-    const W8A8Workspace w = w8a8_workspace(M, N, K);
-    if (workspace_bytes < w.total) return W4A16_ERR_INVALID;
+    const W8A8Workspace w(M, K);
+    if (workspace_bytes < w.needed) return W4A16_ERR_INVALID;
     char* base = static_cast<char*>(workspace);
+    const size_t room = workspace_bytes > w.sums ? workspace_bytes - w.sums : 0;
     w4a16::clear_stale_error();
     return from_hip(w4a16::launch_matmul_w8a8((int)act, x, M, static_cast<const int8_t*>(codes),
-                                              static_cast<const float*>(scales), N, K, y,
-                                              reinterpret_cast<int8_t*>(base + w.xq), reinterpret_cast<float*>(base + w.ascale),
-                                              reinterpret_cast<int32_t*>(base), w.xq, stream));
+                                              static_cast<const float*>(scales), N, K, y, reinterpret_cast<int8_t*>(base),
+                                              reinterpret_cast<float*>(base + w.ascale),
+                                              reinterpret_cast<int32_t*>(room > 0 ? base + w.sums : nullptr), room, stream));
 }
 
 w4a16_status_t w4a16_gemm_w8a8_experts(w4a16_format_t fmt, w4a16_dtype_t out, const int8_t* xq, const float* ascale,

@@ -98,7 +98,7 @@ __device__ __forceinline__ float scaled_sum(int32_t sum, float sn, float am) {
 
 // Weights that one row tile reads (a tile of at most kOnceRows rows holds them all) and that take more than a
 // quarter of the Infinity Cache's 256 MiB, so that they would hardly be there at the next call, are copied
-// past it (`once`): eight matrices of 14336 x 4096 for 16 rows take 63.4 us against 71.5, two of them 23.4
+// past it (kOnce): eight matrices of 14336 x 4096 for 16 rows take 63.4 us against 71.5, two of them 23.4
 // against 26.4.  One of them alone (56 MiB), called again while the cache holds it, takes 11.8 us so against
 // 10.5; called when it does not, 12.3 against 14.1.
 constexpr int kOnceRows = 64;
@@ -118,12 +118,12 @@ constexpr int64_t fused_raw_bytes(int64_t M, int64_t K, int element) {
 }
 
 // TO int32_t: y takes the sums of one part of K (split_k columns of it, a multiple of 128) per block, [parts][M][N].
-template <typename TO, XKind kX, typename C>
+template <typename TO, XKind kX, typename C, bool kOnce>
 __global__ __launch_bounds__(64 * C::NW) void w8a8_tile_kernel(const void* __restrict__ x, const float* __restrict__ ascale,
                                                                const int8_t* __restrict__ codes,
                                                                const float* __restrict__ scales, TO* __restrict__ y, int M,
                                                                int N, int stride, const int32_t* __restrict__ offsets, int E,
-                                                               int n_tiles, int group, int split_k, int once) {
+                                                               int n_tiles, int group, int split_k) {
     constexpr int TM = C::TM, TN = C::TN, R = C::R, U = C::U, BM = C::BM, BN = C::BN, CW = C::kWaveCopies;
     constexpr int kTileCopies = C::kTileBytes / 1024 / U;  // of a unit's part of one k-tile
     constexpr bool kExperts = kX == kExpertRows, kFuse = kX == kFused, kSums = std::is_same_v<TO, int32_t>;
@@ -204,7 +204,7 @@ __global__ __launch_bounds__(64 * C::NW) void w8a8_tile_kernel(const void* __res
         }
         if (t >= T) base = wbase, off = 0;
         const uint32_t lds = lds0 + (uint32_t)(slot * C::kUnitBytes + 1024 * j);
-        if (BM <= kOnceRows && once && is_w(part, jj))
+        if (kOnce && is_w(part, jj))
             dma16_once(off, base, lds);
         else
             dma16(off, base, lds);
@@ -454,11 +454,10 @@ bool fits_grid(int64_t M, int64_t N, bool experts, int64_t E) {
 // The experts that can have rows, and the rows of each if they share them evenly.
 struct Share {
     int64_t experts, rows;
-    Share(int64_t M, int64_t E) : experts(std::min(M, E)), rows((M + experts - 1) / experts) {}
+    Share(int64_t M, int64_t E) : experts(std::min(M, E)), rows(E == 1 ? M : (M + experts - 1) / experts) {}
 };
 template <typename C>
-bool weights_once(int64_t M, int64_t N, int64_t K, int64_t E) {
-    const Share s(M, E);
+bool weights_once(const Share& s, int64_t N, int64_t K) {
     return C::BM <= kOnceRows && s.rows <= C::BM && (double)s.experts * (double)N * (double)K >= kOnceBytes;
 }
 
@@ -466,15 +465,21 @@ template <typename C, typename TO>
 hipError_t launch_tiles(const Product& p, TO* y) {
     const int64_t tn = (p.N + C::BN - 1) / C::BN;
     const dim3 grid((unsigned)launch_blocks<C>(p.M, p.N, p.offsets != nullptr, p.E)), block(64 * C::NW);
-    const int once = weights_once<C>(p.M, p.N, p.K, p.E);
     constexpr int kGroup = C::BM < 256 ? 1024 / C::BM : 4;  // row tiles walked together: about 1024 rows
-    if (p.offsets)
-        hipLaunchKernelGGL((w8a8_tile_kernel<TO, kExpertRows, C>), grid, block, 0, p.stream, p.x, p.ascale, p.codes, p.scales, y,
-                           (int)p.M, (int)p.N, (int)p.K, p.offsets, (int)p.E, (int)tn, kGroup, 0, once);
-    else
-        hipLaunchKernelGGL((w8a8_tile_kernel<TO, kRows, C>), grid, block, 0, p.stream, p.x, p.ascale, p.codes, p.scales, y,
-                           (int)p.M, (int)p.N, (int)p.K, nullptr, 1, (int)tn, kGroup, 0, once);
-    return hipGetLastError();
+    auto launch = [&](auto once) {
+        constexpr bool kOnce = decltype(once)::value;
+        if (p.offsets)
+            hipLaunchKernelGGL((w8a8_tile_kernel<TO, kExpertRows, C, kOnce>), grid, block, 0, p.stream, p.x, p.ascale, p.codes,
+                               p.scales, y, (int)p.M, (int)p.N, (int)p.K, p.offsets, (int)p.E, (int)tn, kGroup, 0);
+        else
+            hipLaunchKernelGGL((w8a8_tile_kernel<TO, kRows, C, kOnce>), grid, block, 0, p.stream, p.x, p.ascale, p.codes,
+                               p.scales, y, (int)p.M, (int)p.N, (int)p.K, nullptr, 1, (int)tn, kGroup, 0);
+        return hipGetLastError();
+    };
+    if constexpr (C::BM <= kOnceRows) {
+        if (weights_once<C>(Share(p.M, p.E), p.N, p.K)) return launch(std::true_type{});
+    }
+    return launch(std::false_type{});
 }
 
 // K in `parts`, one launch for the sums and one that joins them.
@@ -484,8 +489,8 @@ hipError_t launch_parts(const Product& p, TO* y, int parts) {
     const int64_t split = (p.K + 128 * parts - 1) / (128 * parts) * 128;
     const dim3 grid((unsigned)(launch_blocks<C>(p.M, p.N, false, 1) * parts)), block(64 * C::NW);
     constexpr int kGroup = C::BM < 256 ? 1024 / C::BM : 4;
-    hipLaunchKernelGGL((w8a8_tile_kernel<int32_t, kRows, C>), grid, block, 0, p.stream, p.x, nullptr, p.codes, nullptr, p.sums,
-                       (int)p.M, (int)p.N, (int)p.K, nullptr, 1, (int)tn, kGroup, (int)split, 0);
+    hipLaunchKernelGGL((w8a8_tile_kernel<int32_t, kRows, C, false>), grid, block, 0, p.stream, p.x, nullptr, p.codes, nullptr, p.sums,
+                       (int)p.M, (int)p.N, (int)p.K, nullptr, 1, (int)tn, kGroup, (int)split);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     auto join = [&](auto v) {
         constexpr int V = decltype(v)::value;
@@ -561,14 +566,16 @@ Plan plan_product(int64_t M, int64_t N, int64_t K, bool experts, int64_t E, size
         using C = decltype(tiling);
         if (!fits_grid<C>(M, N, experts, E)) return;
         const int64_t tiles = share.experts * ((share.rows + C::BM - 1) / C::BM) * ((N + C::BN - 1) / C::BN);
-        for (int parts = 1; parts <= 8; parts *= 2) {
-            const int64_t part = (ktiles + parts - 1) / parts;
-            if (parts > 1 && (experts || C::WK > 1 || C::BM * C::BN < 64 * 64 || tiles * parts > 512 || part < 16 ||
-                              part * (parts - 1) >= ktiles || sums_bytes(M, N, parts) > room))
+        const bool once = weights_once<C>(share, N, K);
+        const int most = experts || C::WK > 1 || C::BM * C::BN < 64 * 64 || room == 0 || ktiles < 32 ? 0 : 3;
+        for (int log = 0; log <= most; ++log) {  // (host time counts here: a launch is 3.4 us)
+            const int parts = 1 << log;
+            const int64_t part = (ktiles + parts - 1) >> log;
+            if (parts > 1 && (tiles * parts > 512 || part < 16 || part * (parts - 1) >= ktiles || sums_bytes(M, N, parts) > room))
                 break;
             // the parts' sums are written and read once, and joined by a second launch
             const double join = parts > 1 ? kJoinUs + 2.0 * sums_bytes(M, N, parts) / kJoinBytesPerUs : 0.0;
-            const double us = cost.us(tiles * parts, part * 128, weight_bytes, weights_once<C>(M, N, K, E)) + join;
+            const double us = cost.us(tiles * parts, part * 128, weight_bytes, once) + join;
             if (plan.tiling < 0 || us < least) plan = Plan{i, parts}, least = us;
         }
     });
@@ -602,10 +609,13 @@ size_t fused_bytes(const Product& p, int wk) {
 template <typename C, typename TO>
 hipError_t launch_fused_tiles(const Product& p, TO* y) {
     const int64_t tn = (p.N + C::BN - 1) / C::BN, tm = (p.M + 15) / 16;
-    hipLaunchKernelGGL((w8a8_tile_kernel<TO, kFused, C>), dim3((unsigned)(tn * tm)), dim3(64 * C::NW),
-                       fused_bytes<TO>(p, C::WK), p.stream, p.x, nullptr, p.codes, p.scales, y, (int)p.M, (int)p.N, (int)p.K,
-                       nullptr, 1, (int)tn, 64, 0, p.M <= 16 && (double)p.N * (double)p.K >= kOnceBytes);
-    return hipGetLastError();
+    auto launch = [&](auto once) {
+        hipLaunchKernelGGL((w8a8_tile_kernel<TO, kFused, C, decltype(once)::value>), dim3((unsigned)(tn * tm)), dim3(64 * C::NW),
+                           fused_bytes<TO>(p, C::WK), p.stream, p.x, nullptr, p.codes, p.scales, y, (int)p.M, (int)p.N,
+                           (int)p.K, nullptr, 1, (int)tn, 64, 0);
+        return hipGetLastError();
+    };
+    return weights_once<C>(Share(p.M, 1), p.N, p.K) ? launch(std::true_type{}) : launch(std::false_type{});
 }
 using F16x32 = Tiling<1, 2, 2, 1, 1, 4, 1, false>;
 using F16x16 = Tiling<1, 1, 4, 1, 1, 6, 1, false>;

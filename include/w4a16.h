@@ -339,15 +339,17 @@ w4a16_status_t w4a16_gemm_w8a8(w4a16_format_t fmt, w4a16_dtype_t out, const int8
                                void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* y [M][N] = x [M][K] . W_hat^T with x quantized on the way: bit for bit w4a16_quantize_rows_i8
- * followed by w4a16_gemm_w8a8 with out = act.  workspace (w4a16_w8a8_workspace_bytes, 16-byte
- * aligned) holds the codes and scales of x and the parts' sums; it needs no initialisation and must
- * not be shared by calls, or graphs of calls, that may run at the same time.  Errors as for the two
- * calls, and ERR_INVALID for a workspace that is NULL or too small. */
+ * followed by w4a16_gemm_w8a8 with out = act.  workspace (16-byte aligned) holds the codes and scales
+ * of x, M K + 4 M bytes, and the parts' sums where it has room for them (w4a16_w8a8_workspace_bytes is
+ * enough for all); it needs no initialisation and must not be shared by calls, or graphs of calls, that
+ * may run at the same time.  Errors as for the two calls, and ERR_INVALID for a workspace that is NULL
+ * or smaller than M K + 4 M bytes. */
 w4a16_status_t w4a16_matmul_w8a8(w4a16_format_t fmt, w4a16_dtype_t act, const void* x, int64_t M, const void* codes,
                                  const void* scales, const void* mins, int64_t N, int64_t K, void* y, void* workspace,
                                  size_t workspace_bytes, hipStream_t stream);
 
-/* Bytes of workspace w4a16_matmul_w8a8 needs (0 for a shape it refuses or another format). */
+/* Bytes of workspace w4a16_matmul_w8a8 and w4a16_gemm_w8a8 can use (0 for a shape they refuse or another
+ * format). */
 size_t w4a16_w8a8_workspace_bytes(w4a16_format_t fmt, int64_t M, int64_t N, int64_t K);
 
 /* ---- Experts: tokens sorted by expert, the experts' products, and back -----------------------------

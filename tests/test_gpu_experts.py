@@ -134,6 +134,41 @@ def test_gather_i8(T, topk, E, K, kind):
     assert (xq[n:] == 99).all() and (a[n:] == -3).all()
 
 
+def test_rows_past_32_bit_offsets():
+    """More than 2^31 elements of sorted rows, gathered and brought back: the tokens at both ends and around
+    the border, and the gradients' rows."""
+    T, topk, E, N = 70_001, 8, 16, 4096  # 2.3e9 elements
+    ids = torch.randint(0, E, (T, topk), dtype=torch.int32, device="cuda", generator=torch.Generator(device="cuda").manual_seed(7))
+    offsets, pos, src, ws, nb = w.alloc_expert_sort(T, topk, E)
+    w.w4a16_expert_sort(ids, 32, T, topk, E, offsets, pos, src, ws, nb)
+    x = torch.randn((T, N), device="cuda").bfloat16()
+    xs = torch.empty((T * topk, N), dtype=torch.bfloat16, device="cuda")
+    w.w4a16_expert_gather(w.W4A16_BF16, x, T, topk, pos, N, xs)
+    for t in (0, 1, T // 2, T - 1):
+        for j in range(topk):
+            assert torch.equal(xs[int(pos[t, j])], x[t])
+    border = 2 ** 31 // N
+    for r in (border - 1, border, border + 1, T * topk - 1):
+        assert torch.equal(xs[r], x[int(src[r]) // topk])
+    y = torch.empty_like(x)
+    w.w4a16_expert_combine(w.W4A16_BF16, xs, T, topk, pos, None, N, y)
+    assert torch.equal(y[::997], (x[::997].float() * topk).bfloat16())  # eight equal rows: exact
+    dw = torch.empty((T, topk), device="cuda")
+    dys = xs  # its rows are written anew
+    w.w4a16_expert_combine_backward(w.W4A16_BF16, x, xs.clone(), T, topk, pos, torch.full((T, topk), 0.5, device="cuda"), N, dys, dw)
+    for r in (0, border - 1, border, border + 1, T * topk - 1):
+        assert torch.equal(dys[r], (x[int(src[r]) // topk].float() * 0.5).bfloat16())
+    some = torch.tensor([0, 5, T // 2, T - 1], device="cuda")
+    ref = (x[some].double() ** 2).sum(1, keepdim=True)
+    assert ((dw[some].double() - ref).abs() <= (N / 256 + 32) * F24 * ref).all()
+    xq, a = torch.empty((T * topk, N), dtype=torch.int8, device="cuda"), torch.empty(T * topk, device="cuda")
+    w.w4a16_expert_gather_i8(w.W4A16_BF16, x, T, topk, pos, N, xq, a)
+    at = torch.tensor([0, border - 1, border, border + 1, T * topk - 1], device="cuda")
+    q, ra = quantized(x[src[at].long() // topk].cpu())
+    np.testing.assert_array_equal(xq[at].cpu().numpy(), q)
+    np.testing.assert_array_equal(a[at].cpu().numpy(), ra)
+
+
 def combined(ys, pos, wt):
     """sum_j w ys[pos], and the sum of the terms' magnitudes, in 64 bits."""
     ys, live = ys.double(), torch.from_numpy(pos >= 0)
@@ -292,7 +327,8 @@ def test_experts_products(counts, behind, N, K, kind):
 
 WIDE = [([520, 1, 700], 7, 61, 1040), ([2] * 9, 4, 1001, 1040), ([260] * 8, 0, 61, 1040), ([130, 0, 128, 257], 3, 515, 144),
         ([17] * 20, 0, 1001, 1040), ([40] * 32, 11, 520, 1040), ([260] * 8, 1, 1001, 1040), ([1030, 900], 0, 2056, 400),
-        ([520, 1, 700], 300, 8200, 1040), ([0, 0, 900, 0, 300, 1], 2, 8200, 144)]
+        ([520, 1, 700], 300, 8200, 1040), ([0, 0, 900, 0, 300, 1], 2, 8200, 144),
+        ([1, 0, 2, 1] * 4, 3, 2056, 2064), ([20, 0, 33, 17] * 4, 0, 2056, 2064), ([1] * 512, 0, 64, 80), ([0] * 511 + [3], 1, 64, 80)]
 
 
 @pytest.mark.parametrize("counts,behind,N,K", WIDE)

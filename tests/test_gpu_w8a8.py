@@ -135,7 +135,8 @@ def product_on_gpu(q, a, codes, scales):
 # largest tiles, rows of y that are whole 16-byte chunks and rows that are not
 WIDE = [(17, 2050, 1040), (16, 8200, 1040), (17, 4100, 1040), (40, 8200, 1040), (17, 16500, 1040), (33, 16512, 1040),
         (33, 16500, 144), (65, 16500, 1040), (130, 16512, 144), (200, 16500, 1040), (200, 16512, 400), (780, 14350, 1040),
-        (1030, 14352, 144), (515, 14352, 1168), (2050, 3000, 1040), (1030, 2051, 528)]
+        (1030, 14352, 144), (515, 14352, 1168), (2050, 3000, 1040), (1030, 2051, 528),
+        (16, 16500, 4112), (40, 16500, 4112), (3, 4100, 16400)]  # (weights of more than 64 MiB for one row tile)
 
 
 @pytest.mark.parametrize("M,N,K", WIDE)
@@ -186,7 +187,7 @@ def test_largest_sums(M):
                                         (2, 4096, 4096, "bf16"), (3, 8200, 144, "bf16"), (37, 1001, 2064, "f16"),
                                         (16, 4096, 2048, "bf16"), (16, 4100, 2048, "bf16"), (9, 61, 4096, "bf16"),
                                         (8, 700, 4608, "f16"), (40, 1300, 1024, "f32"), (16, 200, 1536, "f32"),
-                                        (500, 100, 1040, "bf16"), (17, 33, 48, "f16"), (512, 2048, 8192, "bf16"), (200, 1030, 14336, "f16"), (128, 512, 512, "f32")])
+                                        (500, 100, 1040, "bf16"), (1, 16500, 4112, "bf16"), (2, 4090, 16416, "f16"), (17, 33, 48, "f16"), (512, 2048, 8192, "bf16"), (200, 1030, 14336, "f16"), (128, 512, 512, "f32")])
 def test_matmul_is_the_two_calls(M, N, K, kind):
     act, dt = TYPES[kind][:2]
     x = rows(M, K, dt, 31)
@@ -229,10 +230,9 @@ def test_weights_from_the_quantizer():
     assert (codes.cpu().double() * scales.cpu().double()[:, None] - W.double()).abs().max() <= scales.max().item() * 0.5001
 
 
-@pytest.mark.parametrize("M", [1, 300])
-def test_captured_and_on_another_stream(M):
+@pytest.mark.parametrize("M,N,K", [(1, 516, 1040), (30, 516, 1040), (300, 516, 1040), (300, 2050, 8208)])
+def test_captured_and_on_another_stream(M, N, K):
     """Replays of a captured call equal eager calls on the inputs of the moment."""
-    N, K = 516, 1040
     codes, scales = weights(N, K, 61)
     codes, scales = codes.cuda(), scales.cuda()
     x = torch.empty((M, K), dtype=torch.float16, device="cuda")
@@ -256,6 +256,20 @@ def test_captured_and_on_another_stream(M):
         y.zero_()
         g.replay()
         assert torch.equal(y, eager)
+
+
+def test_outputs_past_32_bit_offsets():
+    """More than 2^31 outputs: the last rows and columns, and some between, against the product of those alone."""
+    M, N, K = 150_001, 14_400, 64
+    g = torch.Generator(device="cuda").manual_seed(5)
+    xq = torch.randint(-127, 128, (M, K), dtype=torch.int8, device="cuda", generator=g)
+    a = torch.rand(M, device="cuda", generator=g)
+    codes, scales = weights(N, K, 73)
+    y = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    w.w4a16_gemm_w8a8(W8, w.W4A16_BF16, xq, a, M, codes.cuda(), scales.cuda(), None, N, K, y)
+    for at in (0, 74_565, 149_131, 149_140, M - 70):  # (2^31 / 14400 = 149130.8)
+        rows_ = slice(at, at + 70)
+        check(y[rows_], product(xq[rows_].cpu().numpy(), a[rows_].cpu().numpy(), codes, scales), "bf16")
 
 
 def test_outputs_are_written_exactly():

@@ -106,14 +106,10 @@ def _stream_lookup():
     stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     if device is None or stream is None:  # another torch, or one without a GPU
         return torch.cuda.current_device, lambda d: torch.cuda.current_stream(d).cuda_stream
-
-    def current_device():
-        torch.cuda.init()  # (returns at once when done)
-        return device()
-
-    return current_device, stream
+    return device, stream
 
 
+# (for a process that has initialised the GPU: one that holds a tensor there)
 _current_device, _current_stream = _stream_lookup()
 
 
@@ -128,6 +124,8 @@ def _p(a):
 
 def _stream(stream):
     if stream is None:
+        import torch
+        torch.cuda.init()  # (returns at once when done)
         return _current_stream(_current_device())
     if isinstance(stream, int):
         return stream
@@ -265,8 +263,10 @@ def _call(name: str, args, arrays, stream) -> None:
         device = d
         args[at] = t.data_ptr()
     fn = getattr(lib, name)
-    if device is None or device == _current_device():
+    if device is None:
         status = fn(*args, _stream(stream))
+    elif device == _current_device():
+        status = fn(*args, _current_stream(device) if stream is None else _stream(stream))
     else:
         import torch
         with torch.cuda.device(device):

@@ -26,7 +26,9 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
 // ---- activation quantization ------------------------------------------------------------------
 
-// kWaves waves per row (4, or 1: four rows a block).
+// One pass for the largest magnitude, one for the codes, the row held in registers between them.  Bytes and
+// latency bound it: 8192 rows of 4096 fp32 take 31 us (5.4 TB/s), bf16 25 us (4.0 TB/s), 1024 rows 5.4 us, 37 rows
+// 3.3 us.  kWaves waves per row (4, or 1: four rows a block).
 template <typename T, int kWaves>
 __global__ __launch_bounds__(256) void quant_rows_i8_kernel(const T* __restrict__ x, int64_t M, int K,
                                                             int8_t* __restrict__ xq, float* __restrict__ ascale) {
@@ -49,6 +51,15 @@ __global__ __launch_bounds__(256) void quant_rows_i8_kernel(const T* __restrict_
 // stage, and their sums are added at the end.  Operands reach LDS by direct copies into a ring of R
 // units: a unit is a whole stage (U = 1), or a stage's weights or its rows of x (U = 2, BM = BN).
 // kX = false: x is not staged (the ring holds weights alone).
+//
+// What bounds it.  Many rows: the matrix cores at the clock the power limit leaves.  At 1024 x 14336 x 4096 (T256x256,
+// 53 us, 2.27 POP/s; hipBLASLt's int8 product 73 us) timing-only copies took 43 us without the copies inside the
+// loop and 49 with all of them reading one line, and the matrix instructions alone on such data take 36; waiting
+// for the copies costs nothing.  8192 rows: 393 us (2.45 POP/s; hipBLASLt 426).  Eight waves of 128 x 64 rather than
+// four of 128 x 128 (64 us): two waves per SIMD fill each other's gaps.  16x16x64 instructions rather than
+// 32x32x32: 3.8 POP/s against 3.3 on random codes.  Few rows: the weights' bytes.  One row, 14336 x 4096: 10.5
+// us from the Infinity Cache (5.6 TB/s), 14.1 from HBM; 16 rows over eight such matrices 63 us (7.4 TB/s).
+// Few columns: each block's own chain of k-tiles, which K in parts shortens (launch_parts).
 template <int WM_, int WN_, int WK_, int TM_, int TN_, int R_, int U_ = 1, bool kX = true>
 struct Tiling {
     static constexpr int WM = WM_, WN = WN_, WK = WK_, TM = TM_, TN = TN_, R = R_, U = U_;
@@ -406,7 +417,7 @@ __global__ __launch_bounds__(64 * C::NW) void w8a8_tile_kernel(const void* __res
     }
 }
 
-// y = (the parts' sums, [parts][M N]) * s_n * a_m: exactly what the unsplit product stores.  V columns a thread.
+// Reads bound it (512 x 4096 in two parts: 3-4 us).  y = (the parts' sums, [parts][M N]) * s_n * a_m: exactly what the unsplit product stores.  V columns a thread.
 template <typename TO, int V>
 __global__ __launch_bounds__(256) void w8a8_join_kernel(const int32_t* __restrict__ sums, int parts,
                                                         const float* __restrict__ ascale, const float* __restrict__ scales,
@@ -482,7 +493,8 @@ hipError_t launch_tiles(const Product& p, TO* y) {
     return launch(std::false_type{});
 }
 
-// K in `parts`, one launch for the sums and one that joins them.
+// K in `parts`, one launch for the sums and one that joins them: 100 / 256 / 512 rows of 4096 x 14336 18.6 / 25.6 / 39.8
+// us against 32.6 / 32.8 / 43.4 unsplit.
 template <typename C, typename TO>
 hipError_t launch_parts(const Product& p, TO* y, int parts) {
     const int64_t tn = (p.N + C::BN - 1) / C::BN;

@@ -520,20 +520,20 @@ constexpr double kJoinUs = 3.0, kJoinBytesPerUs = 5e6;
 // The tilings, and what one costs.  A block takes `us_ktile` for each 128 of K (measured where every block has
 // a CU to itself: 4096 columns, K = 4096 and 14336) and `us_block` besides; `blocks` of them fit a CU,
 // which runs them at the same rate in all.  Few rows wait for the weights instead, which arrive at `tbs` TB/s
-// (measured on eight matrices of 14336 x 4096 and 64 of 1024 x 2048; any tiling at 7.4 where they are read once).  The choice by this is within 2% of
-// the fastest in 31 of 33 shapes of 1 to 2048 rows of one matrix, within 13% in the others; of experts,
-// whose row counts are not known here, within 10%.
+// (measured on eight matrices of 14336 x 4096 and 64 of 1024 x 2048), or at `tbs_once` where they are read once.
+// The choice by this is within 2% of the fastest in 31 of 33 shapes of 1 to 2048 rows of one matrix, within
+// 13% in the others; of experts, whose row counts are not known here, within 10%.
 struct Cost {
     double us_ktile, us_block;
     int blocks;
-    double tbs;
+    double tbs, tbs_once;
     double us(int64_t tiles, int64_t K, double weight_bytes, bool once) const {
         const double waves = (double)tiles / 256, up = std::ceil(waves), slots = 256.0 * blocks;
         const double rounds = blocks == 1 ? up : waves <= 1 ? 1.0 : std::max(waves, 0.9 * up);
         const double work = rounds * ((double)((K + 127) / 128) * us_ktile + us_block);
         // a stream of more blocks than run at once ends with some of the GPU idle: half a round on average
         const double tail = tiles > slots ? 1.0 + 0.5 * slots / (double)tiles : 1.0;
-        const double stream = weight_bytes / (once ? 7.4 : tbs) * 1e-6 * tail;
+        const double stream = weight_bytes / (once ? tbs_once : tbs) * 1e-6 * tail;
         return 2.6 + std::max(work, stream) + 0.03 * work;  // (of two that wait, the idler one)
     }
 };
@@ -555,16 +555,16 @@ struct Plan {
 };
 template <typename F>
 void each_tiling(F f) {
-    f(0, T256x256{}, Cost{1.25, 4.0, 1, 5.0});
-    f(1, T128x256{}, Cost{0.72, 2.0, 1, 5.0});
-    f(2, T128x128{}, Cost{0.43, 1.0, 2, 5.2});
-    f(3, T64x128{}, Cost{0.33, 1.0, 2, 5.3});
-    f(4, T32x128{}, Cost{0.30, 1.0, 2, 5.5});
-    f(5, T64x64{}, Cost{0.25, 0.6, 2, 5.2});
-    f(6, T32x32{}, Cost{0.13, 0.4, 2, 5.3});
-    f(7, T16x64{}, Cost{0.19, 0.3, 4, 5.8});
-    f(8, T16x32{}, Cost{0.098, 0.3, 3, 5.8});
-    f(9, T16x16{}, Cost{0.07, 0.3, 1, 5.2});
+    f(0, T256x256{}, Cost{1.25, 4.0, 1, 5.0, 5.0});
+    f(1, T128x256{}, Cost{0.72, 2.0, 1, 5.0, 5.0});
+    f(2, T128x128{}, Cost{0.43, 1.0, 2, 5.2, 5.2});
+    f(3, T64x128{}, Cost{0.33, 1.0, 2, 5.3, 6.3});
+    f(4, T32x128{}, Cost{0.30, 1.0, 2, 5.5, 6.9});
+    f(5, T64x64{}, Cost{0.25, 0.6, 2, 5.2, 6.3});
+    f(6, T32x32{}, Cost{0.13, 0.4, 2, 5.3, 6.8});
+    f(7, T16x64{}, Cost{0.19, 0.3, 4, 5.8, 7.2});
+    f(8, T16x32{}, Cost{0.098, 0.3, 3, 5.8, 7.4});
+    f(9, T16x16{}, Cost{0.07, 0.3, 1, 5.2, 6.5});
 }
 size_t sums_bytes(int64_t M, int64_t N, int parts) { return parts > 1 ? (size_t)parts * (size_t)M * (size_t)N * 4 : 0; }
 

@@ -2,8 +2,6 @@
 // types, per-row int8 quantization, and the search for the expert that a row tile belongs to.
 #pragma once
 
-#include <algorithm>
-
 #include "device_common.h"
 
 namespace w4a16 {
@@ -201,8 +199,8 @@ inline bool row_by_wave(int64_t rows, int64_t K) { return K <= 2048 && rows >= 1
 
 // Most row tiles of `tile` rows that R rows over E experts can make: each expert that has rows may end
 // in a part of a tile.
-inline int64_t expert_tiles(int64_t R, int64_t E, int64_t tile) {
-    const int64_t used = std::min(R, E);
+__host__ __device__ constexpr int64_t expert_tiles(int64_t R, int64_t E, int64_t tile) {
+    const int64_t used = R < E ? R : E;
     return (R + used * (tile - 1)) / tile;
 }
 

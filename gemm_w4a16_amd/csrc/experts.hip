@@ -7,6 +7,7 @@
 //   combine   y_t = sum_j w_tj ys[pos_tj], in order of j, in fp32
 //   backward  dys[pos_tj] = w_tj dy_t, dw_tj = sum_n dy_t[n] ys[pos_tj][n]
 // combine without weights is the gather's gradient.
+#include <algorithm>
 #include <type_traits>
 
 #include "device_common.h"

@@ -9,6 +9,7 @@
 //
 // With experts the rows are sorted by expert (offsets[e] is the first row of expert e) and row r of
 // expert e is multiplied by that expert's weights.
+#include <algorithm>
 #include <cmath>
 #include <cstddef>
 #include <type_traits>
@@ -156,7 +157,8 @@ __global__ __launch_bounds__(64 * C::NW) void w8a8_tile_kernel(const void* __res
         ExpertRun first;
         if constexpr (kExperts) {
             first = expert_run(offsets, E, 0, M, BM);
-            m_tiles = count_expert_tiles(first, offsets, E, M, BM);
+            // (offsets that fall can name rows more than once: no more tiles than the launch counted with)
+            m_tiles = min((uint32_t)count_expert_tiles(first, offsets, E, M, BM), (uint32_t)expert_tiles(M, E, BM));
         }
         const int total = kSums ? gridDim.x : m_tiles * n_tiles, b = blockIdx.x;
         if (b >= total) return;

@@ -357,8 +357,8 @@ size_t w4a16_w8a8_workspace_bytes(w4a16_format_t fmt, int64_t M, int64_t N, int6
  * t's j-th choice.  The pairs are sorted by expert, stably (pairs of one expert in order of p); a
  * pair whose id is outside [0, E) -- a padding token's, say -1 -- goes to no expert and gets no row.
  * The same expert may appear twice among a token's choices.  Sorted arrays have T * topk rows; the
- * experts' rows are the first offsets[E] of them, and rows behind those are neither read nor
- * written by any call.  A serving pass is w4a16_expert_sort, w4a16_expert_gather_i8,
+ * experts' rows are the first offsets[E] of them; rows behind those are not written by any call, and what
+ * they hold enters no result.  A serving pass is w4a16_expert_sort, w4a16_expert_gather_i8,
  * w4a16_gemm_w8a8_experts, w4a16_expert_combine; none of them waits for the host, so the pass can be
  * captured into a graph.
  * T, topk and E at least 1; topk and E at most w4a16_max_experts(), T * topk at most 2^30 and rows
@@ -393,7 +393,8 @@ w4a16_status_t w4a16_expert_gather_i8(w4a16_dtype_t act, const void* x, int64_t 
 /* w4a16_gemm_w8a8 with one weight matrix per expert: codes [E][N][K] and scales [E][N], each expert's
  * part as w4a16_quantize_pack writes it; y[r] for the rows r of expert e (offsets[e] <= r <
  * offsets[e + 1]) is multiplied by that expert's weights.  R: rows that xq, ascale and y have.
- * Experts with no rows cost no work.  offsets are read on the device and clamped to [0, R]. */
+ * Experts with no rows cost no work.  offsets are read on the device and clamped to [0, R]; where they
+ * fall, no memory is touched beyond the arrays, but which rows are written is unspecified. */
 w4a16_status_t w4a16_gemm_w8a8_experts(w4a16_format_t fmt, w4a16_dtype_t out, const int8_t* xq, const float* ascale,
                                        int64_t R, const int32_t* offsets, int64_t E, const void* codes, const void* scales,
                                        const void* mins, int64_t N, int64_t K, void* y, hipStream_t stream);

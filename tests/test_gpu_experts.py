@@ -366,6 +366,18 @@ def test_offsets_out_of_range():
         assert (got[R:] == 7).all() and ((got[:R] == 7) | (got[:R] == K)).all()
 
 
+def test_offsets_that_name_rows_many_times():
+    """Every other expert claims all rows: more tiles than any sorted order makes."""
+    E, R, N, K = 512, 333, 300, 64
+    buf = torch.full((R + 600, N), 7.0, device="cuda")
+    xq = torch.ones((R, K), dtype=torch.int8, device="cuda")
+    codes, scales = torch.ones((E, N, K), dtype=torch.int8, device="cuda"), torch.ones((E, N), device="cuda")
+    o = torch.tensor([R * (e % 2) for e in range(E + 1)], dtype=torch.int32, device="cuda")
+    w.w4a16_gemm_w8a8_experts(W8, w.W4A16_FP32, xq, torch.ones(R, device="cuda"), R, o, E, codes, scales, None, N, K, buf[:R])
+    got = buf.cpu()
+    assert (got[R:] == 7).all() and ((got[:R] == 7) | (got[:R] == K)).all()
+
+
 def test_no_expert_has_rows():
     y = torch.full((5, 32), 7.0, device="cuda")
     z = torch.zeros(8, dtype=torch.int32, device="cuda")

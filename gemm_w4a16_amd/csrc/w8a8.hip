@@ -466,8 +466,13 @@ bool fits_grid(int64_t M, int64_t N, bool experts, int64_t E) {
 
 // The experts that can have rows, and the rows of each if they share them evenly.
 struct Share {
-    int64_t experts, rows;
-    Share(int64_t M, int64_t E) : experts(std::min(M, E)), rows(E == 1 ? M : (M + experts - 1) / experts) {}
+    int64_t M, experts, rows;
+    Share(int64_t M, int64_t E) : M(M), experts(std::min(M, E)), rows(E == 1 ? M : (M + experts - 1) / experts) {}
+    // Row tiles: of several experts whose counts differ, each ends half a tile past its share.
+    double row_tiles(int BM) const {
+        if (experts == 1) return (double)((M + BM - 1) / BM);
+        return std::max((double)experts, (double)M / BM + 0.5 * (double)experts);
+    }
 };
 template <typename C>
 bool weights_once(const Share& s, int64_t N, int64_t K) {
@@ -519,24 +524,24 @@ hipError_t launch_parts(const Product& p, TO* y, int parts) {
 // A join costs a launch and its bytes.
 constexpr double kJoinUs = 3.0, kJoinBytesPerUs = 5e6;
 
-// The tilings, and what one costs.  A block takes `us_ktile` for each 128 of K (measured where every block has
-// a CU to itself: 4096 columns, K = 4096 and 14336) and `us_block` besides; `blocks` of them fit a CU,
-// which runs them at the same rate in all.  Few rows wait for the weights instead, which arrive at `tbs` TB/s
-// (measured on eight matrices of 14336 x 4096 and 64 of 1024 x 2048), or at `tbs_once` where they are read once.
-// The choice by this is within 2% of the fastest in 31 of 33 shapes of 1 to 2048 rows of one matrix, within
-// 13% in the others; of experts, whose row counts are not known here, within 10%.
+// The tilings, and what one costs.  A CU's first block takes `us_ktile` for each 128 of K and `us_first`
+// besides, each further one `next_ktile` and `us_next`; `blocks` of them fit a CU.  The weights arrive at 5.6
+// TB/s, or 7.3 where they are read once, and neither hides all of the other; a stream of more blocks than run at
+// once ends with some of the GPU idle.  Fitted to the tilings' times at 200 shapes of one matrix of 3 to 4096
+// rows and 290 of 4 to 256 experts: the choice is on average 1% slower than the fastest tiling for one matrix
+// and 2% for experts, whose row counts are not known here, and within 10% of it in 464 of the 490.  (With
+// us_first also for further blocks, and time as the larger of the two, 2% and 11%, and up to 2.9 times the
+// fastest where K is short.)
 struct Cost {
-    double us_ktile, us_block;
+    double us_ktile, us_first, next_ktile, us_next;
     int blocks;
-    double tbs, tbs_once;
-    double us(int64_t tiles, int64_t K, double weight_bytes, bool once) const {
-        const double waves = (double)tiles / 256, up = std::ceil(waves), slots = 256.0 * blocks;
+    double us(double tiles, int64_t K, double weight_bytes, bool once) const {
+        const double waves = tiles / 256, up = std::ceil(waves), slots = 256.0 * blocks, ktiles = (double)((K + 127) / 128);
         const double rounds = blocks == 1 ? up : waves <= 1 ? 1.0 : std::max(waves, 0.9 * up);
-        const double work = rounds * ((double)((K + 127) / 128) * us_ktile + us_block);
-        // a stream of more blocks than run at once ends with some of the GPU idle: half a round on average
-        const double tail = tiles > slots ? 1.0 + 0.5 * slots / (double)tiles : 1.0;
-        const double stream = weight_bytes / (once ? tbs_once : tbs) * 1e-6 * tail;
-        return 2.6 + std::max(work, stream) + 0.03 * work;  // (of two that wait, the idler one)
+        const double work = ktiles * us_ktile + us_first + (rounds - 1) * (ktiles * next_ktile + us_next);
+        const double tail = tiles > slots ? 1.0 + 0.2 * slots / tiles : 1.0;
+        const double stream = weight_bytes / (once ? 7.3e6 : 5.6e6) * tail;
+        return 2.6 + std::sqrt(work * work + stream * stream);
     }
 };
 using T256x256 = Tiling<2, 4, 1, 8, 4, 5, 2>;
@@ -557,16 +562,16 @@ struct Plan {
 };
 template <typename F>
 void each_tiling(F f) {
-    f(0, T256x256{}, Cost{1.25, 4.0, 1, 5.0, 5.0});
-    f(1, T128x256{}, Cost{0.72, 2.0, 1, 5.0, 5.0});
-    f(2, T128x128{}, Cost{0.43, 1.0, 2, 5.2, 5.2});
-    f(3, T64x128{}, Cost{0.33, 1.0, 2, 5.3, 6.3});
-    f(4, T32x128{}, Cost{0.30, 1.0, 2, 5.5, 6.9});
-    f(5, T64x64{}, Cost{0.25, 0.6, 2, 5.2, 6.3});
-    f(6, T32x32{}, Cost{0.13, 0.4, 2, 5.3, 6.8});
-    f(7, T16x64{}, Cost{0.19, 0.3, 4, 5.8, 7.2});
-    f(8, T16x32{}, Cost{0.098, 0.3, 3, 5.8, 7.4});
-    f(9, T16x16{}, Cost{0.07, 0.3, 1, 5.2, 6.5});
+    f(0, T256x256{}, Cost{1.06, 1.8, 1.27, 5.5, 1});
+    f(1, T128x256{}, Cost{0.73, 1.5, 0.81, 5.9, 1});
+    f(2, T128x128{}, Cost{0.51, 0.1, 0.49, 2.3, 2});
+    f(3, T64x128{}, Cost{0.36, 0.3, 0.38, 1.6, 2});
+    f(4, T32x128{}, Cost{0.31, 0.5, 0.3, 1.8, 2});
+    f(5, T64x64{}, Cost{0.25, 0.5, 0.23, 1.3, 2});
+    f(6, T32x32{}, Cost{0.12, 0.6, 0.098, 1.4, 2});
+    f(7, T16x64{}, Cost{0.22, 0.2, 0.12, 0.7, 4});
+    f(8, T16x32{}, Cost{0.11, 0.3, 0.062, 0.9, 3});
+    f(9, T16x16{}, Cost{0.066, 0.8, 0.051, 2.8, 1});
 }
 size_t sums_bytes(int64_t M, int64_t N, int parts) { return parts > 1 ? (size_t)parts * (size_t)M * (size_t)N * 4 : 0; }
 
@@ -579,7 +584,7 @@ Plan plan_product(int64_t M, int64_t N, int64_t K, bool experts, int64_t E, size
     each_tiling([&](int i, auto tiling, Cost cost) {
         using C = decltype(tiling);
         if (!fits_grid<C>(M, N, experts, E)) return;
-        const int64_t tiles = share.experts * ((share.rows + C::BM - 1) / C::BM) * ((N + C::BN - 1) / C::BN);
+        const double tiles = share.row_tiles(C::BM) * (double)((N + C::BN - 1) / C::BN);
         const bool once = weights_once<C>(share, N, K);
         const int most = experts || C::WK > 1 || C::BM * C::BN < 64 * 64 || room == 0 || ktiles < 32 ? 0 : 3;
         for (int log = 0; log <= most; ++log) {  // (host time counts here: a launch is 3.4 us)

@@ -331,7 +331,13 @@ WIDE = [([520, 1, 700], 7, 61, 1040), ([2] * 9, 4, 1001, 1040), ([260] * 8, 0, 6
         ([1, 0, 2, 1] * 4, 3, 2056, 2064), ([20, 0, 33, 17] * 4, 0, 2056, 2064), ([1] * 512, 0, 64, 80), ([0] * 511 + [3], 1, 64, 80)]
 
 
-@pytest.mark.parametrize("counts,behind,N,K", WIDE)
+MORE = [([1], 1, 37, 1584), ([2, 1, 0, 2], 0, 917, 18592), ([4, 1, 3, 0, 2, 5], 0, 2648, 4240), ([9, 0, 1, 1, 2, 0, 3, 0] * 2, 4, 3131, 1344),
+        ([90, 1, 3, 0, 24, 0, 0, 0], 0, 914, 9584), ([1, 2, 0], 0, 8863, 2528), ([20, 3, 33], 0, 21692, 1056), ([65, 0, 0, 1], 0, 3879, 4400),
+        ([24] * 128, 2, 33, 80), ([1] * 50 + [0] * 9 + [9], 0, 833, 48), ([900, 30, 7], 0, 1008, 672), ([62] * 64, 0, 9, 144),
+        ([400, 60], 0, 530, 160)]
+
+
+@pytest.mark.parametrize("counts,behind,N,K", WIDE + MORE)
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 def test_experts_products_wide(counts, behind, N, K, kind):
     """Each size of tile, with experts that end inside one and rows behind them."""

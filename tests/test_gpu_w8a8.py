@@ -149,10 +149,25 @@ def test_gemm_w8a8_wide(M, N, K, kind):
     assert torch.equal(y, gpu_product(q, a, codes, scales, kind))
 
 
+# weights of more than 64 MiB for one row tile, for each size of tile that they can be read once by
+ONCE = [(2, 3380, 19856), (5, 15536, 4320), (12, 35397, 1904), (31, 24763, 2752), (17, 5481, 12256), (34, 22750, 2960), (62, 16026, 4336)]
+
+
+@pytest.mark.parametrize("M,N,K", ONCE)
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_gemm_w8a8_weights_once(M, N, K, kind):
+    q, a = quantized(rows(M, K, TYPES[kind][1], 27))
+    codes, scales = weights(N, K, 28)
+    check(gpu_product(q, a, codes, scales, kind), product_on_gpu(q, a, codes, scales), kind)
+
+
 PARTS = [(128, 4096, 14336), (512, 4096, 14352), (300, 2050, 8208), (2000, 1000, 20000), (200, 1030, 14336), (100, 515, 40000)]
 
 
-@pytest.mark.parametrize("M,N,K", PARTS)
+MORE_PARTS = [(365, 1389, 8368), (801, 1244, 7984), (1609, 1153, 10112), (81, 1047, 15792), (263, 979, 8096), (1, 1, 15664), (70, 300, 15664)]
+
+
+@pytest.mark.parametrize("M,N,K", PARTS + MORE_PARTS)
 @pytest.mark.parametrize("kind", list(TYPES))
 def test_k_in_parts_is_the_same_product(M, N, K, kind):
     """Few columns and a long K, with a workspace for the sums of K's parts and without: the same bits."""

@@ -2,6 +2,8 @@
 // types, per-row int8 quantization, and the search for the expert that a row tile belongs to.
 #pragma once
 
+#include <type_traits>
+
 #include "device_common.h"
 
 namespace w4a16 {
@@ -51,22 +53,35 @@ struct alignas(V * sizeof(T)) Pack {
     T v[V];
 };
 
-// A unit read or written once: with kStream past the caches' usual order (non-temporal), which large arrays
-// gain by and arrays that the caches hold lose by.
+// V consecutive elements.  With kStream past the caches' usual order (non-temporal), which large arrays gain by and
+// arrays that the caches hold lose by; kAny: at any element (the memory unit takes 16 bytes at any address).
 typedef uint32_t unit16_t __attribute__((ext_vector_type(4)));
-template <bool kStream, typename U>
-__device__ __forceinline__ U load_unit(const U* p) {
-    if constexpr (kStream && sizeof(U) == 16)
-        return __builtin_bit_cast(U, __builtin_nontemporal_load(reinterpret_cast<const unit16_t*>(p)));
-    else
-        return *p;
+typedef unit16_t any16_t __attribute__((aligned(2)));
+template <bool kStream, bool kAny, int V, typename T>
+__device__ __forceinline__ Pack<T, V> load_unit(const T* p) {
+    using U = Pack<T, V>;
+    if constexpr (sizeof(U) == 16 && (kStream || kAny)) {
+        using V16 = std::conditional_t<kAny, any16_t, unit16_t>;
+        const V16* q = reinterpret_cast<const V16*>(p);
+        const unit16_t v = kStream ? __builtin_nontemporal_load(q) : *q;
+        return __builtin_bit_cast(U, v);
+    } else {
+        return *reinterpret_cast<const U*>(p);
+    }
 }
-template <bool kStream, typename U>
-__device__ __forceinline__ void store_unit(U* p, const U& u) {
-    if constexpr (kStream && sizeof(U) == 16)
-        __builtin_nontemporal_store(__builtin_bit_cast(unit16_t, u), reinterpret_cast<unit16_t*>(p));
-    else
-        *p = u;
+template <bool kStream, bool kAny, int V, typename T>
+__device__ __forceinline__ void store_unit(T* p, const Pack<T, V>& u) {
+    if constexpr (sizeof(u) == 16 && (kStream || kAny)) {
+        using V16 = std::conditional_t<kAny, any16_t, unit16_t>;
+        V16* q = reinterpret_cast<V16*>(p);
+        const V16 v = __builtin_bit_cast(unit16_t, u);
+        if constexpr (kStream)
+            __builtin_nontemporal_store(v, q);
+        else
+            *q = v;
+    } else {
+        *reinterpret_cast<Pack<T, V>*>(p) = u;
+    }
 }
 
 // ---- int8 quantization of a row -------------------------------------------------------------------

@@ -184,8 +184,16 @@ __device__ __forceinline__ int64_t pair_row(const int32_t* pos, int64_t p, int64
 // The token and unit of a row (16 bytes, or one element) that a thread moves: a block takes 256 units of a row,
 // or (kShort) `tokens` whole rows where a row has at most 64.
 struct RowShape {
-    int units, tokens, blocks_per_row;
+    int width, units, tokens, blocks_per_row;  // width: elements
 };
+// A unit's first element.  kRagged: rows are not whole units, so units start at any element, and a row's last one is
+// moved back to end with the row: its first elements are the unit's before it too.  (4096 tokens of 2 rows of 4098 bf16:
+// gather 17 us against 59 by element, combine 19 against 62, backward 37 against 55; 333 of 3 rows of 1001 fp16 2.6
+// against 3.3, 2.8 against 3.7, 4.3 against 6.2.)
+template <int V, bool kRagged>
+__device__ __forceinline__ int unit_at(int c, int width) {
+    return kRagged ? min(V * c, width - V) : V * c;
+}
 template <bool kShort>
 __device__ __forceinline__ bool row_place(const RowShape& s, int64_t b, int64_t Tn, int64_t& t, int& c) {
     if constexpr (kShort) {
@@ -201,19 +209,20 @@ __device__ __forceinline__ bool row_place(const RowShape& s, int64_t b, int64_t 
 // xs[pos_tj] = x_t.  A unit is read once and stored for each of the token's pairs, so the writes bound it: 8192 tokens
 // of 8 rows of 2048 bf16 (0.30 GB) take 47 us, 6.4 TB/s over what is read and written; four tokens of 2 rows
 // of 4096 2.5 us, an empty launch's 1.7 and two loads' latency.
-template <typename U, bool kStream, bool kShort>
-__global__ __launch_bounds__(256) void gather_kernel(const U* __restrict__ x, int64_t Tn, int topk,
+template <typename T, int V, bool kRagged, bool kStream, bool kShort>
+__global__ __launch_bounds__(256) void gather_kernel(const T* __restrict__ x, int64_t Tn, int topk,
                                                      const int32_t* __restrict__ pos, RowShape s, int64_t blocks,
-                                                     U* __restrict__ xs) {
+                                                     T* __restrict__ xs) {
     const int64_t P = Tn * topk;
     for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
         int64_t t;
         int c;
         if (!row_place<kShort>(s, b, Tn, t, c)) continue;
-        const U v = x[t * s.units + c];
+        const int at = unit_at<V, kRagged>(c, s.width);
+        const Pack<T, V> v = load_unit<false, kRagged, V>(x + t * s.width + at);
         for (int j = 0; j < topk; ++j) {
             const int64_t r = pair_row(pos, t * topk + j, P);
-            if (r >= 0) store_unit<kStream>(&xs[r * s.units + c], v);
+            if (r >= 0) store_unit<kStream, kRagged>(xs + r * s.width + at, v);
         }
     }
 }
@@ -249,20 +258,20 @@ __global__ __launch_bounds__(256) void gather_i8_kernel(const T* __restrict__ x,
 
 // The rows of kAhead pairs from j0 on, one unit of each: all requested before the first is used (a pair with no
 // row reads row 0 and is left out).
-template <bool kStream, int kAhead, typename U>
-__device__ __forceinline__ void load_pairs(const U* ys, const int32_t* pos, int64_t t, int topk, int j0, int64_t P, int units,
-                                           int c, U (&v)[kAhead], int64_t (&row)[kAhead]) {
+template <bool kStream, bool kRagged, int kAhead, typename T, int V>
+__device__ __forceinline__ void load_pairs(const T* ys, const int32_t* pos, int64_t t, int topk, int j0, int64_t P, int width,
+                                           int at, Pack<T, V> (&v)[kAhead], int64_t (&row)[kAhead]) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
         row[i] = j0 + i < topk ? pair_row(pos, t * topk + j0 + i, P) : -1;
-        v[i] = load_unit<kStream>(&ys[max(row[i], (int64_t)0) * units + c]);
+        v[i] = load_unit<kStream, kRagged, V>(ys + max(row[i], (int64_t)0) * width + at);
     }
 }
 
 // y_t = sum_j w_tj ys[pos_tj] in fp32, in order of j.  A thread owns one unit of y and reads that unit of every pair's
 // row, so nothing is joined and the reads bound it: 4096 tokens of 2 rows of 4096 bf16 (0.10 GB) take 17 us (5.8
 // TB/s), of 8 rows of 2048 (0.15 GB) 25 us (5.9 TB/s).
-template <typename T, int V, int kAhead, bool kStream, bool kShort>
+template <typename T, int V, bool kRagged, int kAhead, bool kStream, bool kShort>
 __global__ __launch_bounds__(256) void combine_kernel(const T* __restrict__ ys, int64_t Tn, int topk,
                                                       const int32_t* __restrict__ pos, const float* __restrict__ weights,
                                                       RowShape s, int64_t blocks, T* __restrict__ y) {
@@ -272,11 +281,12 @@ __global__ __launch_bounds__(256) void combine_kernel(const T* __restrict__ ys, 
         int64_t t;
         int c;
         if (!row_place<kShort>(s, b, Tn, t, c)) continue;
+        const int at = unit_at<V, kRagged>(c, s.width);
         float acc[V] = {};
         for (int j0 = 0; j0 < topk; j0 += kAhead) {
             U v[kAhead];
             int64_t row[kAhead];
-            load_pairs<kStream>(reinterpret_cast<const U*>(ys), pos, t, topk, j0, P, s.units, c, v, row);
+            load_pairs<kStream, kRagged>(ys, pos, t, topk, j0, P, s.width, at, v, row);
 #pragma unroll
             for (int i = 0; i < kAhead; ++i)
                 if (row[i] >= 0) {
@@ -288,7 +298,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const T* __restrict__ ys, 
         U o;
 #pragma unroll
         for (int i = 0; i < V; ++i) o.v[i] = from_f32<T>(acc[i]);
-        store_unit<kStream>(reinterpret_cast<U*>(y) + t * s.units + c, o);
+        store_unit<kStream, kRagged>(y + t * s.width + at, o);
     }
 }
 
@@ -301,10 +311,10 @@ constexpr int kBackwardAhead = 2;
 // tokens a block, for short rows); kAhead pairs at a time.  A thread's partial dot products are summed over
 // the wave, then over the waves, in a fixed order.  Its bytes bound it: 4096 tokens of 8 rows of 2048 bf16 (0.29
 // GB) take 51 us (5.6 TB/s).
-template <typename T, int V, int kAhead, int kWaves, bool kStream>
+template <typename T, int V, bool kRagged, int kAhead, int kWaves, bool kStream>
 __global__ __launch_bounds__(256) void combine_backward_kernel(const T* __restrict__ dy, const T* __restrict__ ys, int64_t Tn,
                                                                int topk, const int32_t* __restrict__ pos,
-                                                               const float* __restrict__ weights, int units,
+                                                               const float* __restrict__ weights, int units, int width,
                                                                T* __restrict__ dys, float* __restrict__ dweights) {
     using U = Pack<T, V>;
     constexpr int kTokens = 4 / kWaves, kThreads = kWave * kWaves;
@@ -317,11 +327,12 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const T* __restri
         for (int j0 = 0; j0 < topk; j0 += kAhead) {
             float dot[kAhead] = {};
             for (int c = lane; c < units; c += kThreads) {
-                const U g = reinterpret_cast<const U*>(dy)[t * units + c];
+                const int at = unit_at<V, kRagged>(c, width), seen = V * c - at;  // (the unit before has its first `seen`)
+                const U g = load_unit<false, kRagged, V>(dy + t * width + at);
                 U v[kAhead];
                 int64_t row[kAhead];
                 if (dweights != nullptr) {
-                    load_pairs<kStream>(reinterpret_cast<const U*>(ys), pos, t, topk, j0, P, units, c, v, row);
+                    load_pairs<kStream, kRagged>(ys, pos, t, topk, j0, P, width, at, v, row);
                 } else {
 #pragma unroll
                     for (int i = 0; i < kAhead; ++i) row[i] = j0 + i < topk ? pair_row(pos, t * topk + j0 + i, P) : -1;
@@ -331,14 +342,15 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const T* __restri
                     if (row[i] < 0) continue;
                     if (dweights != nullptr) {
 #pragma unroll
-                        for (int k = 0; k < V; ++k) dot[i] = __builtin_fmaf(to_f32(g.v[k]), to_f32(v[i].v[k]), dot[i]);
+                        for (int k = 0; k < V; ++k)
+                            if (!kRagged || k >= seen) dot[i] = __builtin_fmaf(to_f32(g.v[k]), to_f32(v[i].v[k]), dot[i]);
                     }
                     if (dys != nullptr) {
                         const float w = weights != nullptr ? weights[t * topk + j0 + i] : 1.0f;
                         U o;
 #pragma unroll
                         for (int k = 0; k < V; ++k) o.v[k] = from_f32<T>(w * to_f32(g.v[k]));
-                        store_unit<kStream>(reinterpret_cast<U*>(dys) + row[i] * units + c, o);
+                        store_unit<kStream, kRagged>(dys + row[i] * width + at, o);
                     }
                 }
             }
@@ -413,33 +425,51 @@ hipError_t launch_expert_sort(const void* ids, int id_bits, int64_t P, int64_t E
 }
 
 // Arrays of sorted rows from this size on are streamed (more than the L2s hold, 8 x 4 MiB): 4096 tokens of 2 rows of
-// 8 KiB are gathered in 16.1 us against 20.5, 333 of 3 rows of 2 KB in 2.8 against 2.5.
-static bool streams(int64_t rows, int64_t row_bytes) { return rows * row_bytes >= ((int64_t)32 << 20); }
+// 8 KiB are gathered in 16.1 us against 20.5, 333 of 3 rows of 2 KB in 2.8 against 2.5.  Rows that are not whole
+// units, whose ends share lines, from twice that: 4096 tokens of 2 rows of 4098 bf16 17.4 against 19.5, 6000 of 7
+// rows of 609 fp16 (49 MiB) 16.7 against 12.1.
+static bool streams(int64_t rows, int64_t row_bytes, bool ragged) {
+    return rows * row_bytes >= ((int64_t)(ragged ? 64 : 32) << 20);
+}
 
-static RowShape row_shape(int64_t units) {
-    return RowShape{(int)units, units <= 64 ? (int)(256 / units) : 1, (int)ceil_div(units, 256)};
+static RowShape row_shape(int64_t width, int64_t units) {
+    return RowShape{(int)width, (int)units, units <= 64 ? (int)(256 / units) : 1, (int)ceil_div(units, 256)};
 }
 static int64_t row_blocks(const RowShape& s, int64_t T) { return s.tokens > 1 ? ceil_div(T, s.tokens) : T * s.blocks_per_row; }
 
+// f(an element, the elements of a unit, whether a row is not whole units, whether rows are streamed) as constants.
+// Rows shorter than a unit go by element.
+template <typename E, typename F>
+static hipError_t with_row_unit(E t, int64_t T, int64_t topk, int64_t N, F f) {
+    using std::false_type;
+    using std::integral_constant;
+    using std::true_type;
+    constexpr int V = 16 / sizeof(E);
+    if (N < V) return f(t, integral_constant<int, 1>{}, false_type{}, false_type{});
+    const bool ragged = N % V != 0, stream = streams(T * topk, N * sizeof(E), ragged);
+    auto run = [&](auto r) {
+        return stream ? f(t, integral_constant<int, V>{}, r, true_type{}) : f(t, integral_constant<int, V>{}, r, false_type{});
+    };
+    return ragged ? run(true_type{}) : run(false_type{});
+}
+
 hipError_t launch_expert_gather(int dtype, const void* x, int64_t T, int64_t topk, const int32_t* pos, int64_t K, void* xs,
                                 hipStream_t stream) {
-    return with_act_type(dtype, [&](auto t) {
+    auto run = [&](auto t, auto v, auto ragged, auto stream_rows) {
         using E = decltype(t);
-        auto run = [&](auto unit, auto stream_rows) {
-            using U = decltype(unit);
-            const RowShape s = row_shape(K * sizeof(E) / sizeof(U));
-            const int64_t blocks = row_blocks(s, T);
-            auto launch = [&](auto is_short) {
-                hipLaunchKernelGGL((gather_kernel<U, decltype(stream_rows)::value, decltype(is_short)::value>),
-                                   row_grid(blocks), dim3(256), 0, stream, static_cast<const U*>(x), T, (int)topk, pos, s,
-                                   blocks, static_cast<U*>(xs));
-                return hipGetLastError();
-            };
-            return s.tokens > 1 ? launch(std::true_type{}) : launch(std::false_type{});
+        constexpr int V = decltype(v)::value;
+        const RowShape s = row_shape(K, ceil_div(K, V));
+        const int64_t blocks = row_blocks(s, T);
+        auto launch = [&](auto is_short) {
+            hipLaunchKernelGGL((gather_kernel<E, V, decltype(ragged)::value, decltype(stream_rows)::value,
+                                              decltype(is_short)::value>),
+                               row_grid(blocks), dim3(256), 0, stream, static_cast<const E*>(x), T, (int)topk, pos, s, blocks,
+                               static_cast<E*>(xs));
+            return hipGetLastError();
         };
-        if (K * sizeof(E) % 16 != 0) return run(E{}, std::false_type{});
-        return streams(T * topk, K * sizeof(E)) ? run(uint4{}, std::true_type{}) : run(uint4{}, std::false_type{});
-    });
+        return s.tokens > 1 ? launch(std::true_type{}) : launch(std::false_type{});
+    };
+    return dtype == 2 ? with_row_unit(uint32_t{}, T, topk, K, run) : with_row_unit(uint16_t{}, T, topk, K, run);
 }
 
 hipError_t launch_expert_gather_i8(int dtype, const void* x, int64_t T, int64_t topk, const int32_t* pos, int64_t K,
@@ -456,29 +486,16 @@ hipError_t launch_expert_gather_i8(int dtype, const void* x, int64_t T, int64_t 
     });
 }
 
-// f(an element, the elements of a unit, whether rows are streamed) as constants.
-template <typename F>
-static hipError_t with_row_unit(int dtype, int64_t T, int64_t topk, int64_t N, F f) {
-    using std::integral_constant;
-    return with_act_type(dtype, [&](auto t) {
-        using E = decltype(t);
-        constexpr int V = 16 / sizeof(E);
-        if (N % V != 0) return f(t, integral_constant<int, 1>{}, std::false_type{});
-        if (streams(T * topk, N * sizeof(E))) return f(t, integral_constant<int, V>{}, std::true_type{});
-        return f(t, integral_constant<int, V>{}, std::false_type{});
-    });
-}
-
 hipError_t launch_expert_combine(int dtype, const void* ys, int64_t T, int64_t topk, const int32_t* pos,
                                  const float* weights, int64_t N, void* y, hipStream_t stream) {
-    return with_row_unit(dtype, T, topk, N, [&](auto t, auto v, auto stream_rows) {
+    auto run = [&](auto t, auto v, auto ragged, auto stream_rows) {
         using E = decltype(t);
         constexpr int V = decltype(v)::value;
-        const RowShape s = row_shape(N / V);
+        const RowShape s = row_shape(N, ceil_div(N, V));
         const int64_t blocks = row_blocks(s, T);
         auto launch = [&](auto ahead, auto is_short) {
-            hipLaunchKernelGGL((combine_kernel<E, V, decltype(ahead)::value, decltype(stream_rows)::value,
-                                               decltype(is_short)::value>),
+            hipLaunchKernelGGL((combine_kernel<E, V, decltype(ragged)::value, decltype(ahead)::value,
+                                               decltype(stream_rows)::value, decltype(is_short)::value>),
                                row_grid(blocks), dim3(256), 0, stream, static_cast<const E*>(ys), T, (int)topk, pos, weights, s,
                                blocks, static_cast<E*>(y));
             return hipGetLastError();
@@ -488,25 +505,34 @@ hipError_t launch_expert_combine(int dtype, const void* ys, int64_t T, int64_t t
             return topk <= 2 ? launch(integral_constant<int, 2>{}, is_short) : launch(integral_constant<int, 4>{}, is_short);
         };
         return s.tokens > 1 ? pairs(std::true_type{}) : pairs(std::false_type{});
-    });
+    };
+    return with_act_type(dtype, [&](auto t) { return with_row_unit(t, T, topk, N, run); });
 }
 
 hipError_t launch_expert_combine_backward(int dtype, const void* dy, const void* ys, int64_t T, int64_t topk,
                                           const int32_t* pos, const float* weights, int64_t N, void* dys, float* dweights,
                                           hipStream_t stream) {
-    return with_row_unit(dtype, T, topk, N, [&](auto t, auto v, auto stream_rows) {
+    auto run = [&](auto t, auto v, auto ragged, auto stream_rows) {
         using E = decltype(t);
         constexpr int V = decltype(v)::value;
-        constexpr bool kStream = decltype(stream_rows)::value;
-        const int64_t units = N / V;
-        auto run = [&](auto waves) {
+        constexpr bool kRagged = decltype(ragged)::value, kStream = decltype(stream_rows)::value;
+        const int64_t units = ceil_div(N, V);
+        auto launch = [&](auto waves) {
             constexpr int kWaves = decltype(waves)::value;
-            hipLaunchKernelGGL((combine_backward_kernel<E, V, kBackwardAhead, kWaves, kStream>), row_grid(ceil_div(T, 4 / kWaves)),
+            hipLaunchKernelGGL((combine_backward_kernel<E, V, kRagged, kBackwardAhead, kWaves, kStream>),
+                               row_grid(ceil_div(T, 4 / kWaves)),
                                dim3(256), 0, stream, static_cast<const E*>(dy), static_cast<const E*>(ys), T, (int)topk, pos,
-                               weights, (int)units, static_cast<E*>(dys), dweights);
+                               weights, (int)units, (int)N, static_cast<E*>(dys), dweights);
             return hipGetLastError();
         };
-        return units <= 64 ? run(std::integral_constant<int, 1>{}) : run(std::integral_constant<int, 4>{});
+        return units <= 64 ? launch(std::integral_constant<int, 1>{}) : launch(std::integral_constant<int, 4>{});
+    };
+    // Rows that a wave's lanes hold by element: 60000 tokens of 4 rows of 64 fp16 28 us against 34, of 63 fp32 46 against
+    // 57 (but of 64 fp32, whole units, 40 against 37).
+    return with_act_type(dtype, [&](auto t) {
+        if (N <= kWave && (sizeof(t) == 2 || N % (16 / sizeof(t)) != 0))
+            return run(t, std::integral_constant<int, 1>{}, std::false_type{}, std::false_type{});
+        return with_row_unit(t, T, topk, N, run);
     });
 }
 

@@ -426,9 +426,9 @@ __global__ __launch_bounds__(256) void w8a8_join_kernel(const int32_t* __restric
                                                         int64_t M, int N, TO* __restrict__ y) {
     const int64_t units = M * N / V, step = (int64_t)gridDim.x * 256;
     for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += step) {
-        Pack<int32_t, V> sum = load_unit<true>(reinterpret_cast<const Pack<int32_t, V>*>(sums) + u);
+        Pack<int32_t, V> sum = load_unit<true, false, V>(sums + V * u);
         for (int p = 1; p < parts; ++p) {
-            const Pack<int32_t, V> more = load_unit<true>(reinterpret_cast<const Pack<int32_t, V>*>(sums) + p * units + u);
+            const Pack<int32_t, V> more = load_unit<true, false, V>(sums + V * (p * units + u));
 #pragma unroll
             for (int i = 0; i < V; ++i) sum.v[i] += more.v[i];
         }
@@ -587,7 +587,7 @@ Plan plan_product(int64_t M, int64_t N, int64_t K, bool experts, int64_t E, size
         const double tiles = share.row_tiles(C::BM) * (double)((N + C::BN - 1) / C::BN);
         const bool once = weights_once<C>(share, N, K);
         const int most = experts || C::WK > 1 || C::BM * C::BN < 64 * 64 || room == 0 || ktiles < 32 ? 0 : 3;
-        for (int log = 0; log <= most; ++log) {  // (host time counts here: a launch is 3.4 us)
+        for (int log = 0; log <= most; ++log) {  // (a plan takes 0.1 us of host time, a launch 3.4)
             const int parts = 1 << log;
             const int64_t part = (ktiles + parts - 1) >> log;
             if (parts > 1 && (tiles * parts > 512 || part < 16 || part * (parts - 1) >= ktiles || sums_bytes(M, N, parts) > room))

@@ -93,6 +93,9 @@ def test_sort_without_src():
 
 ROWS = [(1, 1, 1, 8), (4, 2, 8, 4096), (37, 3, 5, 1), (37, 3, 5, 1001), (200, 8, 64, 520), (513, 5, 16, 72), (9, 20, 30, 24),
         (33, 2, 4, 9000)]
+# rows that are not whole 16-byte units: an element past them, one short of them, of many units, of more than 64 MiB
+ROWS += [(70, 2, 8, 4), (70, 3, 8, 9), (41, 2, 5, 15), (300, 4, 9, 63), (300, 4, 9, 65), (55, 2, 6, 511), (129, 2, 4, 517), (20, 3, 4, 2049),
+         (33, 2, 4, 9001), (4200, 2, 4, 4099)]
 
 
 def plan(T, topk, E, seed, pad=0.2):
@@ -211,6 +214,23 @@ def test_combine_ignores_pairs_without_a_row():
     y = y.cpu()
     assert y[5, 0].isnan() and not y[5, 1:].isnan().any() and not y[:5].isnan().any() and (y[1] == 0).all()
     assert torch.allclose(y[3], wt[3, 1] * ys[4]) and torch.allclose(y[4], wt[4, 0] * ys[5])
+
+
+@pytest.mark.parametrize("N", [4, 9, 13, 40, 69, 1003])
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_infinities_at_the_ends_of_rows(N, kind):
+    """An infinity in a row's first or last elements counts once in its dot product and reaches no other row."""
+    act, dt = TYPES[kind][:2]
+    T, pos = 4, torch.tensor([[0, 1], [2, 3], [4, 5], [6, 7]], dtype=torch.int32, device="cuda")
+    dy, ys = torch.ones((T, N), dtype=dt), torch.ones((8, N), dtype=dt)
+    ys[0, N - 1], ys[2, N - 2], ys[5, 0], ys[6, N // 2] = float("inf"), -float("inf"), float("inf"), float("inf")
+    dw = torch.empty((T, 2), device="cuda")
+    w.w4a16_expert_combine_backward(act, dy.cuda(), ys.cuda(), T, 2, pos, None, N, None, dw)
+    inf = float("inf")
+    assert dw.tolist() == [[inf, N], [-inf, N], [N, inf], [inf, N]]  # (sums of ones are exact)
+    y = torch.empty((T, N), dtype=dt, device="cuda")
+    w.w4a16_expert_combine(act, ys.cuda(), T, 2, pos, None, N, y)
+    assert torch.equal(y.cpu(), ys[0::2] + ys[1::2])
 
 
 @pytest.mark.parametrize("T,topk,E,N", ROWS)

@@ -73,29 +73,32 @@ struct Tiling {
     static constexpr int kWaveCopies = (kCopies + NW - 1) / NW;  // (the last ones may be made twice)
 };
 
-// Rows leave through LDS (pitch: 16 TN outputs and 16 bytes) as 16-byte chunks of consecutive columns
-// where rows of y are whole chunks, else element by element.
+// Rows leave through LDS (pitch: 16 TN outputs and 16 bytes) as 16-byte chunks of consecutive columns, at any
+// element where rows of y are not whole chunks; a row's last outputs then go one by one (4000 x 4098 of K = 1024 35 us
+// against 41 with every output by itself).
 template <typename TO, int TN>
 __device__ __forceinline__ void store_rows(const char* buf, TO* y, int N, int m0, int n0, int row_end) {
     constexpr int kPitch = 16 * TN * sizeof(TO) + 16;
     constexpr int V = 16 / sizeof(TO), kChunks = 16 * TN / V;  // chunks per row
     const int lane = lane_id();
-    if (N % V == 0) {
+    auto chunks = [&](auto any) __attribute__((always_inline)) {
+        constexpr bool kAny = decltype(any)::value;
 #pragma unroll
         for (int i = 0; i < (16 * kChunks + 63) / 64; ++i) {
             const int c = lane + 64 * i, r = c / kChunks, n = n0 + V * (c % kChunks);
-            if (r < 16 && m0 + r < row_end && n < N)
-                *reinterpret_cast<uint4*>(y + (size_t)(m0 + r) * N + n) =
-                    *reinterpret_cast<const uint4*>(buf + r * kPitch + 16 * (c % kChunks));
-        }
-    } else {
+            if (r >= 16 || m0 + r >= row_end || n >= N) continue;
+            const Pack<TO, V> out = *reinterpret_cast<const Pack<TO, V>*>(buf + r * kPitch + 16 * (c % kChunks));
+            TO* p = y + (size_t)(m0 + r) * N + n;
+            if (!kAny || n + V <= N) {
+                store_unit<false, kAny>(p, out);
+            } else {
 #pragma unroll
-        for (int i = 0; i < 4 * TN; ++i) {
-            const int c = lane + 64 * i, r = c / (16 * TN), n = n0 + c % (16 * TN);
-            if (m0 + r < row_end && n < N)
-                y[(size_t)(m0 + r) * N + n] = *reinterpret_cast<const TO*>(buf + r * kPitch + (c % (16 * TN)) * sizeof(TO));
+                for (int k = 0; k < V; ++k)
+                    if (n + k < N) p[k] = out.v[k];
+            }
         }
-    }
+    };
+    N % V == 0 ? chunks(std::false_type{}) : chunks(std::true_type{});
 }
 
 // An output before its last rounding: the sum times the weight row's scale, then the activation row's, each

@@ -422,7 +422,8 @@ __global__ __launch_bounds__(64 * C::NW) void w8a8_tile_kernel(const void* __res
     }
 }
 
-// Reads bound it (512 x 4096 in two parts: 3-4 us).  y = (the parts' sums, [parts][M N]) * s_n * a_m: exactly what the unsplit product stores.  V columns a thread.
+// Reads bound it (512 x 4096 in two parts: 3-4 us).  y = (the parts' sums, [parts][M N]) * s_n * a_m: exactly what the
+// unsplit product stores.  V columns a thread.
 template <typename TO, int V>
 __global__ __launch_bounds__(256) void w8a8_join_kernel(const int32_t* __restrict__ sums, int parts,
                                                         const float* __restrict__ ascale, const float* __restrict__ scales,
@@ -503,8 +504,8 @@ hipError_t launch_tiles(const Product& p, TO* y) {
     return launch(std::false_type{});
 }
 
-// K in `parts`, one launch for the sums and one that joins them: 100 / 256 / 512 rows of 4096 x 14336 18.6 / 25.6 / 39.8
-// us against 32.6 / 32.8 / 43.4 unsplit.
+// K in `parts`, one launch for the sums and one that joins them: 100 / 256 / 512 rows of 4096 x 14336 19.3 / 25.9 / 40.1
+// us against 29.1 / 32.8 / 42.9 unsplit.
 template <typename C, typename TO>
 hipError_t launch_parts(const Product& p, TO* y, int parts) {
     const int64_t tn = (p.N + C::BN - 1) / C::BN;

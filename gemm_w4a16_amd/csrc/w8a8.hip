@@ -596,9 +596,10 @@ Plan plan_product(int64_t M, int64_t N, int64_t K, bool experts, int64_t E, size
             const int64_t part = (ktiles + parts - 1) >> log;
             if (parts > 1 && (tiles * parts > 512 || part < 16 || part * (parts - 1) >= ktiles || sums_bytes(M, N, parts) > room))
                 break;
-            // the parts' sums are written and read once, and joined by a second launch
+            // the parts' sums are written and read once, and joined by a second launch; a part's weights are copied
+            // in the caches' usual order (launch_parts)
             const double join = parts > 1 ? kJoinUs + 2.0 * sums_bytes(M, N, parts) / kJoinBytesPerUs : 0.0;
-            const double us = cost.us(tiles * parts, part * 128, weight_bytes, once) + join;
+            const double us = cost.us(tiles * parts, part * 128, weight_bytes, once && parts == 1) + join;
             if (plan.tiling < 0 || us < least) plan = Plan{i, parts}, least = us;
         }
     });

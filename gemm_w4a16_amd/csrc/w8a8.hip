@@ -645,26 +645,44 @@ using F16x32 = Tiling<1, 2, 2, 1, 1, 4, 1, false>;
 using F16x16 = Tiling<1, 1, 4, 1, 1, 6, 1, false>;
 using F16x16K8 = Tiling<1, 1, 8, 1, 1, 2, 1, false>;
 
-// One launch for activations where quantizing them in every block costs less than a launch of its own:
-//  - one or two rows (each block quantizes all of x, so the work grows with every row: at K = 4096, N = 14336 one
-//    row takes 10.6 us against 13.5 in two launches, two rows 11.8 against 13.8, four 16.2 against 13.6), which
-//    take few enough bytes that the blocks of a CU keep their number.  16 columns a block where that leaves
-//    no CU more than one block (4096 columns of K = 4096: 5.8 us against 6.8), else 32 (14336: 10.6 against 13.5);
-//  - up to 256 tiles of 16 rows x 16 columns, a CU each, of few enough activations (8 rows x 4096 columns of K =
-//    2048 5.2 us against 6.9, 37 x 1001 of K = 1024 5.6 against 6.5, 16 x 4096 of K = 2048 7.0 either way,
-//    37 x 1001 of K = 2064 8.4 against 7.5).
-constexpr int64_t kFusedRows = 2;
-constexpr size_t kFusedBytes = 48 << 10;
-constexpr int64_t kFusedTileActs = 32 << 10;
-constexpr size_t kLdsBytes = (160 << 10) - 1024;  // (1 KB: scales and maxima)
+// One launch for activations where quantizing them in every block costs less than a launch of its own (weights from
+// HBM; us of one launch against two):
+//  - one or two rows, in tiles as wide as leave no CU more than one block (16 columns up to N = 4096: K = 4096, N =
+//    4096, bf16 6.4 against 9.8, two rows 7.6 against 9.5), else 32 columns (N = 14336 14.1 against 18.1, two rows
+//    15.0 against 19.1).  More than one block a CU wants room for two at once (two rows of K = 8192, one block at a
+//    time: N = 14336 31.1 against 25.6, N = 28672 59.1 against 48.6), and a CU that quantizes at most eight rows
+//    in all (two rows of K = 1024, N = 57344 18.5 against 16.1, N = 131072 34.5 against 26.1; K = 4096, N = 28672
+//    25.1 against 28.9);
+//  - up to 256 tiles of 16 rows x 16 columns, a CU each.  A wave quantizes whole rows, so beyond two rows short ones
+//    and few activations in all (bf16, N = 4096: 4 rows of K = 2048 6.5 against 8.1, of 4096 9.7 against 9.4, of 8192
+//    16.6 against 13.8; 8 of 2048 7.5 against 8.4; 16 of 1024 6.9 against 7.3, of 1360 10.0 against 8.5; fp32 16 of
+//    1360 7.4 against 7.9, 3 of 8192 19.7 against 12.7); one or two rows, by all eight waves, up to 96 KB (bf16
+//    32768 of K, N = 2048 30.2 against 37.6, fp32 16384 15.5 against 18.8, 24576 25.9 against 22.6).
+constexpr int64_t kFusedRows = 2, kFusedRowsPerCU = 8;
+constexpr size_t kFusedBytes = 48 << 10, kFusedLongBytes = 96 << 10;
+constexpr int64_t kFusedTileK = 2816;
+constexpr size_t kLdsBytes = 160 << 10, kFusedLdsMore = 1 << 10;  // (scales and maxima)
 template <typename TO>
 auto fused_launch(const Product& p) -> hipError_t (*)(const Product&, TO*) {
-    if (p.M <= kFusedRows && fused_bytes<TO>(p, 4) <= kFusedBytes)
-        return p.N <= 16 * 256 ? launch_fused_tiles<F16x16, TO> : launch_fused_tiles<F16x32, TO>;
+    // Blocks that fit a CU at once, by their LDS.
+    auto blocks = [&](auto tiling) {
+        using C = decltype(tiling);
+        return kLdsBytes / (fused_bytes<TO>(p, C::WK) + C::R * C::kUnitBytes + kFusedLdsMore);
+    };
+    if (p.M <= kFusedRows) {
+        if (p.N <= 16 * 256) {
+            if (fused_bytes<TO>(p, F16x16::WK) <= kFusedBytes) return launch_fused_tiles<F16x16, TO>;
+        } else if (fused_bytes<TO>(p, F16x32::WK) <= kFusedBytes) {
+            const int64_t tiles = launch_blocks<F16x32>(p.M, p.N, false, 1);
+            if (blocks(F16x32{}) >= (tiles > 256 ? 2 : 1) && tiles * p.M <= 256 * kFusedRowsPerCU)
+                return launch_fused_tiles<F16x32, TO>;
+        }
+    }
     using C = F16x16K8;
-    if (launch_blocks<C>(p.M, p.N, false, 1) <= 256 && std::min<int64_t>(p.M, 16) * p.K <= kFusedTileActs &&
-        fused_bytes<TO>(p, C::WK) + C::R * C::kUnitBytes <= kLdsBytes)
-        return launch_fused_tiles<C, TO>;
+    const int64_t rows = std::min<int64_t>(p.M, 16), acts = rows * p.K;
+    const bool few = rows <= kFusedRows ? fused_bytes<TO>(p, C::WK) <= kFusedLongBytes
+                                        : p.K <= kFusedTileK && acts <= (sizeof(TO) == 2 ? 16 : 24) << 10;
+    if (few && launch_blocks<C>(p.M, p.N, false, 1) <= 256 && blocks(C{}) >= 1) return launch_fused_tiles<C, TO>;
     return nullptr;
 }
 

@@ -236,29 +236,29 @@ def w4a16_matmul_w4a8(fmt: int, x, M: int, codes, scales, mins, N: int, K: int, 
 
 
 # ---- W8A8 and the experts' operators --------------------------------------------------------------
-# Tensors given to these must be on one GPU, contiguous, of elements as wide as the call takes them and at
-# least as large as it reads or writes (W4A16_ERR_INVALID otherwise); the launch goes to that GPU's current
-# stream, whichever GPU is current.  Raw addresses are passed as they are.
+# Tensors given to these must be on one GPU, contiguous, of the type the call takes them as and at least as
+# large as it reads or writes (W4A16_ERR_INVALID otherwise); the launch goes to that GPU's current stream,
+# whichever GPU is current.  Raw addresses are passed as they are.
 
-_ELEMENT = {W4A16_BF16: 2, W4A16_FP16: 2, W4A16_FP32: 4}
+import torch  # noqa: E402 (loaded with the library, above)
 
-
-def _element(dtype: int) -> int:
-    return _ELEMENT.get(dtype, 0)  # an unknown type is refused by the library
+_I8, _I32, _F32 = torch.int8, torch.int32, torch.float32
+_ACT = {W4A16_BF16: torch.bfloat16, W4A16_FP16: torch.float16, W4A16_FP32: _F32}.get  # None: the library refuses it
+_ID = {32: _I32, 64: torch.int64}.get
 
 
 def _call(name: str, args, arrays, stream) -> None:
     """lib.<name>(*args, stream): ``arrays`` gives the array arguments' places in ``args``, the elements
-    each must hold and their bytes (0: any)."""
+    each must hold and their type (None: any, and that many bytes)."""
     device = None
     args = list(args)
-    for at, count, width in arrays:
+    for at, count, dtype in arrays:
         t = args[at]
         if t is None or isinstance(t, int):
             continue
         d = t.get_device()
-        if (d != device and (d < 0 or device is not None) or t.nbytes < count * (width or 1)
-                or (width and t.element_size() != width) or not t.is_contiguous()):
+        if (d != device and (d < 0 or device is not None) or (t.nbytes if dtype is None else t.numel()) < count
+                or (dtype is not None and t.dtype is not dtype) or not t.is_contiguous()):
             raise W4A16Error(W4A16_ERR_INVALID, name)
         device = d
         args[at] = t.data_ptr()
@@ -268,7 +268,6 @@ def _call(name: str, args, arrays, stream) -> None:
     elif device == _current_device():
         status = fn(*args, _current_stream(device) if stream is None else _stream(stream))
     else:
-        import torch
         with torch.cuda.device(device):
             status = fn(*args, _stream(stream))
     if status != W4A16_OK:
@@ -277,21 +276,21 @@ def _call(name: str, args, arrays, stream) -> None:
 
 def w4a16_quantize_rows_i8(act: int, x, M: int, K: int, xq, ascale, stream=None) -> None:
     _call("w4a16_quantize_rows_i8", (act, x, M, K, xq, ascale),
-          ((1, M * K, _element(act)), (4, M * K, 1), (5, M, 4)), stream)
+          ((1, M * K, _ACT(act)), (4, M * K, _I8), (5, M, _F32)), stream)
 
 
 def w4a16_gemm_w8a8(fmt: int, out: int, xq, ascale, M: int, codes, scales, mins, N: int, K: int, y, workspace=None,
                     workspace_bytes: int = 0, stream=None) -> None:
     _call("w4a16_gemm_w8a8", (fmt, out, xq, ascale, M, codes, scales, mins, N, K, y, workspace, workspace_bytes),
-          ((2, M * K, 1), (3, M, 4), (5, N * K, 1), (6, N, 4), (7, 0, 0), (10, M * N, _element(out)),
-           (11, workspace_bytes, 0)), stream)
+          ((2, M * K, _I8), (3, M, _F32), (5, N * K, _I8), (6, N, _F32), (7, 0, None), (10, M * N, _ACT(out)),
+           (11, workspace_bytes, None)), stream)
 
 
 def w4a16_matmul_w8a8(fmt: int, act: int, x, M: int, codes, scales, mins, N: int, K: int, y, workspace,
                       workspace_bytes: int, stream=None) -> None:
-    b = _element(act)
+    t = _ACT(act)
     _call("w4a16_matmul_w8a8", (fmt, act, x, M, codes, scales, mins, N, K, y, workspace, workspace_bytes),
-          ((2, M * K, b), (4, N * K, 1), (5, N, 4), (6, 0, 0), (9, M * N, b), (10, workspace_bytes, 0)), stream)
+          ((2, M * K, t), (4, N * K, _I8), (5, N, _F32), (6, 0, None), (9, M * N, t), (10, workspace_bytes, None)), stream)
 
 
 def w4a16_w8a8_workspace_bytes(fmt: int, M: int, N: int, K: int) -> int:
@@ -301,8 +300,8 @@ def w4a16_w8a8_workspace_bytes(fmt: int, M: int, N: int, K: int) -> int:
 def w4a16_gemm_w8a8_experts(fmt: int, out: int, xq, ascale, R: int, offsets, E: int, codes, scales, mins, N: int, K: int,
                             y, stream=None) -> None:
     _call("w4a16_gemm_w8a8_experts", (fmt, out, xq, ascale, R, offsets, E, codes, scales, mins, N, K, y),
-          ((2, R * K, 1), (3, R, 4), (5, E + 1, 4), (7, E * N * K, 1), (8, E * N, 4), (9, 0, 0),
-           (12, R * N, _element(out))), stream)
+          ((2, R * K, _I8), (3, R, _F32), (5, E + 1, _I32), (7, E * N * K, _I8), (8, E * N, _F32), (9, 0, None),
+           (12, R * N, _ACT(out))), stream)
 
 
 def w4a16_max_experts() -> int:
@@ -317,31 +316,31 @@ def w4a16_expert_sort(ids, id_bits: int, T: int, topk: int, E: int, offsets, pos
                       workspace_bytes: int = 0, stream=None) -> None:
     P = T * topk
     _call("w4a16_expert_sort", (ids, id_bits, T, topk, E, offsets, pos, src, workspace, workspace_bytes),
-          ((0, P, id_bits // 8), (5, E + 1, 4), (6, P, 4), (7, P, 4), (8, workspace_bytes, 0)), stream)
+          ((0, P, _ID(id_bits)), (5, E + 1, _I32), (6, P, _I32), (7, P, _I32), (8, workspace_bytes, None)), stream)
 
 
 def w4a16_expert_gather(act: int, x, T: int, topk: int, pos, K: int, xs, stream=None) -> None:
-    P, b = T * topk, _element(act)
-    _call("w4a16_expert_gather", (act, x, T, topk, pos, K, xs), ((1, T * K, b), (4, P, 4), (6, P * K, b)), stream)
+    P, t = T * topk, _ACT(act)
+    _call("w4a16_expert_gather", (act, x, T, topk, pos, K, xs), ((1, T * K, t), (4, P, _I32), (6, P * K, t)), stream)
 
 
 def w4a16_expert_gather_i8(act: int, x, T: int, topk: int, pos, K: int, xq, ascale, stream=None) -> None:
     P = T * topk
     _call("w4a16_expert_gather_i8", (act, x, T, topk, pos, K, xq, ascale),
-          ((1, T * K, _element(act)), (4, P, 4), (6, P * K, 1), (7, P, 4)), stream)
+          ((1, T * K, _ACT(act)), (4, P, _I32), (6, P * K, _I8), (7, P, _F32)), stream)
 
 
 def w4a16_expert_combine(act: int, ys, T: int, topk: int, pos, weights, N: int, y, stream=None) -> None:
-    P, b = T * topk, _element(act)
+    P, t = T * topk, _ACT(act)
     _call("w4a16_expert_combine", (act, ys, T, topk, pos, weights, N, y),
-          ((1, P * N, b), (4, P, 4), (5, P, 4), (7, T * N, b)), stream)
+          ((1, P * N, t), (4, P, _I32), (5, P, _F32), (7, T * N, t)), stream)
 
 
 def w4a16_expert_combine_backward(act: int, dy, ys, T: int, topk: int, pos, weights, N: int, dys, dweights,
                                   stream=None) -> None:
-    P, b = T * topk, _element(act)
+    P, t = T * topk, _ACT(act)
     _call("w4a16_expert_combine_backward", (act, dy, ys, T, topk, pos, weights, N, dys, dweights),
-          ((1, T * N, b), (2, P * N, b), (5, P, 4), (6, P, 4), (8, P * N, b), (9, P, 4)), stream)
+          ((1, T * N, t), (2, P * N, t), (5, P, _I32), (6, P, _F32), (8, P * N, t), (9, P, _F32)), stream)
 
 
 # ---- memory plumbing (torch allocations with the ABI's shapes and dtypes) ------------------------

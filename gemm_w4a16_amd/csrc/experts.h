@@ -86,11 +86,7 @@ __device__ __forceinline__ void store_unit(T* p, const Pack<T, V>& u) {
 
 // ---- int8 quantization of a row -------------------------------------------------------------------
 
-// Bits of |v| as an unsigned integer of the type's own width: these order like the magnitudes, with
-// infinity above every finite value and NaN above infinity.
-__device__ __forceinline__ uint32_t abs_bits(bf16_t v) { return v.bits & 0x7FFFu; }
-__device__ __forceinline__ uint32_t abs_bits(f16_t v) { return v.bits & 0x7FFFu; }
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+// The value whose magnitude has these bits.
 __device__ __forceinline__ float from_abs_bits(uint32_t b, bf16_t) { return bf16_bits_to_f32(b); }
 __device__ __forceinline__ float from_abs_bits(uint32_t b, f16_t) { return f16_bits_to_f32(b); }
 __device__ __forceinline__ float from_abs_bits(uint32_t b, float) { return __uint_as_float(b); }
@@ -114,7 +110,8 @@ template <typename T>
 struct alignas(16) Act16 {
     T v[16];
 };
-// (16-bit types: the two halves of a word at once; fold_max joins them.)
+// The bits of |v| as an unsigned integer of the type's own width order like the magnitudes, with infinity above every
+// finite value and NaN above infinity.  (16-bit types: the two halves of a word at once; fold_max joins them.)
 typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 template <typename T>
 __device__ __forceinline__ uint32_t max_bits(const Act16<T>& x, uint32_t m) {
@@ -126,7 +123,7 @@ __device__ __forceinline__ uint32_t max_bits(const Act16<T>& x, uint32_t m) {
                                                                        __builtin_bit_cast(u16x2_t, w[j] & 0x7FFF7FFFu)));
     } else {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) m = max(m, abs_bits(x.v[j]));
+        for (int j = 0; j < 16; ++j) m = max(m, __float_as_uint(x.v[j]) & 0x7FFFFFFFu);
     }
     return m;
 }

@@ -99,7 +99,7 @@ __device__ __forceinline__ float scale_i8(float amax) {
     return a == 0.0f ? 1.0f : a;
 }
 
-// rint(v / a), ties to even, clamped to +-127; 0 where a is NaN.
+// rint(v / a), ties to even, clamped to +-127 (a not NaN).
 __device__ __forceinline__ uint32_t code_i8(float v, float a) {
     const float r = rintf(v / a);
     return (uint32_t)(int)fminf(fmaxf(r, -127.0f), 127.0f) & 0xFFu;

@@ -56,11 +56,12 @@ __global__ __launch_bounds__(256) void quant_rows_i8_kernel(const T* __restrict_
 // What bounds it.  Many rows: the matrix cores at the clock the power limit leaves.  At 1024 x 14336 x 4096 (T256x256,
 // 53 us, 2.27 POP/s; hipBLASLt's int8 product 73 us) timing-only copies took 43 us without the copies inside the
 // loop and 49 with all of them reading one line, and the matrix instructions alone on such data take 36; waiting
-// for the copies costs nothing.  8192 rows: 393 us (2.45 POP/s; hipBLASLt 426).  Eight waves of 128 x 64 rather than
-// four of 128 x 128 (64 us): two waves per SIMD fill each other's gaps.  16x16x64 instructions rather than
-// 32x32x32: 3.8 POP/s against 3.3 on random codes.  Few rows: the weights' bytes.  One row, 14336 x 4096: 10.5
-// us from the Infinity Cache (5.6 TB/s), 14.1 from HBM; 16 rows over eight such matrices 63 us (7.4 TB/s).
-// Few columns: each block's own chain of k-tiles, which K in parts shortens (launch_parts).
+// for the copies costs nothing.  8192 rows: 376-393 us (2.45-2.56 POP/s; hipBLASLt 426-430).  Eight waves of 128 x 64
+// rather than four of 128 x 128 (64 us): two waves per SIMD fill each other's gaps.  16x16x64 instructions rather
+// than 32x32x32: 3.8 POP/s against 3.3 on random codes.  Few rows: the weights' bytes.  One row, 14336 x 4096:
+// 14.1 us from HBM (4.2 TB/s), 11 from the Infinity Cache (5.3 TB/s); two rows for each of eight such matrices 79
+// us (5.9 TB/s).  Few columns: each block's own chain of k-tiles, which K in parts shortens (launch_parts).  Short
+// rows (K of 500 to 1000): a block's first copies and its outputs, which nothing hides (1621 x 19712 x 512 36 us).
 template <int WM_, int WN_, int WK_, int TM_, int TN_, int R_, int U_ = 1, bool kX = true>
 struct Tiling {
     static constexpr int WM = WM_, WN = WN_, WK = WK_, TM = TM_, TN = TN_, R = R_, U = U_;
@@ -113,9 +114,10 @@ __device__ __forceinline__ float scaled_sum(int32_t sum, float sn, float am) {
 
 // Weights that one row tile reads (a tile of at most kOnceRows rows holds them all) and that take more than a
 // quarter of the Infinity Cache's 256 MiB, so that they would hardly be there at the next call, are copied
-// past it (kOnce): eight matrices of 14336 x 4096 for 16 rows take 63.4 us against 71.5, two of them 23.4
-// against 26.4.  One of them alone (56 MiB), called again while the cache holds it, takes 11.8 us so against
-// 10.5; called when it does not, 12.3 against 14.1.
+// past it (kOnce): eight matrices of 14336 x 4096 for two rows each take 79 us against 87, two of them, from HBM, 25.8
+// against 28.6, and one row of 28672 x 4096 26.6 against 29.0 (while the cache holds it 25.8 against 21.1).  Below, one
+// row of 14336 x 4096 (56 MiB) takes 12.6 us so against 14.2 from HBM, and 11.9 against 11.0 where it shares the cache
+// with two more such matrices.
 constexpr int kOnceRows = 64;
 constexpr double kOnceBytes = 64 << 20;
 
@@ -504,8 +506,8 @@ hipError_t launch_tiles(const Product& p, TO* y) {
     return launch(std::false_type{});
 }
 
-// K in `parts`, one launch for the sums and one that joins them: 100 / 256 / 512 rows of 4096 x 14336 19.3 / 25.9 / 40.1
-// us against 29.1 / 32.8 / 42.9 unsplit.
+// K in `parts`, one launch for the sums and one that joins them: 100 / 512 rows of 4096 x 14336, weights from HBM, 22.2 /
+// 45.1 us against 30.2 / 54.7 unsplit.
 template <typename C, typename TO>
 hipError_t launch_parts(const Product& p, TO* y, int parts) {
     const int64_t tn = (p.N + C::BN - 1) / C::BN;
@@ -535,7 +537,8 @@ constexpr double kJoinUs = 3.0, kJoinBytesPerUs = 5e6;
 // rows and 290 of 4 to 256 experts: the choice is on average 1% slower than the fastest tiling for one matrix
 // and 2% for experts, whose row counts are not known here, and within 10% of it in 464 of the 490.  (With
 // us_first also for further blocks, and time as the larger of the two, 2% and 11%, and up to 2.9 times the
-// fastest where K is short.)
+// fastest where K is short.)  It ranks tilings and does not predict times: the clock falls under large products
+// (1024 x 14336 x 4096 39.8 us by it, 54 measured), and 7.3 counts the weights of experts that have no rows.
 struct Cost {
     double us_ktile, us_first, next_ktile, us_next;
     int blocks;

@@ -30,6 +30,7 @@ EXPORTED = (
     "w4a16_quantize_rows_i8", "w4a16_gemm_w8a8", "w4a16_matmul_w8a8", "w4a16_w8a8_workspace_bytes",
     "w4a16_gemm_w8a8_experts", "w4a16_max_experts", "w4a16_expert_sort", "w4a16_expert_sort_workspace_bytes",
     "w4a16_expert_gather", "w4a16_expert_gather_i8", "w4a16_expert_combine", "w4a16_expert_combine_backward",
+    "w4a16_add_rmsnorm", "w4a16_add_rmsnorm_i8", "w4a16_add_rmsnorm_backward", "w4a16_add_rmsnorm_backward_workspace_bytes",
 )
 
 
@@ -50,7 +51,7 @@ def _load() -> ctypes.CDLL:
     # launch on a torch stream would then fail).
     import torch  # noqa: F401
     L = ctypes.CDLL(str(_LIB_PATH))
-    P, I64, I, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+    P, I64, I, SZ, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
     L.w4a16_status_string.argtypes, L.w4a16_status_string.restype = [I], ctypes.c_char_p
     L.w4a16_packed_sizes.argtypes = [I, I64, I64, ctypes.POINTER(SZ), ctypes.POINTER(SZ), ctypes.POINTER(SZ)]
     L.w4a16_quantize_pack.argtypes = [I, P, I64, I64, P, P, P, P]
@@ -83,9 +84,14 @@ def _load() -> ctypes.CDLL:
     L.w4a16_expert_gather_i8.argtypes = [I, P, I64, I64, P, I64, P, P, P]
     L.w4a16_expert_combine.argtypes = [I, P, I64, I64, P, P, I64, P, P]
     L.w4a16_expert_combine_backward.argtypes = [I, P, P, I64, I64, P, P, I64, P, P, P]
+    L.w4a16_add_rmsnorm.argtypes = [I, P, P, I64, I64, P, F, P, P, P]
+    L.w4a16_add_rmsnorm_i8.argtypes = [I, P, P, I64, I64, P, F, P, P, P, P]
+    L.w4a16_add_rmsnorm_backward.argtypes = [I, P, P, P, I64, I64, P, F, P, P, P, SZ, P]
+    L.w4a16_add_rmsnorm_backward_workspace_bytes.argtypes = [I64, I64]
+    L.w4a16_add_rmsnorm_backward_workspace_bytes.restype = SZ
     for name in ("w4a16_quantize_rows_i8", "w4a16_gemm_w8a8", "w4a16_matmul_w8a8", "w4a16_gemm_w8a8_experts",
                  "w4a16_expert_sort", "w4a16_expert_gather", "w4a16_expert_gather_i8", "w4a16_expert_combine",
-                 "w4a16_expert_combine_backward"):
+                 "w4a16_expert_combine_backward", "w4a16_add_rmsnorm", "w4a16_add_rmsnorm_i8", "w4a16_add_rmsnorm_backward"):
         getattr(L, name).restype = I
     for name in ("w4a16_packed_sizes", "w4a16_quantize_pack", "w4a16_check_weights", "w4a16_dequant", "w4a16_gemv",
                  "w4a16_gemm", "w4a16_matmul", "w4a16_matmul_noalloc", "w4a16_quantize_act_i8", "w4a16_gemm_w4a8",
@@ -235,7 +241,7 @@ def w4a16_matmul_w4a8(fmt: int, x, M: int, codes, scales, mins, N: int, K: int, 
         "w4a16_matmul_w4a8")
 
 
-# ---- W8A8 and the experts' operators --------------------------------------------------------------
+# ---- W8A8, the experts' operators, norms -----------------------------------------------------------
 # Tensors given to these must be on one GPU, contiguous, of the type the call takes them as and at least as
 # large as it reads or writes (W4A16_ERR_INVALID otherwise); the launch goes to that GPU's current stream,
 # whichever GPU is current.  Raw addresses are passed as they are.
@@ -343,6 +349,29 @@ def w4a16_expert_combine_backward(act: int, dy, ys, T: int, topk: int, pos, weig
           ((1, T * N, t), (2, P * N, t), (5, P, _I32), (6, P, _F32), (8, P * N, t), (9, P, _F32)), stream)
 
 
+def w4a16_add_rmsnorm(act: int, x, residual, T: int, N: int, weight, eps: float, h, y, stream=None) -> None:
+    t, n = _ACT(act), T * N
+    _call("w4a16_add_rmsnorm", (act, x, residual, T, N, weight, eps, h, y),
+          ((1, n, t), (2, n, t), (5, N, t), (7, n, t), (8, n, t)), stream)
+
+
+def w4a16_add_rmsnorm_i8(act: int, x, residual, T: int, N: int, weight, eps: float, h, xq, ascale, stream=None) -> None:
+    t, n = _ACT(act), T * N
+    _call("w4a16_add_rmsnorm_i8", (act, x, residual, T, N, weight, eps, h, xq, ascale),
+          ((1, n, t), (2, n, t), (5, N, t), (7, n, t), (8, n, _I8), (9, T, _F32)), stream)
+
+
+def w4a16_add_rmsnorm_backward(act: int, dy, dh, h, T: int, N: int, weight, eps: float, dx, dweight, workspace=None,
+                               workspace_bytes: int = 0, stream=None) -> None:
+    t, n = _ACT(act), T * N
+    _call("w4a16_add_rmsnorm_backward", (act, dy, dh, h, T, N, weight, eps, dx, dweight, workspace, workspace_bytes),
+          ((1, n, t), (2, n, t), (3, n, t), (6, N, t), (8, n, t), (9, N, _F32), (10, workspace_bytes, None)), stream)
+
+
+def w4a16_add_rmsnorm_backward_workspace_bytes(T: int, N: int) -> int:
+    return int(lib.w4a16_add_rmsnorm_backward_workspace_bytes(T, N))
+
+
 # ---- memory plumbing (torch allocations with the ABI's shapes and dtypes) ------------------------
 
 def alloc_packed(fmt: int, N: int, K: int, device="cuda"):
@@ -402,3 +431,10 @@ def alloc_expert_sort(T: int, topk: int, E: int, device="cuda"):
     i32 = lambda *shape: torch.empty(shape, dtype=torch.int32, device=device)
     return (i32(E + 1), i32(T, topk), i32(T * topk),
             torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None, nbytes)
+
+
+def alloc_add_rmsnorm_backward_workspace(T: int, N: int, device="cuda"):
+    """(tensor, bytes) sized for w4a16_add_rmsnorm_backward."""
+    import torch
+    nbytes = w4a16_add_rmsnorm_backward_workspace_bytes(T, N)
+    return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes

@@ -138,6 +138,14 @@ w4a16_status_t check_pairs(int64_t T, int64_t topk, int64_t width) {
     return W4A16_OK;
 }
 
+// Rows of a norm: T of them, N wide; eps finite and not negative.
+w4a16_status_t check_norm(w4a16_dtype_t act, int64_t T, int64_t N, float eps) {
+    if (!valid_dtype(act) || T <= 0 || T > kMaxDim || N <= 0 || N > kMaxDim) return W4A16_ERR_INVALID;
+    if (!(eps >= 0.0f) || !std::isfinite(eps)) return W4A16_ERR_INVALID;
+    return N > kMaxK ? W4A16_ERR_UNSUPPORTED : W4A16_OK;
+}
+bool null_or_aligned16(const void* p) { return p == nullptr || aligned16(p); }
+
 // The W8A8 workspace: the codes of x and its row scales (matmul_w8a8 needs these), then room for the sums of
 // K's parts, each 16-byte aligned.
 struct W8A8Workspace {
@@ -651,6 +659,50 @@ w4a16_status_t w4a16_expert_combine_backward(w4a16_dtype_t act, const void* dy, 
     w4a16::clear_stale_error();
     return from_hip(w4a16::launch_expert_combine_backward((int)act, dy, ys, T, topk, pos, weights, N, dys, dweights,
                                                           stream));
+}
+
+w4a16_status_t w4a16_add_rmsnorm(w4a16_dtype_t act, const void* x, const void* residual, int64_t T, int64_t N,
+                                 const void* weight, float eps, void* h, void* y, hipStream_t stream) {
+    const w4a16_status_t st = check_norm(act, T, N, eps);
+    if (st == W4A16_ERR_INVALID || !aligned16(x) || !aligned16(y)) return W4A16_ERR_INVALID;
+    if (!null_or_aligned16(residual) || !null_or_aligned16(weight) || !null_or_aligned16(h)) return W4A16_ERR_INVALID;
+    if (h != nullptr && h == y) return W4A16_ERR_INVALID;
+    if (st != W4A16_OK) return st;
+    w4a16::clear_stale_error();
+    return from_hip(w4a16::launch_add_rmsnorm((int)act, x, residual, T, N, weight, eps, h, y, nullptr, nullptr, stream));
+}
+
+w4a16_status_t w4a16_add_rmsnorm_i8(w4a16_dtype_t act, const void* x, const void* residual, int64_t T, int64_t N,
+                                    const void* weight, float eps, void* h, int8_t* xq, float* ascale, hipStream_t stream) {
+    const w4a16_status_t st = check_norm(act, T, N, eps);
+    if (st == W4A16_ERR_INVALID || N % kW8RowAlign != 0 || !aligned16(x) || !aligned16(xq) || !aligned16(ascale))
+        return W4A16_ERR_INVALID;
+    if (!null_or_aligned16(residual) || !null_or_aligned16(weight) || !null_or_aligned16(h)) return W4A16_ERR_INVALID;
+    if (st != W4A16_OK) return st;
+    w4a16::clear_stale_error();
+    return from_hip(w4a16::launch_add_rmsnorm((int)act, x, residual, T, N, weight, eps, h, nullptr, xq, ascale, stream));
+}
+
+size_t w4a16_add_rmsnorm_backward_workspace_bytes(int64_t T, int64_t N) {
+    if (check_norm(W4A16_FP32, T, N, 0.0f) != W4A16_OK) return 0;
+    return w4a16::add_rmsnorm_backward_workspace_bytes(T, N);
+}
+
+w4a16_status_t w4a16_add_rmsnorm_backward(w4a16_dtype_t act, const void* dy, const void* dh, const void* h, int64_t T,
+                                          int64_t N, const void* weight, float eps, void* dx, float* dweight, void* workspace,
+                                          size_t workspace_bytes, hipStream_t stream) {
+    const w4a16_status_t st = check_norm(act, T, N, eps);
+    if (st == W4A16_ERR_INVALID || !aligned16(dy) || !aligned16(h) || (dx == nullptr && dweight == nullptr))
+        return W4A16_ERR_INVALID;
+    if (!null_or_aligned16(dh) || !null_or_aligned16(weight) || !null_or_aligned16(dx) || !null_or_aligned16(dweight))
+        return W4A16_ERR_INVALID;
+    if (st != W4A16_OK) return st;
+    if (dweight != nullptr &&
+        (!aligned16(workspace) || workspace_bytes < w4a16::add_rmsnorm_backward_workspace_bytes(T, N)))
+        return W4A16_ERR_INVALID;
+    w4a16::clear_stale_error();
+    return from_hip(w4a16::launch_add_rmsnorm_backward((int)act, dy, dh, h, T, N, weight, eps, dx, dweight,
+                                                       static_cast<float*>(workspace), stream));
 }
 
 }  // extern "C"

@@ -184,4 +184,13 @@ hipError_t launch_expert_combine_backward(int dtype, const void* dy, const void*
                                           const int32_t* pos, const float* weights, int64_t N, void* dys, float* dweights,
                                           hipStream_t stream);
 
+// The RMS norm of rows x + residual (residual, h, weight or null), written to y in the activations' type, or (xq not
+// null, N % 16 == 0) to xq and ascale in 8 bits; its gradients (dh, weight, and dx or dweight or null; ws as
+// add_rmsnorm_backward_workspace_bytes says, for dweight).
+hipError_t launch_add_rmsnorm(int dtype, const void* x, const void* residual, int64_t rows, int64_t N, const void* weight,
+                              float eps, void* h, void* y, int8_t* xq, float* ascale, hipStream_t stream);
+size_t add_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t N);
+hipError_t launch_add_rmsnorm_backward(int dtype, const void* dy, const void* dh, const void* h, int64_t rows, int64_t N,
+                                       const void* weight, float eps, void* dx, float* dweight, float* ws, hipStream_t stream);
+
 }  // namespace w4a16

@@ -1,0 +1,464 @@
+// norm.hip -- RMS norm of rows with a residual added first, in the activations' type or in 8-bit integers with a
+// scale per row (what the int8 products take), and its gradients.
+//
+// Row t of T, width N:  s = x + residual (fp32),  h = s rounded to the activations' type,
+//     r = 1 / sqrt(sum_n s_n^2 / N + eps),   v_n = (s_n r) w_n   (fp32),   y = v rounded once;
+// in 8 bits a = max|v| / 127, q = clamp(rint(v / a), -127, 127).  The norm is of the sum as it is in fp32, not of
+// the rounded h: h is what goes on, and one rounding of y is enough.
+// Gradients, of y = norm(h) for the h that was stored (g = dy w, r from h):
+//     dx = r (g - h r^2 sum_n(g h) / N) + dh,   dw_n = sum_t dy h r.
+//
+// Bytes bound all of these for many rows, and a row's chain of two reductions for few.  A row stays in registers
+// between its passes (kKeep units of 16 bytes a thread); what a long row has beyond that is read again, from the
+// caches.
+#include <algorithm>
+#include <type_traits>
+
+#include "device_common.h"
+#include "experts.h"
+#include "launch.h"
+
+namespace w4a16 {
+
+namespace {
+
+constexpr int kKeep = 4;  // units of a row that a thread holds
+
+template <typename T>
+constexpr int kUnit = 16 / (int)sizeof(T);
+
+// Unit c of a row of N elements as fp32: elements past the row's end are zero.  kAny: rows start at any element.
+template <bool kAny, typename T>
+__device__ __forceinline__ void load_row_unit(const T* row, int c, int N, float (&f)[kUnit<T>]) {
+    constexpr int V = kUnit<T>;
+    Pack<T, V> u;
+    if (!kAny || (c + 1) * V <= N) {
+        u = load_unit<false, kAny, V>(row + c * V);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) u.v[j] = c * V + j < N ? row[c * V + j] : from_f32<T>(0.0f);
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = to_f32(u.v[j]);
+}
+template <bool kAny, typename T>
+__device__ __forceinline__ void store_row_unit(T* row, int c, int N, const float (&f)[kUnit<T>]) {
+    constexpr int V = kUnit<T>;
+    Pack<T, V> u;
+#pragma unroll
+    for (int j = 0; j < V; ++j) u.v[j] = from_f32<T>(f[j]);
+    if (!kAny || (c + 1) * V <= N) {
+        store_unit<false, kAny>(row + c * V, u);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (c * V + j < N) row[c * V + j] = u.v[j];
+    }
+}
+
+// A sum or maximum over the threads of a row, the same in each: lanes, then waves in order.  red: a word per wave.
+template <int kWaves>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+    v = wave_sum(v);
+    if constexpr (kWaves > 1) {
+        __syncthreads();  // red may still be read
+        if (lane_id() == 0) red[wave_id()] = v;
+        __syncthreads();
+        v = red[0];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) v += red[w];
+    }
+    return v;
+}
+// (of magnitudes' bits, which order like the magnitudes, infinity above every finite value and NaN above infinity)
+template <int kWaves>
+__device__ __forceinline__ uint32_t row_max(uint32_t m, float* red) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off));
+    if constexpr (kWaves > 1) {
+        __syncthreads();
+        if (lane_id() == 0) red[wave_id()] = __uint_as_float(m);
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) m = max(m, __float_as_uint(red[w]));
+    }
+    return m;
+}
+
+// The 8-bit codes of V values by a product with inv = 1 / a where that cannot differ from the division (codes16 has the
+// argument); else by the division, and zero where a is NaN.
+template <int V>
+__device__ __forceinline__ void codes_i8(const float (&v)[V], float a, float inv, uint32_t (&w)[V / 4]) {
+    constexpr float kMagic = 12582912.0f;
+    float far = a >= 0x1p-100f ? 0.0f : 1.0f;  // largest distance from a code
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+        uint32_t b[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float t = __builtin_fmaf(v[4 * i + j], inv, kMagic);
+            far = fmaxf(far, fabsf(__builtin_fmaf(v[4 * i + j], inv, kMagic - t)));
+            b[j] = __float_as_uint(t);
+        }
+        w[i] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0C0C0400u), __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u),
+                                     0x05040100u);
+    }
+    if (!(far <= 0.4999f)) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) w[i] = 0;
+        if (a != a) return;
+#pragma unroll
+        for (int j = 0; j < V; ++j) w[j / 4] |= code_i8(v[j], a) << (8 * (j % 4));
+    }
+}
+
+// x, residual, h and y may be the same memory: a thread reads a unit of x and residual before it writes that unit of h
+// and y, in each pass, and no other thread's.
+template <typename T, int kWaves, bool kI8, bool kAny>
+__global__ __launch_bounds__(256) void add_rmsnorm_kernel(const T* x, const T* residual, int64_t rows, int N,
+                                                          const T* __restrict__ weight, float eps, T* h, T* y,
+                                                          int8_t* __restrict__ xq, float* __restrict__ ascale) {
+    constexpr int V = kUnit<T>, kThreads = 64 * kWaves, kRows = 4 / kWaves;
+    __shared__ float red[kWaves];
+    const int tid = kWaves == 1 ? lane_id() : (int)threadIdx.x;
+    const int units = (N + V - 1) / V;
+    for (int64_t m0 = (int64_t)blockIdx.x * kRows; m0 < rows; m0 += (int64_t)gridDim.x * kRows) {
+        const int64_t m = kWaves == 1 ? m0 + wave_id() : m0;
+        if (kWaves == 1 && m >= rows) continue;
+        const T* xr = x + m * N;
+        const T* rr = residual ? residual + m * N : nullptr;
+        auto sum_unit = [&](int c, float (&s)[V]) __attribute__((always_inline)) {
+            load_row_unit<kAny>(xr, c, N, s);
+            if (rr) {
+                float a[V];
+                load_row_unit<kAny>(rr, c, N, a);
+#pragma unroll
+                for (int j = 0; j < V; ++j) s[j] += a[j];
+            }
+        };
+        float keep[kKeep][V], ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i) {
+            const int c = tid + kThreads * i;
+            if (c < units) {
+                sum_unit(c, keep[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) keep[i][j] = 0.0f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) ss = __builtin_fmaf(keep[i][j], keep[i][j], ss);
+        for (int c = tid + kThreads * kKeep; c < units; c += kThreads) {
+            float s[V];
+            sum_unit(c, s);
+#pragma unroll
+            for (int j = 0; j < V; ++j) ss = __builtin_fmaf(s[j], s[j], ss);
+        }
+        ss = row_sum<kWaves>(ss, red);
+        const float r = 1.0f / sqrtf(ss / (float)N + eps);
+        // s -> v
+        auto scaled = [&](int c, float (&s)[V]) __attribute__((always_inline)) {
+            float w[V];
+            if (weight) load_row_unit<kAny>(weight, c, N, w);
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[j] = weight ? s[j] * r * w[j] : s[j] * r;
+        };
+        if constexpr (!kI8) {
+            auto out = [&](int c, float (&s)[V]) __attribute__((always_inline)) {
+                if (h) store_row_unit<kAny>(h + m * N, c, N, s);
+                scaled(c, s);
+                store_row_unit<kAny>(y + m * N, c, N, s);
+            };
+#pragma unroll
+            for (int i = 0; i < kKeep; ++i) {
+                const int c = tid + kThreads * i;
+                if (c < units) out(c, keep[i]);
+            }
+            for (int c = tid + kThreads * kKeep; c < units; c += kThreads) {
+                float s[V];
+                sum_unit(c, s);
+                out(c, s);
+            }
+        } else {
+            uint32_t top = 0;
+            auto widest = [&](const float (&v)[V]) __attribute__((always_inline)) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+            };
+#pragma unroll
+            for (int i = 0; i < kKeep; ++i) {
+                const int c = tid + kThreads * i;
+                if (c < units) {
+                    if (h) store_row_unit<kAny>(h + m * N, c, N, keep[i]);
+                    scaled(c, keep[i]);
+                    widest(keep[i]);
+                }
+            }
+            for (int c = tid + kThreads * kKeep; c < units; c += kThreads) {
+                float s[V];
+                sum_unit(c, s);
+                scaled(c, s);
+                widest(s);
+            }
+            const float a = scale_i8(__uint_as_float(row_max<kWaves>(top, red))), inv = 1.0f / a;
+            auto codes = [&](int c, const float (&v)[V]) __attribute__((always_inline)) {
+                uint32_t w[V / 4];
+                codes_i8(v, a, inv, w);
+                if constexpr (V == 8)
+                    *reinterpret_cast<uint2*>(xq + m * N + c * V) = make_uint2(w[0], w[1]);
+                else
+                    *reinterpret_cast<uint32_t*>(xq + m * N + c * V) = w[0];
+            };
+#pragma unroll
+            for (int i = 0; i < kKeep; ++i) {
+                const int c = tid + kThreads * i;
+                if (c < units) codes(c, keep[i]);
+            }
+            for (int c = tid + kThreads * kKeep; c < units; c += kThreads) {
+                float s[V];
+                sum_unit(c, s);
+                if (h) store_row_unit<kAny>(h + m * N, c, N, s);
+                scaled(c, s);
+                codes(c, s);
+            }
+            if (lane_id() == 0) ascale[m] = a;  // (every wave's is the same)
+        }
+    }
+}
+
+// ---- gradients ----------------------------------------------------------------------------------
+
+// dx, and this block's part of dweight: a block takes rows blockIdx.x, + gridDim.x, ..., and a thread the same columns
+// of each, so that the columns' sums stay in its registers (N at most kThreads kUnits V) and leave once, to part
+// [blocks][N].  The order of additions does not depend on timing.
+template <typename T, int kWaves, int kUnits, bool kAny>
+__global__ __launch_bounds__(64 * kWaves) void add_rmsnorm_backward_kernel(const T* dy, const T* dh, const T* __restrict__ h,
+                                                                           int64_t rows, int N, const T* __restrict__ weight,
+                                                                           float eps, T* dx, float* __restrict__ part) {
+    constexpr int V = kUnit<T>, kThreads = 64 * kWaves;
+    __shared__ float red[kWaves];
+    const int tid = threadIdx.x, units = (N + V - 1) / V;
+    float w[kUnits][V], dw[kUnits][V];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+        const int c = tid + kThreads * i;
+#pragma unroll
+        for (int j = 0; j < V; ++j) dw[i][j] = 0.0f, w[i][j] = 1.0f;
+        if (weight && c < units) load_row_unit<kAny>(weight, c, N, w[i]);
+    }
+    for (int64_t m = blockIdx.x; m < rows; m += gridDim.x) {
+        float g[kUnits][V], hv[kUnits][V], ss = 0.0f, gh = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            const int c = tid + kThreads * i;
+            if (c < units) {
+                load_row_unit<kAny>(h + m * N, c, N, hv[i]);
+                load_row_unit<kAny>(dy + m * N, c, N, g[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) g[i][j] = hv[i][j] = 0.0f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                ss = __builtin_fmaf(hv[i][j], hv[i][j], ss);
+                gh = __builtin_fmaf(g[i][j] * w[i][j], hv[i][j], gh);
+            }
+        ss = row_sum<kWaves>(ss, red);
+        gh = row_sum<kWaves>(gh, red);
+        const float r = 1.0f / sqrtf(ss / (float)N + eps), c0 = gh / (float)N * (r * r);
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            const int c = tid + kThreads * i;
+            if (c >= units) continue;
+            float o[V], add[V];
+            if (dx && dh) load_row_unit<kAny>(dh + m * N, c, N, add);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                dw[i][j] = __builtin_fmaf(g[i][j], hv[i][j] * r, dw[i][j]);
+                o[j] = r * (g[i][j] * w[i][j] - hv[i][j] * c0);
+                if (dx && dh) o[j] += add[j];
+            }
+            if (dx) store_row_unit<kAny>(dx + m * N, c, N, o);
+        }
+    }
+    if (part) {
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            const int c = tid + kThreads * i;
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (c < units && c * V + j < N) part[(int64_t)blockIdx.x * N + c * V + j] = dw[i][j];
+        }
+    }
+}
+
+// Rows too long for that: dx row by row, each read twice, and r kept for the columns' sums below.
+template <typename T, int kWaves>
+__global__ __launch_bounds__(64 * kWaves) void add_rmsnorm_backward_long_kernel(const T* dy, const T* dh, const T* __restrict__ h,
+                                                                                int64_t rows, int N, const T* __restrict__ weight,
+                                                                                float eps, T* dx, float* __restrict__ rstd) {
+    constexpr int V = kUnit<T>, kThreads = 64 * kWaves;
+    __shared__ float red[kWaves];
+    const int units = (N + V - 1) / V;
+    for (int64_t m = blockIdx.x; m < rows; m += gridDim.x) {
+        float ss = 0.0f, gh = 0.0f;
+        for (int c = threadIdx.x; c < units; c += kThreads) {
+            float hv[V], g[V], w[V];
+            load_row_unit<true>(h + m * N, c, N, hv);
+            load_row_unit<true>(dy + m * N, c, N, g);
+            if (weight) load_row_unit<true>(weight, c, N, w);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                ss = __builtin_fmaf(hv[j], hv[j], ss);
+                gh = __builtin_fmaf(weight ? g[j] * w[j] : g[j], hv[j], gh);
+            }
+        }
+        ss = row_sum<kWaves>(ss, red);
+        gh = row_sum<kWaves>(gh, red);
+        const float r = 1.0f / sqrtf(ss / (float)N + eps), c0 = gh / (float)N * (r * r);
+        if (rstd && threadIdx.x == 0) rstd[m] = r;
+        if (!dx) continue;
+        for (int c = threadIdx.x; c < units; c += kThreads) {
+            float hv[V], g[V], w[V], add[V];
+            load_row_unit<true>(h + m * N, c, N, hv);
+            load_row_unit<true>(dy + m * N, c, N, g);
+            if (weight) load_row_unit<true>(weight, c, N, w);
+            if (dh) load_row_unit<true>(dh + m * N, c, N, add);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                g[j] = r * ((weight ? g[j] * w[j] : g[j]) - hv[j] * c0);
+                if (dh) g[j] += add[j];
+            }
+            store_row_unit<true>(dx + m * N, c, N, g);
+        }
+    }
+}
+template <typename T>
+__global__ __launch_bounds__(256) void rmsnorm_dweight_long_kernel(const T* __restrict__ dy, const T* __restrict__ h, int64_t rows,
+                                                                   int N, const float* __restrict__ rstd,
+                                                                   float* __restrict__ part, int64_t each) {
+    const int n = blockIdx.x * 256 + threadIdx.x;
+    const int64_t lo = blockIdx.y * each, hi = min(lo + each, rows);
+    if (n >= N) return;
+    float sum = 0.0f;
+    for (int64_t m = lo; m < hi; ++m) sum = __builtin_fmaf(to_f32(dy[m * N + n]), to_f32(h[m * N + n]) * rstd[m], sum);
+    part[(int64_t)blockIdx.y * N + n] = sum;
+}
+
+// dweight = the parts' sums over [parts][N], in an order of their own: kGroups threads a column take every kGroups-th
+// part, and the groups are added in order.
+constexpr int kJoinColumns = 32, kJoinGroups = 32;
+__global__ __launch_bounds__(kJoinColumns* kJoinGroups) void join_dweight_kernel(const float* __restrict__ part, int parts, int N,
+                                                                                 float* __restrict__ dweight) {
+    __shared__ float sums[kJoinGroups][kJoinColumns + 1];
+    const int col = threadIdx.x % kJoinColumns, group = threadIdx.x / kJoinColumns;
+    const int n = blockIdx.x * kJoinColumns + col;
+    float s = 0.0f;
+    if (n < N) {
+#pragma unroll 4
+        for (int p = group; p < parts; p += kJoinGroups) s += part[(int64_t)p * N + n];
+    }
+    sums[group][col] = s;
+    __syncthreads();
+    if (group == 0 && n < N) {
+        s = sums[0][col];
+#pragma unroll
+        for (int g = 1; g < kJoinGroups; ++g) s += sums[g][col];
+        dweight[n] = s;
+    }
+}
+
+// Rows by a wave each where they are short and many enough for every SIMD.
+bool norm_by_wave(int64_t rows, int64_t N, int element) { return N * element <= 64 * 16 * kKeep && rows >= 1024; }
+
+// Blocks of the gradients' kernel, each with a part of dweight.
+constexpr int64_t kGradBlocks = 512;
+// Longest row, in elements, whose columns' sums stay in registers.
+template <typename T>
+constexpr int64_t kGradKept = 512 * 4 * kUnit<T>;
+constexpr int64_t kLongParts = 64;
+
+int64_t grad_parts(int64_t rows) { return std::min(rows, kGradBlocks); }
+
+}  // namespace
+
+hipError_t launch_add_rmsnorm(int dtype, const void* x, const void* residual, int64_t rows, int64_t N, const void* weight,
+                              float eps, void* h, void* y, int8_t* xq, float* ascale, hipStream_t stream) {
+    return with_act_type(dtype, [&](auto t) {
+        using T = decltype(t);
+        auto run = [&](auto waves, auto i8, auto any) {
+            constexpr int kWaves = decltype(waves)::value;
+            const dim3 grid((unsigned)std::min<int64_t>((rows + 4 / kWaves - 1) / (4 / kWaves), kMaxGridBlocks));
+            hipLaunchKernelGGL((add_rmsnorm_kernel<T, kWaves, decltype(i8)::value, decltype(any)::value>), grid, dim3(256), 0,
+                               stream, static_cast<const T*>(x), static_cast<const T*>(residual), rows, (int)N,
+                               static_cast<const T*>(weight), eps, static_cast<T*>(h), static_cast<T*>(y), xq, ascale);
+            return hipGetLastError();
+        };
+        auto pick = [&](auto i8, auto any) {
+            return norm_by_wave(rows, N, sizeof(T)) ? run(std::integral_constant<int, 1>{}, i8, any)
+                                                    : run(std::integral_constant<int, 4>{}, i8, any);
+        };
+        if (xq) return pick(std::true_type{}, std::false_type{});  // (whole units: N % 16 == 0)
+        return N % kUnit<T> == 0 ? pick(std::false_type{}, std::false_type{}) : pick(std::false_type{}, std::true_type{});
+    });
+}
+
+size_t add_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t N) {
+    // the parts of dweight, and a factor per row that the longest rows need
+    const int64_t parts = N <= kGradKept<bf16_t> ? grad_parts(rows) : std::min(rows, kLongParts);
+    return (size_t)parts * (size_t)N * 4 + (size_t)((rows + 3) / 4 * 16);
+}
+
+hipError_t launch_add_rmsnorm_backward(int dtype, const void* dy, const void* dh, const void* h, int64_t rows, int64_t N,
+                                       const void* weight, float eps, void* dx, float* dweight, float* ws, hipStream_t stream) {
+    return with_act_type(dtype, [&](auto t) {
+        using T = decltype(t);
+        const T *dyt = static_cast<const T*>(dy), *dht = static_cast<const T*>(dh), *ht = static_cast<const T*>(h),
+                *wt = static_cast<const T*>(weight);
+        T* dxt = static_cast<T*>(dx);
+        int parts = (int)grad_parts(rows);
+        if (N <= kGradKept<T>) {
+            float* part = dweight ? ws : nullptr;
+            auto run = [&](auto waves, auto keep, auto any) {
+                constexpr int kWaves = decltype(waves)::value, kUnits = decltype(keep)::value;
+                hipLaunchKernelGGL((add_rmsnorm_backward_kernel<T, kWaves, kUnits, decltype(any)::value>), dim3((unsigned)parts),
+                                   dim3(64 * kWaves), 0, stream, dyt, dht, ht, rows, (int)N, wt, eps, dxt, part);
+                return hipGetLastError();
+            };
+            auto pick = [&](auto any) {
+                const int64_t units = (N + kUnit<T> - 1) / kUnit<T>;
+                using I1 = std::integral_constant<int, 1>;
+                using I4 = std::integral_constant<int, 4>;
+                if (units <= 256) return run(I4{}, I1{}, any);
+                if (units <= 512) return run(I4{}, std::integral_constant<int, 2>{}, any);
+                if (units <= 1024) return run(I4{}, I4{}, any);
+                return run(std::integral_constant<int, 8>{}, I4{}, any);
+            };
+            const hipError_t e = N % kUnit<T> == 0 ? pick(std::false_type{}) : pick(std::true_type{});
+            if (e != hipSuccess || !dweight) return e;
+        } else {
+            float* rstd = ws;
+            float* part = ws + (rows + 3) / 4 * 4;
+            hipLaunchKernelGGL((add_rmsnorm_backward_long_kernel<T, 16>), dim3((unsigned)std::min<int64_t>(rows, kMaxGridBlocks)),
+                               dim3(1024), 0, stream, dyt, dht, ht, rows, (int)N, wt, eps, dxt, dweight ? rstd : nullptr);
+            if (const hipError_t e = hipGetLastError(); e != hipSuccess || !dweight) return e;
+            const int64_t each = (rows + kLongParts - 1) / kLongParts;
+            parts = (int)((rows + each - 1) / each);
+            hipLaunchKernelGGL((rmsnorm_dweight_long_kernel<T>), dim3((unsigned)((N + 255) / 256), (unsigned)parts), dim3(256), 0,
+                               stream, dyt, ht, rows, (int)N, rstd, part, each);
+            if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+            ws = part;
+        }
+        hipLaunchKernelGGL(join_dweight_kernel, dim3((unsigned)((N + kJoinColumns - 1) / kJoinColumns)),
+                           dim3(kJoinColumns * kJoinGroups), 0, stream, ws, parts, (int)N, dweight);
+        return hipGetLastError();
+    });
+}
+
+}  // namespace w4a16

@@ -413,6 +413,42 @@ w4a16_status_t w4a16_expert_combine_backward(w4a16_dtype_t act, const void* dy, 
                                              const int32_t* pos, const float* weights, int64_t N, void* dys,
                                              float* dweights, hipStream_t stream);
 
+/* ---- RMS norm with a residual: what stands before a layer's products ------------------------------
+ * Row t of x and residual [T][N] (type `act`): s = x + residual in fp32 (residual NULL: s = x), and
+ *   h [T][N]  s rounded to `act`: the sum that goes on past the layer; NULL where it is not wanted
+ *   v = s r w in fp32 with r = 1 / sqrt(sum_n s^2 / N + eps), weight w [N] of type `act` (NULL: ones)
+ * The norm is of s before it is rounded.  Sums are fp32 in a fixed order: bitwise reproducible.  eps finite
+ * and not negative; N at most 2^22 (ERR_UNSUPPORTED above).  A row whose sum of squares passes fp32's
+ * range gets zeros, one with an infinity or NaN gets NaN where it has one (and zeros or NaN besides); other rows
+ * are not touched by it.  h and y may each be x's or residual's own array (the same address), but not one
+ * array for both; other overlaps are not allowed. */
+
+/* y [T][N] = v rounded to `act`. */
+w4a16_status_t w4a16_add_rmsnorm(w4a16_dtype_t act, const void* x, const void* residual, int64_t T, int64_t N,
+                                 const void* weight, float eps, void* h, void* y, hipStream_t stream);
+
+/* v in 8-bit integers as w4a16_quantize_rows_i8 quantizes fp32 rows, N % 16 == 0: ascale [T] = max_n |v| / 127 (1.0
+ * where that is zero, NaN with codes 0 where v is not finite) and xq int8 [T][N].  They are what w4a16_gemm_w8a8
+ * takes. */
+w4a16_status_t w4a16_add_rmsnorm_i8(w4a16_dtype_t act, const void* x, const void* residual, int64_t T, int64_t N,
+                                    const void* weight, float eps, void* h, int8_t* xq, float* ascale, hipStream_t stream);
+
+/* Gradients of y = h r w, r = 1 / sqrt(sum_n h^2 / N + eps), for h [T][N] as w4a16_add_rmsnorm stored it: with
+ * g = dy w,
+ *   dx [T][N]    r (g - h r^2 sum_n(g h) / N) + dh, of x and of residual alike (type `act`, rounded once); dh [T][N]
+ *                is the gradient that reaches h itself (NULL: none)
+ *   dweight [N]  fp32, sum_t dy h r, in a fixed order
+ * dx or dweight may be NULL (not wanted), not both.  dx may be dh's own array; other overlaps are not allowed.
+ * workspace (16-byte aligned, for dweight; else it may be NULL): w4a16_add_rmsnorm_backward_workspace_bytes(T, N) bytes,
+ * needs no initialisation and must not be shared by calls, or graphs of calls, that may run at the same
+ * time. */
+w4a16_status_t w4a16_add_rmsnorm_backward(w4a16_dtype_t act, const void* dy, const void* dh, const void* h, int64_t T,
+                                          int64_t N, const void* weight, float eps, void* dx, float* dweight, void* workspace,
+                                          size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace that w4a16_add_rmsnorm_backward needs for dweight (0 for sizes it refuses). */
+size_t w4a16_add_rmsnorm_backward_workspace_bytes(int64_t T, int64_t N);
+
 #ifdef __cplusplus
 }
 #endif

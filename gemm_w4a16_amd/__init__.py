@@ -18,6 +18,7 @@ _LIB_PATH = Path(__file__).resolve().parent / "libw4a16.so"
 
 W4A16_OK, W4A16_ERR_INVALID, W4A16_ERR_UNSUPPORTED, W4A16_ERR_DEVICE = 0, 1, 2, 3
 W4A16_FMT_G128_ASYM_BF16, W4A16_FMT_Q4_B32_SYM_FP16, W4A16_FMT_G128_ZP_FP16, W4A16_FMT_W8_ROW_FP32 = 0, 1, 2, 3
+W4A16_FMT_MX4_B32_E8M0 = 4
 W4A16_BF16, W4A16_FP16, W4A16_FP32 = 0, 1, 2
 
 # Every symbol include/w4a16.h declares.
@@ -31,6 +32,9 @@ EXPORTED = (
     "w4a16_gemm_w8a8_experts", "w4a16_max_experts", "w4a16_expert_sort", "w4a16_expert_sort_workspace_bytes",
     "w4a16_expert_gather", "w4a16_expert_gather_i8", "w4a16_expert_combine", "w4a16_expert_combine_backward",
     "w4a16_add_rmsnorm", "w4a16_add_rmsnorm_i8", "w4a16_add_rmsnorm_backward", "w4a16_add_rmsnorm_backward_workspace_bytes",
+    "w4a16_quantize_rows_mx4", "w4a16_gemm_w4a4", "w4a16_matmul_w4a4", "w4a16_w4a4_workspace_bytes",
+    "w4a16_expert_layer_w8a8", "w4a16_expert_layer_max_tokens", "w4a16_expert_layer_max_pairs",
+    "w4a16_expert_layer_workspace_bytes",
 )
 
 
@@ -89,9 +93,18 @@ def _load() -> ctypes.CDLL:
     L.w4a16_add_rmsnorm_backward.argtypes = [I, P, P, P, I64, I64, P, F, P, P, P, SZ, P]
     L.w4a16_add_rmsnorm_backward_workspace_bytes.argtypes = [I64, I64]
     L.w4a16_add_rmsnorm_backward_workspace_bytes.restype = SZ
+    L.w4a16_quantize_rows_mx4.argtypes = [I, P, I64, I64, P, P, P]
+    L.w4a16_gemm_w4a4.argtypes = [I, I, P, P, I64, P, P, P, I64, I64, P, P]
+    L.w4a16_matmul_w4a4.argtypes = [I, I, P, I64, P, P, P, I64, I64, P, P, SZ, P]
+    L.w4a16_w4a4_workspace_bytes.argtypes, L.w4a16_w4a4_workspace_bytes.restype = [I, I64, I64, I64], SZ
+    L.w4a16_expert_layer_w8a8.argtypes = [I, I, P, P, I64, P, I64, I64, P, I64, P, P, P, P, I64, I64, P, P, SZ, P]
+    L.w4a16_expert_layer_max_tokens.argtypes, L.w4a16_expert_layer_max_tokens.restype = [], I64
+    L.w4a16_expert_layer_max_pairs.argtypes, L.w4a16_expert_layer_max_pairs.restype = [], I64
+    L.w4a16_expert_layer_workspace_bytes.argtypes, L.w4a16_expert_layer_workspace_bytes.restype = [I64, I64, I64], SZ
     for name in ("w4a16_quantize_rows_i8", "w4a16_gemm_w8a8", "w4a16_matmul_w8a8", "w4a16_gemm_w8a8_experts",
                  "w4a16_expert_sort", "w4a16_expert_gather", "w4a16_expert_gather_i8", "w4a16_expert_combine",
-                 "w4a16_expert_combine_backward", "w4a16_add_rmsnorm", "w4a16_add_rmsnorm_i8", "w4a16_add_rmsnorm_backward"):
+                 "w4a16_expert_combine_backward", "w4a16_add_rmsnorm", "w4a16_add_rmsnorm_i8", "w4a16_add_rmsnorm_backward",
+                 "w4a16_quantize_rows_mx4", "w4a16_gemm_w4a4", "w4a16_matmul_w4a4", "w4a16_expert_layer_w8a8"):
         getattr(L, name).restype = I
     for name in ("w4a16_packed_sizes", "w4a16_quantize_pack", "w4a16_check_weights", "w4a16_dequant", "w4a16_gemv",
                  "w4a16_gemm", "w4a16_matmul", "w4a16_matmul_noalloc", "w4a16_quantize_act_i8", "w4a16_gemm_w4a8",
@@ -241,14 +254,14 @@ def w4a16_matmul_w4a8(fmt: int, x, M: int, codes, scales, mins, N: int, K: int, 
         "w4a16_matmul_w4a8")
 
 
-# ---- W8A8, the experts' operators, norms -----------------------------------------------------------
+# ---- W8A8, the experts' operators, W4A4, norms -----------------------------------------------------
 # Tensors given to these must be on one GPU, contiguous, of the type the call takes them as and at least as
 # large as it reads or writes (W4A16_ERR_INVALID otherwise); the launch goes to that GPU's current stream,
 # whichever GPU is current.  Raw addresses are passed as they are.
 
 import torch  # noqa: E402 (loaded with the library, above)
 
-_I8, _I32, _F32 = torch.int8, torch.int32, torch.float32
+_I8, _U8, _I32, _F32 = torch.int8, torch.uint8, torch.int32, torch.float32
 _ACT = {W4A16_BF16: torch.bfloat16, W4A16_FP16: torch.float16, W4A16_FP32: _F32}.get  # None: the library refuses it
 _ID = {32: _I32, 64: torch.int64}.get
 
@@ -349,6 +362,55 @@ def w4a16_expert_combine_backward(act: int, dy, ys, T: int, topk: int, pos, weig
           ((1, T * N, t), (2, P * N, t), (5, P, _I32), (6, P, _F32), (8, P * N, t), (9, P, _F32)), stream)
 
 
+def w4a16_expert_layer_w8a8(fmt: int, out: int, xq, ascale, T: int, ids, id_bits: int, topk: int, weights, E: int, up_codes,
+                            up_scales, down_codes, down_scales, H: int, I: int, y, workspace, workspace_bytes: int,
+                            stream=None) -> None:
+    P, W = T * topk, E * H * I
+    _call("w4a16_expert_layer_w8a8", (fmt, out, xq, ascale, T, ids, id_bits, topk, weights, E, up_codes, up_scales, down_codes,
+                                      down_scales, H, I, y, workspace, workspace_bytes),
+          ((2, T * H, _I8), (3, T, _F32), (5, P, _ID(id_bits)), (8, P, _F32), (10, 2 * W, _I8), (11, 2 * E * I, _F32),
+           (12, W, _I8), (13, E * H, _F32), (16, T * H, _ACT(out)), (17, workspace_bytes, None)), stream)
+
+
+def w4a16_expert_layer_max_tokens() -> int:
+    return int(lib.w4a16_expert_layer_max_tokens())
+
+
+def w4a16_expert_layer_max_pairs() -> int:
+    return int(lib.w4a16_expert_layer_max_pairs())
+
+
+def w4a16_expert_layer_workspace_bytes(T: int, topk: int, I: int) -> int:
+    return int(lib.w4a16_expert_layer_workspace_bytes(T, topk, I))
+
+
+def _mx4_scale_bytes(rows: int, K: int) -> int:
+    return (K + 255) // 256 * ((rows + 15) // 16 * 16) * 8
+
+
+def w4a16_quantize_rows_mx4(act: int, x, M: int, K: int, xq, xscales, stream=None) -> None:
+    _call("w4a16_quantize_rows_mx4", (act, x, M, K, xq, xscales),
+          ((1, M * K, _ACT(act)), (4, M * K // 2, _U8), (5, _mx4_scale_bytes(M, K), _U8)), stream)
+
+
+def w4a16_gemm_w4a4(fmt: int, out: int, xq, xscales, M: int, codes, scales, mins, N: int, K: int, y, stream=None) -> None:
+    _call("w4a16_gemm_w4a4", (fmt, out, xq, xscales, M, codes, scales, mins, N, K, y),
+          ((2, M * K // 2, _U8), (3, _mx4_scale_bytes(M, K), _U8), (5, N * K // 2, _U8), (6, _mx4_scale_bytes(N, K), _U8),
+           (7, 0, None), (10, M * N, _ACT(out))), stream)
+
+
+def w4a16_matmul_w4a4(fmt: int, act: int, x, M: int, codes, scales, mins, N: int, K: int, y, workspace,
+                      workspace_bytes: int, stream=None) -> None:
+    t = _ACT(act)
+    _call("w4a16_matmul_w4a4", (fmt, act, x, M, codes, scales, mins, N, K, y, workspace, workspace_bytes),
+          ((2, M * K, t), (4, N * K // 2, _U8), (5, _mx4_scale_bytes(N, K), _U8), (6, 0, None), (9, M * N, t),
+           (10, workspace_bytes, None)), stream)
+
+
+def w4a16_w4a4_workspace_bytes(fmt: int, M: int, N: int, K: int) -> int:
+    return int(lib.w4a16_w4a4_workspace_bytes(fmt, M, N, K))
+
+
 def w4a16_add_rmsnorm(act: int, x, residual, T: int, N: int, weight, eps: float, h, y, stream=None) -> None:
     t, n = _ACT(act), T * N
     _call("w4a16_add_rmsnorm", (act, x, residual, T, N, weight, eps, h, y),
@@ -375,7 +437,7 @@ def w4a16_add_rmsnorm_backward_workspace_bytes(T: int, N: int) -> int:
 # ---- memory plumbing (torch allocations with the ABI's shapes and dtypes) ------------------------
 
 def alloc_packed(fmt: int, N: int, K: int, device="cuda"):
-    """Empty (codes, scales, mins) device tensors for an N x K weight (mins is None for Q4 and W8;
+    """Empty (codes, scales, mins) device tensors for an N x K weight (mins is None for Q4, W8 and MX4;
     the zero points for the zero-point format)."""
     import torch
     w4a16_packed_sizes(fmt, N, K)  # validates the shape
@@ -389,6 +451,10 @@ def alloc_packed(fmt: int, N: int, K: int, device="cuda"):
     if fmt == W4A16_FMT_W8_ROW_FP32:
         return (torch.empty((N, K), dtype=torch.int8, device=device),
                 torch.empty(N, dtype=torch.float32, device=device),
+                None)
+    if fmt == W4A16_FMT_MX4_B32_E8M0:  # (rows' codes and scales as well, with M for N)
+        return (torch.empty((N, K // 2), dtype=torch.uint8, device=device),
+                torch.empty(((K + 255) // 256, (N + 15) // 16 * 16, 8), dtype=torch.uint8, device=device),
                 None)
     if fmt == W4A16_FMT_G128_ZP_FP16:
         return (torch.empty((N, K // 8), dtype=torch.int32, device=device),
@@ -423,6 +489,13 @@ def alloc_w8a8_workspace(fmt: int, M: int, N: int, K: int, device="cuda"):
     return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
 
 
+def alloc_w4a4_workspace(fmt: int, M: int, N: int, K: int, device="cuda"):
+    """(tensor, bytes) sized for w4a16_matmul_w4a4 on this shape."""
+    import torch
+    nbytes = w4a16_w4a4_workspace_bytes(fmt, M, N, K)
+    return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
+
+
 def alloc_expert_sort(T: int, topk: int, E: int, device="cuda"):
     """Empty (offsets [E + 1], pos [T][topk], src [T * topk], workspace or None, its bytes) for
     w4a16_expert_sort."""
@@ -437,4 +510,11 @@ def alloc_add_rmsnorm_backward_workspace(T: int, N: int, device="cuda"):
     """(tensor, bytes) sized for w4a16_add_rmsnorm_backward."""
     import torch
     nbytes = w4a16_add_rmsnorm_backward_workspace_bytes(T, N)
+    return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
+
+
+def alloc_expert_layer_workspace(T: int, topk: int, I: int, device="cuda"):
+    """(tensor, bytes) sized for w4a16_expert_layer_w8a8."""
+    import torch
+    nbytes = w4a16_expert_layer_workspace_bytes(T, topk, I)
     return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes

@@ -10,6 +10,7 @@
 
 #include "../../include/w4a16.h"
 #include "launch.h"
+#include "mx4.h"
 
 namespace {
 
@@ -33,15 +34,16 @@ constexpr int64_t kW4A8FusedMaxRows = 1;
 bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int64_t group_of(w4a16_format_t fmt) {
+    if (fmt == W4A16_FMT_MX4_B32_E8M0) return w4a16::kMx4Block;
     return fmt == W4A16_FMT_Q4_B32_SYM_FP16 ? kBlockQ4 : fmt == W4A16_FMT_W8_ROW_FP32 ? kW8RowAlign : kGroupG128;
 }
 
-// Formats with no third array (Q4, W8): `mins` must be NULL.
+// Formats with no third array (Q4, W8, MX4): `mins` must be NULL.
 bool has_mins(w4a16_format_t fmt) { return fmt == W4A16_FMT_G128_ASYM_BF16 || fmt == W4A16_FMT_G128_ZP_FP16; }
 
 bool valid_format(w4a16_format_t fmt) {
     return fmt == W4A16_FMT_G128_ASYM_BF16 || fmt == W4A16_FMT_Q4_B32_SYM_FP16 || fmt == W4A16_FMT_G128_ZP_FP16 ||
-           fmt == W4A16_FMT_W8_ROW_FP32;
+           fmt == W4A16_FMT_W8_ROW_FP32 || fmt == W4A16_FMT_MX4_B32_E8M0;
 }
 
 w4a16_status_t check_shape(w4a16_format_t fmt, int64_t N, int64_t K) {
@@ -61,6 +63,7 @@ w4a16_status_t check_packed(w4a16_format_t fmt, const void* codes, const void* s
 
 w4a16_status_t check_act(w4a16_format_t fmt, w4a16_dtype_t act) {
     if (act != W4A16_BF16 && act != W4A16_FP16 && act != W4A16_FP32) return W4A16_ERR_INVALID;
+    if (fmt == W4A16_FMT_MX4_B32_E8M0) return W4A16_ERR_UNSUPPORTED;  // W4A4 only
     if (fmt == W4A16_FMT_G128_ASYM_BF16 && act != W4A16_BF16) return W4A16_ERR_UNSUPPORTED;
     if (fmt != W4A16_FMT_G128_ASYM_BF16 && act == W4A16_FP32) return W4A16_ERR_UNSUPPORTED;
     if (fmt == W4A16_FMT_W8_ROW_FP32 && act != W4A16_FP16) return W4A16_ERR_UNSUPPORTED;
@@ -146,6 +149,30 @@ w4a16_status_t check_norm(w4a16_dtype_t act, int64_t T, int64_t N, float eps) {
 }
 bool null_or_aligned16(const void* p) { return p == nullptr || aligned16(p); }
 
+// A W4A4 product's arguments but its activations.
+w4a16_status_t check_w4a4(w4a16_format_t fmt, w4a16_dtype_t out, int64_t M, const void* codes, const void* scales,
+                          const void* mins, int64_t N, int64_t K, const void* y) {
+    if (w4a16_status_t st = check_shape(fmt, N, K); st != W4A16_OK) return st;
+    if (M <= 0 || M > kMaxDim || !valid_dtype(out) || !aligned16(y)) return W4A16_ERR_INVALID;
+    if (w4a16_status_t st = check_packed(fmt, codes, scales, mins); st != W4A16_OK) return st;
+    return fmt == W4A16_FMT_MX4_B32_E8M0 ? W4A16_OK : W4A16_ERR_UNSUPPORTED;
+}
+
+// The W4A4 workspace: the codes of x, then their scales (both 16-byte aligned).
+struct W4A4Workspace {
+    size_t scales, needed;
+    W4A4Workspace(int64_t M, int64_t K)
+        : scales((size_t)M * (size_t)K / 2), needed(scales + w4a16::mx4_scale_bytes(M, K)) {}  // K % 32 == 0
+};
+
+// Tokens, choices and the width between an experts' layer's two products.
+w4a16_status_t check_layer(int64_t T, int64_t topk, int64_t I) {
+    if (T <= 0 || T > kMaxDim || topk <= 0 || topk > kMaxDim || I <= 0 || I > kMaxDim || I % kW8RowAlign != 0)
+        return W4A16_ERR_INVALID;
+    if (T > w4a16::kLayerTokens || T * topk > w4a16::kLayerPairs || 2 * I > kMaxN || I > kMaxK) return W4A16_ERR_UNSUPPORTED;
+    return W4A16_OK;
+}
+
 // The W8A8 workspace: the codes of x and its row scales (matmul_w8a8 needs these), then room for the sums of
 // K's parts, each 16-byte aligned.
 struct W8A8Workspace {
@@ -213,6 +240,7 @@ w4a16_status_t w4a16_packed_sizes(w4a16_format_t fmt, int64_t N, int64_t K, size
     }
     const size_t codes = (size_t)N * (size_t)K / 2;  // 4 bits per weight in the other formats
     size_t scales = (size_t)N * (size_t)(K / group_of(fmt)) * 2;
+    if (fmt == W4A16_FMT_MX4_B32_E8M0) scales = w4a16::mx4_scale_bytes(N, K);
     // G128: the GEMM reads scales and minimums as aligned 4-byte words, so an odd element count
     // gets 2 bytes of padding (never written, never used)
     if (fmt == W4A16_FMT_G128_ASYM_BF16) scales = (scales + 3) & ~(size_t)3;
@@ -250,7 +278,7 @@ w4a16_status_t w4a16_check_weights(w4a16_format_t fmt, const float* W, int64_t N
                 case W4A16_FMT_Q4_B32_SYM_FP16:
                     if (!fits_fp16(amax / 7.0f)) return W4A16_ERR_INVALID;
                     break;
-                default:  // W8: an fp32 scale max|w| / 127 is always finite
+                default:  // W8: an fp32 scale max|w| / 127 is always finite; MX4: a power of two below 2^126
                     break;
             }
         }
@@ -277,6 +305,9 @@ w4a16_status_t w4a16_quantize_pack(w4a16_format_t fmt, const float* W, int64_t N
     if (fmt == W4A16_FMT_G128_ASYM_BF16)
         return from_hip(w4a16::launch_pack_g128(W, N, K, static_cast<uint32_t*>(codes), static_cast<uint16_t*>(scales),
                                                 static_cast<uint16_t*>(mins), stream));
+    if (fmt == W4A16_FMT_MX4_B32_E8M0)
+        return from_hip(w4a16::launch_quant_mx4((int)W4A16_FP32, W, N, K, static_cast<uint8_t*>(codes),
+                                                static_cast<uint8_t*>(scales), stream));
     if (fmt == W4A16_FMT_W8_ROW_FP32)
         return from_hip(w4a16::launch_pack_w8row(W, N, K, static_cast<int8_t*>(codes), static_cast<float*>(scales),
                                                  stream));
@@ -302,6 +333,9 @@ w4a16_status_t w4a16_dequant(w4a16_format_t fmt, const void* codes, const void* 
         return from_hip(w4a16::launch_dequant_g128(static_cast<const uint32_t*>(codes),
                                                    static_cast<const uint16_t*>(scales),
                                                    static_cast<const uint16_t*>(mins), N, K, dt, W_hat, stream));
+    if (fmt == W4A16_FMT_MX4_B32_E8M0)
+        return from_hip(w4a16::launch_dequant_mx4(static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), N, K,
+                                                  dt, W_hat, stream));
     if (fmt == W4A16_FMT_W8_ROW_FP32)
         return from_hip(w4a16::launch_dequant_w8row(static_cast<const int8_t*>(codes), static_cast<const float*>(scales),
                                                     N, K, dt, W_hat, stream));
@@ -703,6 +737,77 @@ w4a16_status_t w4a16_add_rmsnorm_backward(w4a16_dtype_t act, const void* dy, con
     w4a16::clear_stale_error();
     return from_hip(w4a16::launch_add_rmsnorm_backward((int)act, dy, dh, h, T, N, weight, eps, dx, dweight,
                                                        static_cast<float*>(workspace), stream));
+}
+
+w4a16_status_t w4a16_quantize_rows_mx4(w4a16_dtype_t act, const void* x, int64_t M, int64_t K, uint8_t* xq, uint8_t* xscales,
+                                       hipStream_t stream) {
+    if (!valid_dtype(act) || M <= 0 || M > kMaxDim || K <= 0 || K > kMaxDim || K % w4a16::kMx4Block != 0)
+        return W4A16_ERR_INVALID;
+    if (!aligned16(x) || !aligned16(xq) || !aligned16(xscales)) return W4A16_ERR_INVALID;
+    if (K > kMaxK) return W4A16_ERR_UNSUPPORTED;
+    w4a16::clear_stale_error();
+    return from_hip(w4a16::launch_quant_mx4((int)act, x, M, K, xq, xscales, stream));
+}
+
+w4a16_status_t w4a16_gemm_w4a4(w4a16_format_t fmt, w4a16_dtype_t out, const uint8_t* xq, const uint8_t* xscales, int64_t M,
+                               const void* codes, const void* scales, const void* mins, int64_t N, int64_t K, void* y,
+                               hipStream_t stream) {
+    if (w4a16_status_t st = check_w4a4(fmt, out, M, codes, scales, mins, N, K, y); st != W4A16_OK) return st;
+    if (!aligned16(xq) || !aligned16(xscales)) return W4A16_ERR_INVALID;
+    w4a16::clear_stale_error();
+    return from_hip(w4a16::launch_gemm_w4a4((int)out, xq, xscales, M, static_cast<const uint8_t*>(codes),
+                                            static_cast<const uint8_t*>(scales), N, K, y, stream));
+}
+
+size_t w4a16_w4a4_workspace_bytes(w4a16_format_t fmt, int64_t M, int64_t N, int64_t K) {
+    if (fmt != W4A16_FMT_MX4_B32_E8M0 || check_shape(fmt, N, K) != W4A16_OK || M <= 0 || M > kMaxDim) return 0;
+    return W4A4Workspace(M, K).needed;
+}
+
+w4a16_status_t w4a16_matmul_w4a4(w4a16_format_t fmt, w4a16_dtype_t act, const void* x, int64_t M, const void* codes,
+                                 const void* scales, const void* mins, int64_t N, int64_t K, void* y, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream) {
+    if (w4a16_status_t st = check_w4a4(fmt, act, M, codes, scales, mins, N, K, y); st != W4A16_OK) return st;
+    if (!aligned16(x) || !aligned16(workspace)) return W4A16_ERR_INVALID;
+    const W4A4Workspace w(M, K);
+    if (workspace_bytes < w.needed) return W4A16_ERR_INVALID;
+    uint8_t* base = static_cast<uint8_t*>(workspace);
+    w4a16::clear_stale_error();
+    if (const hipError_t e = w4a16::launch_quant_mx4((int)act, x, M, K, base, base + w.scales, stream); e != hipSuccess)
+        return from_hip(e);
+    return from_hip(w4a16::launch_gemm_w4a4((int)act, base, base + w.scales, M, static_cast<const uint8_t*>(codes),
+                                            static_cast<const uint8_t*>(scales), N, K, y, stream));
+}
+
+int64_t w4a16_expert_layer_max_tokens(void) { return w4a16::kLayerTokens; }
+int64_t w4a16_expert_layer_max_pairs(void) { return w4a16::kLayerPairs; }
+
+size_t w4a16_expert_layer_workspace_bytes(int64_t T, int64_t topk, int64_t I) {
+    if (check_layer(T, topk, I) != W4A16_OK) return 0;
+    return (size_t)(T * topk) * (size_t)I + w4a16::expert_layer_scale_bytes(T * topk, I);  // (I % 16 == 0)
+}
+
+w4a16_status_t w4a16_expert_layer_w8a8(w4a16_format_t fmt, w4a16_dtype_t out, const int8_t* xq, const float* ascale, int64_t T,
+                                       const void* ids, int64_t id_bits, int64_t topk, const float* weights, int64_t E,
+                                       const void* up_codes, const void* up_scales, const void* down_codes,
+                                       const void* down_scales, int64_t H, int64_t I, void* y, void* workspace,
+                                       size_t workspace_bytes, hipStream_t stream) {
+    const w4a16_status_t st = check_layer(T, topk, I);
+    if (!valid_format(fmt) || !valid_dtype(out) || st == W4A16_ERR_INVALID) return W4A16_ERR_INVALID;
+    if (H <= 0 || H > kMaxDim || H % kW8RowAlign != 0 || E <= 0 || E > kMaxDim || (id_bits != 32 && id_bits != 64))
+        return W4A16_ERR_INVALID;
+    if (!aligned16(xq) || !aligned16(ascale) || !aligned16(ids) || !aligned16(weights) || !aligned16(y) || !aligned16(workspace))
+        return W4A16_ERR_INVALID;
+    if (!aligned16(up_codes) || !aligned16(up_scales) || !aligned16(down_codes) || !aligned16(down_scales))
+        return W4A16_ERR_INVALID;
+    if (fmt != W4A16_FMT_W8_ROW_FP32 || st != W4A16_OK || E > w4a16::kMaxExperts || H > kMaxKInt8) return W4A16_ERR_UNSUPPORTED;
+    if (workspace_bytes < w4a16_expert_layer_workspace_bytes(T, topk, I)) return W4A16_ERR_INVALID;
+    int8_t* hq = static_cast<int8_t*>(workspace);
+    w4a16::clear_stale_error();
+    return from_hip(w4a16::launch_expert_layer_w8a8(
+        (int)out, xq, ascale, T, ids, (int)id_bits, topk, weights, E, static_cast<const int8_t*>(up_codes),
+        static_cast<const float*>(up_scales), static_cast<const int8_t*>(down_codes), static_cast<const float*>(down_scales), H, I,
+        y, hq, reinterpret_cast<float*>(hq + T * topk * I), stream));
 }
 
 }  // extern "C"

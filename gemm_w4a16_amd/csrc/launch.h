@@ -193,4 +193,22 @@ size_t add_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t N);
 hipError_t launch_add_rmsnorm_backward(int dtype, const void* dy, const void* dh, const void* h, int64_t rows, int64_t N,
                                        const void* weight, float eps, void* dx, float* dweight, float* ws, hipStream_t stream);
 
+// The microscaled 4-bit format (codes [rows][K/2], scales as mx4.h lays them out): rows of `dtype` quantized, values
+// back, and the product of two arrays of it.
+hipError_t launch_quant_mx4(int dtype, const void* x, int64_t M, int64_t K, uint8_t* codes, uint8_t* scales, hipStream_t stream);
+hipError_t launch_dequant_mx4(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K, int dtype, void* out,
+                              hipStream_t stream);
+hipError_t launch_gemm_w4a4(int dtype, const uint8_t* xq, const uint8_t* xscales, int64_t M, const uint8_t* codes,
+                            const uint8_t* scales, int64_t N, int64_t K, void* y, hipStream_t stream);
+
+// A few tokens' whole pass through their experts; hq [T topk][I] and hscale (expert_layer_scale_bytes of it) hold the
+// experts' activations between the two launches.
+constexpr int64_t kLayerTokens = 32;
+constexpr int64_t kLayerPairs = 256;
+size_t expert_layer_scale_bytes(int64_t pairs, int64_t I);
+hipError_t launch_expert_layer_w8a8(int dtype, const int8_t* xq, const float* ascale, int64_t T, const void* ids, int id_bits,
+                                    int64_t topk, const float* weights, int64_t E, const int8_t* up, const float* up_scales,
+                                    const int8_t* down, const float* down_scales, int64_t H, int64_t I, void* y, int8_t* hq,
+                                    float* hscale, hipStream_t stream);
+
 }  // namespace w4a16

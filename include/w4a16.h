@@ -86,7 +86,20 @@ typedef enum {
      * scales fp32   [N]     s = max|w| / 127 per row (1.0 for an all-zero row)
      * mins   unused (pass NULL)
      * w_hat = q * s; K % 16 == 0; fp16 activations only.  Packed sizes: N*K and 4*N bytes. */
-    W4A16_FMT_W8_ROW_FP32 = 3
+    W4A16_FMT_W8_ROW_FP32 = 3,
+    /* Microscaled 4-bit floating point (OCP Microscaling Formats specification v1.0, MXFP4; secemp.blog
+     * "Hardware-invariant NVFP4 progress report 1" for a neighbour of it): blocks of 32 along K that share a
+     * power of two X = 2^(floor(log2 max|w|) - 2), its exponent not below -127, and elements with a sign, two exponent
+     * bits and a mantissa bit, of magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6 (codes 0..7, 8..15 negative)
+     * codes  uint8 [N][K/2]     byte j of a row = element of k = 2j (low nibble) and k = 2j+1 (high nibble)
+     * scales uint8 [T][N'][8]   T = K/256 and N' = N/16 x 16, both rounded up; byte (t, n, b) = 127 + log2 X of
+     *                           row n's block 8t + b, or 255 (NaN) for a block that holds an infinity or NaN
+     *                           (its elements 0).  Bytes past K are 0, those of rows past N are neither written
+     *                           nor of any effect.
+     * mins   unused (pass NULL)
+     * element = w / X to nearest, ties to even, magnitudes past 6 becoming 6; w_hat = element X; K % 32 == 0.  For
+     * the W4A4 calls (the 16-bit products return ERR_UNSUPPORTED).  Weights need not be finite. */
+    W4A16_FMT_MX4_B32_E8M0 = 4
 } w4a16_format_t;
 
 typedef enum {
@@ -110,6 +123,7 @@ const char* w4a16_status_string(w4a16_status_t status);
  * multiple of 4 bytes: the GEMM reads them as aligned 4-byte words, so when (K/128)*N is odd
  * the last word covers 2 bytes past the last element (read, never written, value unused).
  * Buffers passed to the matmul entry points must have at least these sizes.
+ * MX4 stores N*K/2 bytes of codes and a byte per block of 32 (and what its rows are rounded up by).
  * Pure host arithmetic; any output pointer may be NULL.  ERR_INVALID if N, K <= 0 or K is not a
  * multiple of the format's group (128, 32, or 16 for W8). */
 w4a16_status_t w4a16_packed_sizes(w4a16_format_t fmt, int64_t N, int64_t K,
@@ -413,6 +427,64 @@ w4a16_status_t w4a16_expert_combine_backward(w4a16_dtype_t act, const void* dy, 
                                              const int32_t* pos, const float* weights, int64_t N, void* dys,
                                              float* dweights, hipStream_t stream);
 
+/* A whole layer for a few tokens, in two launches (a decode step's form of the pass above, with the products up and
+ * down, SwiGLU between them, and no sorted copies): xq int8 [T][H] and ascale [T] as w4a16_quantize_rows_i8 or
+ * w4a16_add_rmsnorm_i8 writes them; ids [T][topk] (id_bits 32 or 64) and weights fp32 [T][topk] as for the calls above;
+ * W8 weights up_codes [E][2 I][H] with up_scales [E][2 I] (an expert's I gate rows, then its I up rows) and
+ * down_codes [E][H][I] with down_scales [E][H].  For pair (t, j) of expert e = ids[t][j]:
+ *   g_i = a_t s_i sum_k xq[t][k] up[e][i][k], u_i the same of row I + i; v_i = g_i / (1 + exp(-g_i)) u_i in fp32
+ *   v in 8-bit integers with a scale for each group of 64 columns (columns 64 c .. 64 c + 63; the last group may be
+ *   shorter): b = max|v| / 127, 1.0 where that is zero, NaN with codes 0 where v is not finite; hq = clamp(rint(v / b))
+ *   o_n = s_n sum over groups of b sum_i hq_i down[e][n][i], y[t][n] = sum_j weights[t][j] o_n in order of j
+ * The integer sums are exact, the rest fp32; y [T][H] (type `out`) is rounded once.  Pairs with no expert add
+ * nothing (their weights are not read into the sum); a token with none gets zeros.  A token that is not
+ * finite makes NaN of its own row only.  Bitwise reproducible; weights of experts that no token chose are not read.
+ * T at most w4a16_expert_layer_max_tokens(), T * topk at most w4a16_expert_layer_max_pairs(), E at most
+ * w4a16_max_experts(), H at most 2^17 - 16, I at most 2^22 (ERR_UNSUPPORTED above, and for formats but W8);
+ * H % 16 == 0, I % 16 == 0.  workspace (16-byte aligned): w4a16_expert_layer_workspace_bytes(T, topk, I) bytes, needs
+ * no initialisation and must not be shared by calls, or graphs of calls, that may run at the same time. */
+w4a16_status_t w4a16_expert_layer_w8a8(w4a16_format_t fmt, w4a16_dtype_t out, const int8_t* xq, const float* ascale, int64_t T,
+                                       const void* ids, int64_t id_bits, int64_t topk, const float* weights, int64_t E,
+                                       const void* up_codes, const void* up_scales, const void* down_codes,
+                                       const void* down_scales, int64_t H, int64_t I, void* y, void* workspace,
+                                       size_t workspace_bytes, hipStream_t stream);
+
+/* Most tokens and most (token, choice) pairs that w4a16_expert_layer_w8a8 takes. */
+int64_t w4a16_expert_layer_max_tokens(void);
+int64_t w4a16_expert_layer_max_pairs(void);
+
+/* Bytes of workspace w4a16_expert_layer_w8a8 needs (0 for sizes it refuses). */
+size_t w4a16_expert_layer_workspace_bytes(int64_t T, int64_t topk, int64_t I);
+
+/* ---- W4A4: activations and weights both in the MX4 format ----------------------------------------
+ * y[m][n] = sum over blocks of X_mb X_nb (sum of the elements' products), on the matrix instructions that take
+ * both scales; products are exact, sums fp32.  Activations and outputs may be bf16, fp16 or fp32; any M and N,
+ * K % 32 == 0. */
+
+/* Rows x [M][K] (type `act`) in the MX4 format: xq uint8 [M][K/2] and xscales as the format's scales with M for N
+ * (w4a16_packed_sizes of M x K gives both sizes).  Bit-identical to the definition, also for values that are not
+ * finite.  ERR_INVALID: type, sizes, alignment; ERR_UNSUPPORTED: K above 2^22. */
+w4a16_status_t w4a16_quantize_rows_mx4(w4a16_dtype_t act, const void* x, int64_t M, int64_t K, uint8_t* xq, uint8_t* xscales,
+                                       hipStream_t stream);
+
+/* y [M][N] (type `out`) from rows and weights in the MX4 format.  A block that is not a number makes NaN of its
+ * row's (or column's) outputs and of no others.  MX4 only (ERR_UNSUPPORTED otherwise).  Bitwise
+ * reproducible. */
+w4a16_status_t w4a16_gemm_w4a4(w4a16_format_t fmt, w4a16_dtype_t out, const uint8_t* xq, const uint8_t* xscales, int64_t M,
+                               const void* codes, const void* scales, const void* mins, int64_t N, int64_t K, void* y,
+                               hipStream_t stream);
+
+/* y [M][N] = x [M][K] . W_hat^T with x quantized on the way: bit for bit w4a16_quantize_rows_mx4 followed by
+ * w4a16_gemm_w4a4 with out = act.  workspace (16-byte aligned, w4a16_w4a4_workspace_bytes) holds the codes and
+ * scales of x; it needs no initialisation and must not be shared by calls, or graphs of calls, that may run at the
+ * same time.  Errors as for the two calls, and ERR_INVALID for a workspace that is NULL or too small. */
+w4a16_status_t w4a16_matmul_w4a4(w4a16_format_t fmt, w4a16_dtype_t act, const void* x, int64_t M, const void* codes,
+                                 const void* scales, const void* mins, int64_t N, int64_t K, void* y, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace w4a16_matmul_w4a4 needs (0 for a shape it refuses or another format). */
+size_t w4a16_w4a4_workspace_bytes(w4a16_format_t fmt, int64_t M, int64_t N, int64_t K);
+
 /* ---- RMS norm with a residual: what stands before a layer's products ------------------------------
  * Row t of x and residual [T][N] (type `act`): s = x + residual in fp32 (residual NULL: s = x), and
  *   h [T][N]  s rounded to `act`: the sum that goes on past the layer; NULL where it is not wanted
@@ -429,7 +501,7 @@ w4a16_status_t w4a16_add_rmsnorm(w4a16_dtype_t act, const void* x, const void* r
 
 /* v in 8-bit integers as w4a16_quantize_rows_i8 quantizes fp32 rows, N % 16 == 0: ascale [T] = max_n |v| / 127 (1.0
  * where that is zero, NaN with codes 0 where v is not finite) and xq int8 [T][N].  They are what w4a16_gemm_w8a8
- * takes. */
+ * and w4a16_expert_layer_w8a8 take. */
 w4a16_status_t w4a16_add_rmsnorm_i8(w4a16_dtype_t act, const void* x, const void* residual, int64_t T, int64_t N,
                                     const void* weight, float eps, void* h, int8_t* xq, float* ascale, hipStream_t stream);
 

@@ -1,0 +1,254 @@
+"""A few tokens' whole pass through their experts against its definition in 64 bits.
+
+Bounds.  F is 2^-24.  g and u are exact integers' conversion and two products: 3 F each.  v = g / (1 + exp(-g)) u: the
+exponential is off by 2 F of its own and 3 F |g| from its argument, and there are three operations more, so v is off by
+(16 + 4 |g|) F relative at most; the group's scale b by that of its largest value and a rounding.  A code differs
+from the definition's only where v / b lies within those errors of a border between two codes: there a whole step
+of b is allowed for, elsewhere none.  The sum over groups has a rounding each, and four more follow.
+"""
+import numpy as np
+import pytest
+import torch
+
+import gemm_w4a16_amd as w
+from test_gpu_memory_around_w8a8_experts import Arena
+
+pytestmark = pytest.mark.gpu
+
+F = 2.0 ** -24
+W8 = w.W4A16_FMT_W8_ROW_FP32
+TYPES = {"bf16": (w.W4A16_BF16, torch.bfloat16, 2.0 ** -8, 0.0), "f16": (w.W4A16_FP16, torch.float16, 2.0 ** -11, 2.0 ** -25),
+         "f32": (w.W4A16_FP32, torch.float32, F, 0.0)}
+GROUP = 64
+
+
+def data(T, topk, E, H, I, seed, pad=0.2):
+    g = torch.Generator().manual_seed(seed)
+    d = {"T": T, "topk": topk, "E": E, "H": H, "I": I}
+    d["xq"] = torch.randint(-127, 128, (T, H), generator=g, dtype=torch.int8)
+    d["ascale"] = torch.rand(T, generator=g) * 0.05 + 1e-3
+    d["up"] = torch.randint(-127, 128, (E, 2 * I, H), generator=g, dtype=torch.int8)
+    d["us"] = (torch.rand((E, 2 * I), generator=g) + 0.1) / (60 * H ** 0.5)
+    d["down"] = torch.randint(-127, 128, (E, H, I), generator=g, dtype=torch.int8)
+    d["ds"] = (torch.rand((E, H), generator=g) + 0.1) / (60 * I ** 0.5)
+    d["weights"] = torch.rand((T, topk), generator=g) - 0.2
+    ids = torch.randint(0, E, (T, topk), generator=g)
+    ids[torch.rand((T, topk), generator=g) < pad] = -1
+    d["ids"] = ids
+    return d
+
+
+def reference(d):
+    """(y, what it may be off by before its last rounding)."""
+    T, topk, E, H, I = (d[k] for k in ("T", "topk", "E", "H", "I"))
+    y, off = torch.zeros((T, H), dtype=torch.float64), torch.zeros((T, H), dtype=torch.float64)
+    G = (I + GROUP - 1) // GROUP
+    for t in range(T):
+        for j in range(topk):
+            e = int(d["ids"][t, j])
+            if not 0 <= e < E:
+                continue
+            gu = (d["up"][e].double() @ d["xq"][t].double()) * d["us"][e].double() * d["ascale"][t].double()
+            g, u = gu[:I], gu[I:]
+            v = g * torch.sigmoid(g) * u
+            rel = (16 + 4 * g.abs()) * F
+            fill = lambda a: torch.cat([a, torch.zeros(G * GROUP - I, dtype=torch.float64)]).reshape(G, GROUP)
+            v, rel = fill(v), fill(rel)
+            top, at = v.abs().max(1, keepdim=True)
+            b = torch.where(top == 0, torch.ones_like(top), top / 127)
+            rel_b = torch.gather(rel, 1, at) + 2 * F
+            q = torch.round(v / b)
+            near = ((v / b).abs() % 1 - 0.5).abs() <= (v / b).abs() * (rel + rel_b) + 1e-9
+            down = torch.zeros((H, G * GROUP), dtype=torch.float64)
+            down[:, :I] = d["down"][e].double()
+            s, wt = d["ds"][e].double(), d["weights"][t, j].double()
+            y[t] += (down @ (q * b).reshape(-1)) * s * wt
+            mag = down.abs() @ (q.abs() * b * (rel_b + (G + 8 + topk) * F)).reshape(-1)
+            off[t] += (mag + down.abs() @ (near * b * (1 + rel_b)).reshape(-1)) * s * wt.abs()
+    return y, off
+
+
+def run(d, kind, arena=None, bits=32, stream=None):
+    act, dt = TYPES[kind][:2]
+    put = arena.put if arena else lambda t: t.cuda()
+    T, topk, E, H, I = (d[k] for k in ("T", "topk", "E", "H", "I"))
+    y = arena.out((T, H), dt) if arena else torch.full((T, H), float("nan"), dtype=dt, device="cuda")
+    nb = w.w4a16_expert_layer_workspace_bytes(T, topk, I)
+    ws = arena.workspace(nb) if arena else torch.empty(nb, dtype=torch.uint8, device="cuda")
+    ids = put(d["ids"].to(torch.int32 if bits == 32 else torch.int64))
+    w.w4a16_expert_layer_w8a8(W8, act, put(d["xq"]), put(d["ascale"]), T, ids, bits, topk, put(d["weights"]), E, put(d["up"]),
+                              put(d["us"]), put(d["down"]), put(d["ds"]), H, I, y, ws, nb, stream=stream)
+    return y
+
+
+def check(y, d, kind):
+    _, _, u, tiny = TYPES[kind]
+    ref, off = reference(d)
+    err = (y.cpu().double() - ref).abs() - (u * ref.abs() + (1 + u) * off + tiny)
+    assert not y.isnan().any() and err.max().item() <= 0
+
+
+SHAPES = [(1, 1, 1, 16, 16), (1, 2, 8, 4096, 1024), (1, 1, 3, 48, 80), (2, 2, 4, 1008, 496), (5, 3, 20, 1008, 496), (3, 8, 64, 256, 64),
+          (8, 2, 8, 512, 2064), (9, 2, 2, 272, 400), (16, 1, 1, 144, 128), (17, 1, 1, 96, 192), (32, 8, 64, 128, 96), (32, 8, 9, 80, 272),
+          (32, 1, 1, 528, 64), (31, 8, 3, 64, 4112), (4, 64, 70, 64, 48), (1, 256, 512, 32, 16), (7, 5, 512, 112, 32), (6, 2, 3, 8208, 32),
+          (24, 4, 33, 2048, 320), (1, 8, 8, 2064, 112)]
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("T,topk,E,H,I", SHAPES)
+def test_layer(T, topk, E, H, I, kind):
+    d = data(T, topk, E, H, I, 1)
+    if T > 2:
+        d["ids"][1] = -1             # a padding token
+        d["ids"][2] = d["ids"][0, 0]  # one expert for all its choices
+    m = Arena()
+    y = run(d, kind, m, 64 if T % 2 else 32)
+    check(y, d, kind)
+    if T > 2:
+        assert (y[1] == 0).all()
+    m.check()
+
+
+@pytest.mark.parametrize("T,topk,E", [(32, 8, 64), (32, 8, 2), (9, 2, 40), (1, 8, 300)])
+def test_every_token_to_the_same_experts(T, topk, E):
+    d = data(T, topk, E, 288, 176, 2, 0.0)
+    d["ids"][:] = (torch.arange(topk) * 37 + E - 1) % E
+    check(run(d, "f32"), d, "f32")
+    d["ids"][:] = E - 1
+    check(run(d, "f32"), d, "f32")
+
+
+@pytest.mark.parametrize("bits", [32, 64])
+def test_ids_out_of_range_and_no_experts_at_all(bits):
+    d = data(6, 3, 5, 64, 96, 3, 0.0)
+    d["ids"][0] = torch.tensor([5, -1, 2])
+    d["ids"][1] = torch.tensor([-2 ** 31, 2 ** 31 - 1, 4])
+    d["ids"][2] = torch.tensor([7, 7, 7])
+    if bits == 64:
+        d["ids"][3] = torch.tensor([2 ** 32 + 1, -2 ** 40, 3])
+    d["weights"][d["ids"] < 0] = float("nan")
+    d["weights"][d["ids"] >= 5] = float("inf")
+    y = run(d, "f32", bits=bits)
+    check(y, d, "f32")
+    assert (y[2] == 0).all()
+    d["ids"][:] = -1
+    assert (run(d, "bf16", bits=bits) == 0).all()
+
+
+@pytest.mark.parametrize("T,topk,E,H,I", [(12, 2, 4, 128, 192), (32, 4, 3, 256, 64)])
+def test_a_token_that_is_not_finite_stays_its_own(T, topk, E, H, I):
+    d = data(T, topk, E, H, I, 4, 0.0)
+    clean = run(d, "bf16").cpu()
+    d["ascale"][3], d["ascale"][T - 1] = float("nan"), float("inf")
+    d["xq"][3] = 0
+    dirty = run(d, "bf16").cpu()
+    bad = torch.zeros(T, dtype=torch.bool)
+    bad[[3, T - 1]] = True
+    assert dirty[bad].isnan().all() and torch.equal(clean[~bad], dirty[~bad])
+
+
+def test_large_and_vanishing_gates():
+    """Gates far on either side of zero, where exp(-g) passes fp32's range or vanishes, and rows of zeros."""
+    d = data(4, 2, 3, 64, 128, 5, 0.0)
+    d["us"][:, :128] *= torch.logspace(-6, 3, 128)
+    d["xq"][1] = 0
+    y = run(d, "f32")
+    check(y, d, "f32")
+    assert (y[1] == 0).all()
+
+
+def test_captured_and_on_another_stream():
+    d = data(8, 2, 8, 512, 320, 6, 0.0)
+    T, topk, E, H, I = (d[k] for k in ("T", "topk", "E", "H", "I"))
+    t = {k: v.cuda() for k, v in d.items() if isinstance(v, torch.Tensor)}
+    y = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+    ws, nb = w.alloc_expert_layer_workspace(T, topk, I)
+    step = lambda stream=None: w.w4a16_expert_layer_w8a8(W8, w.W4A16_BF16, t["xq"], t["ascale"], T, t["ids"], 64, topk, t["weights"], E, t["up"],
+                                                         t["us"], t["down"], t["ds"], H, I, y, ws, nb, stream=stream)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    s = torch.cuda.Stream()
+    for seed in range(4):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        t["ids"].copy_(torch.randint(-1, E, (T, topk), generator=g, device="cuda"))
+        t["ascale"].copy_(torch.rand(T, generator=g, device="cuda") * 0.05)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = y.clone()
+        ws.fill_(0xFF)
+        y.fill_(0)
+        torch.cuda.synchronize()
+        step(s)
+        s.synchronize()
+        assert torch.equal(got, y)
+
+
+def test_weights_past_32_bit_offsets():
+    """More than 2^32 bytes of up weights: the last experts' rows are those of a call with them alone."""
+    T, topk, H, I = 3, 2, 4096, 2048
+    E = (1 << 32) // (2 * H * I) + 4
+    d = data(T, topk, 2, H, I, 7, 0.0)
+    want = run(d, "f32")
+    up, down = (torch.zeros((E, n, k), dtype=torch.int8, device="cuda") for n, k in ((2 * I, H), (H, I)))
+    us, ds = torch.ones((E, 2 * I), device="cuda"), torch.ones((E, H), device="cuda")
+    up[-2:], down[-2:], us[-2:], ds[-2:] = d["up"].cuda(), d["down"].cuda(), d["us"].cuda(), d["ds"].cuda()
+    y = torch.empty((T, H), device="cuda")
+    ws, nb = w.alloc_expert_layer_workspace(T, topk, I)
+    w.w4a16_expert_layer_w8a8(W8, w.W4A16_FP32, d["xq"].cuda(), d["ascale"].cuda(), T, (d["ids"] + E - 2).cuda(), 64, topk,
+                              d["weights"].cuda(), E, up, us, down, ds, H, I, y, ws, nb)
+    assert torch.equal(y, want)
+
+
+def test_a_decode_step_of_all_together():
+    """Norm with the residual in 8 bits, the experts' layer on its rows, the next norm, and a 4-bit product of that, in
+    one captured graph: each step against 64 bits on what the step before wrote."""
+    T, topk, E, H, I, N = 5, 2, 4, 512, 192, 300
+    g = torch.Generator().manual_seed(8)
+    d = data(T, topk, E, H, I, 9, 0.0)
+    t = {k: v.cuda() for k, v in d.items() if isinstance(v, torch.Tensor)}
+    bf, act, eps = torch.bfloat16, w.W4A16_BF16, 1e-5
+    mx4 = w.W4A16_FMT_MX4_B32_E8M0
+    x, res = (torch.randn((T, H), generator=g).to(bf).cuda() for _ in range(2))
+    n1, n2 = ((1 + 0.2 * torch.randn(H, generator=g)).to(bf).cuda() for _ in range(2))
+    wt = torch.randn((N, H), generator=g) * 0.05
+    codes, scales, _ = w.alloc_packed(mx4, N, H)
+    w.w4a16_quantize_pack(mx4, wt.cuda(), N, H, codes, scales, None)
+    h, y, h2, z = (torch.empty((T, H), dtype=bf, device="cuda") for _ in range(4))
+    out = torch.empty((T, N), dtype=bf, device="cuda")
+    xq, a = torch.empty((T, H), dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    lws, lnb = w.alloc_expert_layer_workspace(T, topk, I)
+    pws, pnb = w.alloc_w4a4_workspace(mx4, T, N, H)
+
+    def step():
+        w.w4a16_add_rmsnorm_i8(act, x, res, T, H, n1, eps, h, xq, a)
+        w.w4a16_expert_layer_w8a8(W8, act, xq, a, T, t["ids"], 64, topk, t["weights"], E, t["up"], t["us"], t["down"], t["ds"], H, I, y,
+                                  lws, lnb)
+        w.w4a16_add_rmsnorm(act, y, h, T, H, n2, eps, h2, z)
+        w.w4a16_matmul_w4a4(mx4, act, z, T, codes, scales, None, N, H, out, pws, pnb)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in range(3):
+        res.copy_(torch.randn((T, H), generator=g).to(bf))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [v.clone() for v in (h, xq, a, y, h2, z, out)]
+        step()
+        assert all(torch.equal(p, q) for p, q in zip(got, (h, xq, a, y, h2, z, out)))
+        s = x.cpu().float() + res.cpu().float()
+        assert torch.equal(h.cpu(), s.to(bf))
+        v = s.double() / torch.sqrt((s.double() ** 2).mean(1, keepdim=True) + eps) * n1.cpu().double()
+        assert ((xq.cpu().double() * a.cpu().double()[:, None] - v).abs() <= a.cpu().double()[:, None] * 0.501 + 40 * F * v.abs()).all()
+        check(y, {**d, "xq": xq.cpu(), "ascale": a.cpu()}, "bf16")
+        s = h.cpu().double() + y.cpu().double()
+        v = s / torch.sqrt((s * s).mean(1, keepdim=True) + eps) * n2.cpu().double()
+        assert ((z.cpu().double() - v).abs() <= (2.0 ** -8 + 40 * F) * v.abs()).all()
+        from test_gpu_mx4 import product
+        ref, mag = product(z.cpu(), wt)
+        assert ((out.cpu().double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 1.01 * H * 2 * F * mag).all()

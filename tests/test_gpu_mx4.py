@@ -1,0 +1,273 @@
+"""The microscaled 4-bit format on the GPU: rows and weights bit-exact with the definition in 64 bits, values back
+exact, and the W4A4 product against exact products of those values.
+
+Bound of a product: K products, exact, are added in fp32 in an order that the matrix instructions choose.  Each
+addition is off by at most one rounding, to nearest or toward zero, of a partial sum no larger than the sum of the
+magnitudes: K 2^-23 of that sum in all, and the output type's rounding.  A sum below fp32's normal numbers (2^-126) may
+be taken as zero.
+"""
+import numpy as np
+import pytest
+import torch
+
+import gemm_w4a16_amd as w
+from test_gpu_memory_around_w8a8_experts import Arena
+
+pytestmark = pytest.mark.gpu
+
+MX4 = w.W4A16_FMT_MX4_B32_E8M0
+F = 2.0 ** -24
+TYPES = {"bf16": (w.W4A16_BF16, torch.bfloat16, 2.0 ** -8, 0.0), "f16": (w.W4A16_FP16, torch.float16, 2.0 ** -11, 2.0 ** -25),
+         "f32": (w.W4A16_FP32, torch.float32, F, 0.0)}
+MAGNITUDES = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6])
+
+
+def rows(M, K, dt, seed):
+    """Random rows with what a quantizer can get wrong among the first: zeros, every border between elements, the
+    largest magnitudes just below a power of two, the smallest and largest numbers of the type."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((M, K), generator=g)
+    if M > 1:
+        x[1, :32] = 0
+        if K > 32:
+            x[1, 32:64] = -0.0
+    if M > 2:
+        b = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, 7.0, 7.5, 0.24, 0.26, 4.9, 5.1, 0.0, -0.0])
+        x[2, :32] = torch.cat([b, -b])
+        if K > 32:
+            x[2, 32:64] = torch.cat([b, -b]) * 2.0 ** -9
+    if M > 3:
+        x[3] *= 2.0 ** -12
+    if M > 4:
+        x[4] *= 2.0 ** torch.randint(-14, 10, (K,), generator=g).float()
+    x = x.to(dt)
+    if M > 5:
+        x[5, :32] = torch.finfo(dt).smallest_normal * torch.randn(32, generator=g).to(dt) / 64
+        x[5, 3] = torch.finfo(dt).max if K == 32 else 0
+    return x
+
+
+def quantized(x):
+    """The definition in 64 bits: (elements' codes [M][K], blocks' scale bytes [M][K/32])."""
+    v = x.double().numpy()
+    M, K = v.shape
+    b = v.reshape(M, K // 32, 32)
+    top = np.abs(b).max(2)
+    bad = ~np.isfinite(top)
+    e = np.where((top > 0) & ~bad, np.frexp(np.where(bad, 1.0, top))[1] - 1, -1000)  # top = m 2^e with 1 <= m < 2
+    e = np.maximum(e - 2, -127)
+    a = np.abs(b) * np.exp2(-e.astype(np.float64))[:, :, None]
+    a = np.where(bad[:, :, None], 0.0, a)
+    d = np.abs(a[..., None] - MAGNITUDES)
+    near = d.min(-1, keepdims=True)
+    # of two elements equally near, the one of even code
+    code = np.where(d == near, np.arange(8) + 100 * (np.arange(8) % 2), 1000).min(-1) % 100
+    code = code + 8 * np.signbit(b)
+    code = np.where(bad[:, :, None], 0, code)
+    return code.reshape(M, K).astype(np.uint8), np.where(bad, 255, e + 127).astype(np.uint8)
+
+
+def packed(code, scale):
+    """The arrays of the format, without the rows that pad the scales."""
+    M, G = scale.shape
+    T = (G + 7) // 8
+    s = np.zeros((M, T * 8), np.uint8)
+    s[:, :G] = scale
+    return code[:, 0::2] | code[:, 1::2] << 4, s.reshape(M, T, 8).transpose(1, 0, 2)
+
+
+def values(code, scale):
+    m = MAGNITUDES[code & 7] * np.where(code & 8, -1.0, 1.0)
+    X = np.where(scale == 255, np.nan, np.exp2(scale.astype(np.float64) - 127))
+    return torch.from_numpy(m * np.repeat(X, 32, 1))
+
+
+def on_gpu(x, kind, arena=None):
+    """Rows quantized by the library."""
+    M, K = x.shape
+    xq, xs, _ = w.alloc_packed(MX4, M, K)
+    if arena:
+        xq, xs = arena.out(xq.shape, torch.uint8), arena.out(xs.shape, torch.uint8)
+    w.w4a16_quantize_rows_mx4(TYPES[kind][0], arena.put(x) if arena else x.cuda(), M, K, xq, xs)
+    return xq, xs
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("M,K", [(1, 32), (5, 64), (6, 32), (37, 2080), (300, 4096), (17, 288), (1000, 96), (3, 40000)])
+def test_rows_bit_exact(M, K, kind):
+    act, dt = TYPES[kind][:2]
+    m, x = Arena(), rows(M, K, dt, 1)
+    xq, xs = on_gpu(x, kind, m)
+    ref = packed(*quantized(x))
+    np.testing.assert_array_equal(xq.cpu().numpy(), ref[0])
+    np.testing.assert_array_equal(xs.cpu().numpy()[:, :M], ref[1])
+    assert (xs[:, M:] == 0xFF).all()
+    m.check()
+    if kind == "f32":  # weights are quantized the same way
+        codes, scales = m.out(xq.shape, torch.uint8), m.out(xs.shape, torch.uint8)
+        w.w4a16_quantize_pack(MX4, m.put(x), M, K, codes, scales, None)
+        assert torch.equal(codes, xq) and torch.equal(scales, xs)
+    for out, t in (("bf16", torch.bfloat16), ("f16", torch.float16), ("f32", torch.float32)):
+        v = m.out((M, K), t)
+        w.w4a16_dequant(MX4, xq, xs, None, M, K, TYPES[out][0], v)
+        want = values(*quantized(x)).float().to(t)  # (exact in fp32, then rounded once)
+        assert torch.equal(v.cpu(), want)
+    m.check()
+
+
+def test_smallest_and_largest_numbers():
+    """fp32 from the subnormal numbers to the largest: exponents of blocks over the whole range of their byte."""
+    g = torch.Generator().manual_seed(3)
+    e = torch.arange(-149, 128).repeat_interleave(32).double()
+    mant = 1 + torch.rand(e.shape, generator=g).double()
+    x = (mant * torch.exp2(e)).clamp(max=torch.finfo(torch.float32).max).float().reshape(277, 32)
+    x = x * torch.where(torch.rand(x.shape, generator=g) < 0.5, -1.0, 1.0)
+    x[:, 5:] *= torch.rand((277, 27), generator=g)
+    xq, xs = on_gpu(x, "f32")
+    code, scale = quantized(x)
+    ref = packed(code, scale)
+    np.testing.assert_array_equal(xs.cpu().numpy()[:, :277], ref[1])
+    np.testing.assert_array_equal(xq.cpu().numpy(), ref[0])
+    assert scale.min() == 0 and scale.max() == 252
+    v = torch.empty((277, 32), device="cuda")
+    w.w4a16_dequant(MX4, xq, xs, None, 277, 32, w.W4A16_FP32, v)
+    assert torch.equal(v.cpu().double(), values(code, scale))
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_blocks_that_are_not_finite(kind):
+    x = rows(9, 160, TYPES[kind][1], 5)
+    x[0, 40], x[3, 159], x[7, 0] = float("inf"), float("nan"), float("-inf")
+    xq, xs = on_gpu(x, kind)
+    code, scale = quantized(x)
+    assert (scale == 255).sum() == 3
+    ref = packed(code, scale)
+    np.testing.assert_array_equal(xq.cpu().numpy(), ref[0])
+    np.testing.assert_array_equal(xs.cpu().numpy()[:, :9], ref[1])
+    v = torch.empty((9, 160), device="cuda")
+    w.w4a16_dequant(MX4, xq, xs, None, 9, 160, w.W4A16_FP32, v)
+    assert torch.equal(v.cpu().double().isnan(), values(code, scale).isnan())
+
+
+def product(x, wt):
+    """(exact product, sum of magnitudes) of the values that rows and weights stand for, on the GPU in 64 bits."""
+    a, b = values(*quantized(x)).cuda(), values(*quantized(wt)).cuda()
+    return (a @ b.t().contiguous()).cpu(), (a.abs() @ b.abs().t().contiguous()).cpu()
+
+
+SHAPES = [(1, 1, 32), (1, 4100, 64), (1, 1001, 4096), (2, 61, 96), (3, 300, 2080), (5, 2049, 1056), (8, 512, 288), (16, 700, 4096),
+          (17, 1001, 2080), (31, 64, 32), (37, 1001, 2080), (64, 257, 544), (65, 2000, 128), (100, 515, 20000), (129, 130, 256), (200, 1030, 8192),
+          (257, 520, 1024), (300, 2050, 1312), (520, 4104, 512), (1030, 1030, 160), (1500, 770, 320), (40, 16400, 96), (4, 8192, 16384)]
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_product(M, N, K, kind):
+    act, dt, u, tiny = TYPES[kind]
+    m = Arena()
+    x = rows(M, K, dt, 7)
+    if M > 5:
+        x[5, 3] = 0  # (the largest number, whose products leave fp16's range)
+    wt = torch.randn((N, K), generator=torch.Generator().manual_seed(8)) * 0.05
+    codes, scales = on_gpu(wt, "f32", m)
+    nb = w.w4a16_w4a4_workspace_bytes(MX4, M, N, K)
+    y, dx = m.out((M, N), dt), m.put(x)
+    w.w4a16_matmul_w4a4(MX4, act, dx, M, codes, scales, None, N, K, y, m.workspace(nb), nb)
+    ref, mag = product(x, wt)
+    err = (y.cpu().double() - ref).abs() - (u * ref.abs() + (1 + u) * K * 2 * F * mag + tiny + 2.0 ** -126)
+    assert not y.isnan().any() and err.max().item() <= 0
+    m.check()
+    xq, xs = on_gpu(x, kind, m)
+    y2 = m.out((M, N), dt)
+    w.w4a16_gemm_w4a4(MX4, act, xq, xs, M, codes, scales, None, N, K, y2)
+    assert torch.equal(y, y2)
+    m.check()
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_whole_numbers_are_exact(M, N, K):
+    """Elements that are whole numbers with scales of 1, 2 and 4: every partial sum is one below 2^24, so any order of
+    additions gives it, and a wrong pairing of values or scales does not."""
+    rng = np.random.default_rng(9)
+    def arrays(R):
+        code = rng.choice([0, 0, 2, 4, 10], (R, K)).astype(np.uint8)
+        scale = rng.choice([127, 128, 129], (R, K // 32)).astype(np.uint8)
+        if K > 8192:
+            scale[:] = 127
+        q, s = packed(code, scale)
+        full = np.full((s.shape[0], (R + 15) // 16 * 16, 8), 0xFF, np.uint8)
+        full[:, :R] = s
+        return torch.from_numpy(q).cuda(), torch.from_numpy(full).cuda(), values(code, scale).cuda()
+    xq, xs, xv = arrays(M)
+    wq, ws, wv = arrays(N)
+    y = torch.empty((M, N), device="cuda")
+    w.w4a16_gemm_w4a4(MX4, w.W4A16_FP32, xq, xs, M, wq, ws, None, N, K, y)
+    assert (xv.abs() @ wv.abs().t().contiguous()).max() < 2 ** 24
+    assert torch.equal(y.double(), xv @ wv.t().contiguous())
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 100, 512), (20, 200, 288), (300, 300, 1056)])
+def test_a_block_that_is_not_finite_stays_its_rows(M, N, K):
+    x = rows(M, K, torch.bfloat16, 11)
+    if M > 5:
+        x[5, 3] = 0
+    wt = torch.randn((N, K), generator=torch.Generator().manual_seed(12)) * 0.05
+    out = []
+    for hurt in (False, True):
+        if hurt:
+            x[M // 2, K - 1], wt[N // 3, 5] = float("inf"), float("nan")
+        codes, scales = on_gpu(wt, "f32")
+        y = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+        ws, nb = w.alloc_w4a4_workspace(MX4, M, N, K)
+        w.w4a16_matmul_w4a4(MX4, w.W4A16_BF16, x.cuda(), M, codes, scales, None, N, K, y, ws, nb)
+        out.append(y.cpu())
+    bad = torch.zeros((M, N), dtype=torch.bool)
+    bad[M // 2], bad[:, N // 3] = True, True
+    assert out[1][bad].isnan().all() and torch.equal(out[0][~bad], out[1][~bad])
+
+
+def test_captured_and_on_another_stream():
+    M, N, K = 20, 1001, 2080
+    wt = torch.randn((N, K), generator=torch.Generator().manual_seed(13)) * 0.05
+    codes, scales = on_gpu(wt, "f32")
+    x = torch.empty((M, K), dtype=torch.bfloat16, device="cuda")
+    y = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    ws, nb = w.alloc_w4a4_workspace(MX4, M, N, K)
+    step = lambda stream=None: w.w4a16_matmul_w4a4(MX4, w.W4A16_BF16, x, M, codes, scales, None, N, K, y, ws, nb, stream=stream)
+    x.copy_(rows(M, K, torch.bfloat16, 14))
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    s = torch.cuda.Stream()
+    for seed in range(4):
+        x.copy_(rows(M, K, torch.bfloat16, 20 + seed))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = y.clone()
+        y.fill_(0)
+        torch.cuda.synchronize()
+        step(s)
+        s.synchronize()
+        assert torch.equal(got, y)
+
+
+def test_rows_past_32_bit_offsets():
+    """More than 2^32 bytes of activations and 2^31 outputs: the last rows are those of a call of their own."""
+    K, N = 2048, 1040
+    M = (1 << 31) // N + 37
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    x[-40:] = torch.randn((40, K), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    wt = torch.randn((N, K), generator=torch.Generator().manual_seed(15)) * 0.05
+    codes, scales = on_gpu(wt, "f32")
+    y = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    ws, nb = w.alloc_w4a4_workspace(MX4, M, N, K)
+    w.w4a16_matmul_w4a4(MX4, w.W4A16_BF16, x, M, codes, scales, None, N, K, y, ws, nb)
+    last, y40 = x[-40:].clone(), torch.empty((40, N), dtype=torch.bfloat16, device="cuda")
+    w.w4a16_matmul_w4a4(MX4, w.W4A16_BF16, last, 40, codes, scales, None, N, K, y40, ws, nb)
+    u, bound = 2.0 ** -8, K * 2 * F
+    ref, mag = product(last.cpu(), wt)
+    for got in (y[-40:], y40):  # (another tile may add in another order)
+        assert ((got.cpu().double() - ref).abs() <= u * ref.abs() + (1 + u) * bound * mag).all()
+    assert (y[:-40] == 0).all()

@@ -169,7 +169,7 @@ struct W4A4Workspace {
 w4a16_status_t check_layer(int64_t T, int64_t topk, int64_t I) {
     if (T <= 0 || T > kMaxDim || topk <= 0 || topk > kMaxDim || I <= 0 || I > kMaxDim || I % kW8RowAlign != 0)
         return W4A16_ERR_INVALID;
-    if (T > w4a16::kLayerTokens || T * topk > w4a16::kLayerPairs || 2 * I > kMaxN || I > kMaxK) return W4A16_ERR_UNSUPPORTED;
+    if (T > w4a16::kLayerTokens || T * topk > w4a16::kLayerPairs || I > kMaxKInt8) return W4A16_ERR_UNSUPPORTED;
     return W4A16_OK;
 }
 

@@ -12,6 +12,9 @@ namespace w4a16 {
 // more items than that walk them with a stride of the grid.
 constexpr int64_t kMaxGridBlocks = (int64_t)1 << 21;
 
+// Bytes of weights from which those that a call reads once are copied past the Infinity Cache (w8a8.hip has the figures).
+constexpr double kOnceBytes = 64 << 20;
+
 // ---- activation types ---------------------------------------------------------------------------
 // Raw storage types: a distinct struct per 16-bit type, so that templates tell them apart.
 struct bf16_t {

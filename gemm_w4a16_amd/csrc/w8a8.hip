@@ -119,7 +119,6 @@ __device__ __forceinline__ float scaled_sum(int32_t sum, float sn, float am) {
 // row of 14336 x 4096 (56 MiB) takes 12.6 us so against 14.2 from HBM, and 11.9 against 11.0 where it shares the cache
 // with two more such matrices.
 constexpr int kOnceRows = 64;
-constexpr double kOnceBytes = 64 << 20;
 
 // What x is: int8 rows; int8 rows sorted by expert; or a few rows of activations (TO) that every block
 // quantizes for itself (kFused: no other launch, and x stays in LDS whole, behind the ring).

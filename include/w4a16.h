@@ -440,7 +440,7 @@ w4a16_status_t w4a16_expert_combine_backward(w4a16_dtype_t act, const void* dy, 
  * nothing (their weights are not read into the sum); a token with none gets zeros.  A token that is not
  * finite makes NaN of its own row only.  Bitwise reproducible; weights of experts that no token chose are not read.
  * T at most w4a16_expert_layer_max_tokens(), T * topk at most w4a16_expert_layer_max_pairs(), E at most
- * w4a16_max_experts(), H at most 2^17 - 16, I at most 2^22 (ERR_UNSUPPORTED above, and for formats but W8);
+ * w4a16_max_experts(), H and I at most 2^17 - 16 (ERR_UNSUPPORTED above, and for formats but W8);
  * H % 16 == 0, I % 16 == 0.  workspace (16-byte aligned): w4a16_expert_layer_workspace_bytes(T, topk, I) bytes, needs
  * no initialisation and must not be shared by calls, or graphs of calls, that may run at the same time. */
 w4a16_status_t w4a16_expert_layer_w8a8(w4a16_format_t fmt, w4a16_dtype_t out, const int8_t* xq, const float* ascale, int64_t T,

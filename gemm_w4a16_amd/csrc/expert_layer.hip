@@ -27,58 +27,91 @@ constexpr int kPairs = (int)kLayerPairs;
 
 // ---- the pairs, sorted by expert and cut into tiles of at most XR rows of one expert -------------------
 
+constexpr int kExperts = (int)kMaxExperts;
+constexpr int kPairWaves = kPairs / kWave;
+
+template <int XR>
 struct alignas(16) PairTiles {
-    int ids[kPairs];             // a pair's expert, INT32_MAX for none
-    uint16_t sorted[kPairs];     // pairs by expert, those of one expert in their own order
-    uint16_t first[kPairs + 1];  // a tile's first place in sorted; first[tiles] the number of pairs with an expert
-    int heads[kPairs / kWave], tiles;
+    union {
+        uint8_t count[kPairWaves][kExperts];  // pairs of an expert among a wave's 64
+        uint8_t row[kPairs][XR];              // a tile's pairs
+    };
+    uint16_t base[kExperts];                  // an expert's first tile
+    uint16_t expert[kPairs], rows[kPairs];    // of a tile
+    int wave_tiles[kPairWaves], tiles;
 };
 
-// By every block for itself: a thread a pair, which counts the pairs that come before its own.  At least kPairs
-// threads.  Ends with a barrier.
+// By every block for itself, the same in all of them: tiles in order of experts, an expert's pairs in their own order.
+// At least kPairs threads, a thread a pair, then a thread two experts.  Returns this thread's pair's expert (-1: none).
+// Ends with a barrier.
 template <int XR, typename TI>
-__device__ __forceinline__ void sort_pairs(const TI* __restrict__ ids, int P, int E, PairTiles& s) {
-    const int p = threadIdx.x;
-    int e = INT32_MAX;
+__device__ __forceinline__ int sort_pairs(const TI* __restrict__ ids, int P, int E, PairTiles<XR>& s) {
+    static_assert(kExperts == 2 * kPairs, "a thread two experts");
+    const int p = threadIdx.x, wave = wave_id(), lane = lane_id();
+    int e = -1;
     if (p < P) {
         const TI id = ids[p];
         if (id >= 0 && id < E) e = (int)id;
     }
-    if (p < kPairs) s.ids[p] = e;
+    for (int i = p; i < kPairWaves * kExperts / 16; i += blockDim.x) reinterpret_cast<uint4*>(s.count)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    int less = 0, same = 0;
-    if (p < P) {
-        for (int q = 0; q < P; q += 4) {  // (places from P on hold INT32_MAX)
-            const int4 v = *reinterpret_cast<const int4*>(s.ids + q);
-            const int f[4] = {v.x, v.y, v.z, v.w};
+    // this pair's place among its expert's in the wave: one expert at a time
+    int same = 0;
+    uint64_t left = __ballot(e >= 0);
+    while (left != 0) {
+        const int f = __builtin_amdgcn_readlane(e, __ffsll((unsigned long long)left) - 1);
+        const uint64_t m = __ballot(e == f);
+        if (e == f) {
+            same = __popcll(m & ((1ull << lane) - 1));
+            if ((m >> lane) == 1) s.count[wave][f] = (uint8_t)(same + 1);
+        }
+        left &= ~m;
+    }
+    __syncthreads();
+    int before[2], tiles[2], count[2];
+    if (wave < kPairWaves) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                less += f[i] < e;
-                same += f[i] == e && q + i < p;
+        for (int w = 0; w < kPairWaves; ++w)
+            if (w < wave && e >= 0) same += s.count[w][e];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            count[i] = 0;
+#pragma unroll
+            for (int w = 0; w < kPairWaves; ++w) count[i] += s.count[w][2 * p + i];
+            tiles[i] = (count[i] + XR - 1) / XR;
+        }
+        int end = tiles[0] + tiles[1];
+#pragma unroll
+        for (int off = 1; off < kWave; off <<= 1) {
+            const int v = __shfl_up(end, off);
+            if (lane >= off) end += v;
+        }
+        if (lane == kWave - 1) s.wave_tiles[wave] = end;
+        before[0] = end - tiles[0] - tiles[1];
+    }
+    __syncthreads();  // (count is read: row may overwrite it)
+    if (wave < kPairWaves) {
+        int all = 0;
+#pragma unroll
+        for (int w = 0; w < kPairWaves; ++w) {
+            if (w < wave) before[0] += s.wave_tiles[w];
+            all += s.wave_tiles[w];
+        }
+        before[1] = before[0] + tiles[0];
+        if (p == 0) s.tiles = all;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            s.base[2 * p + i] = (uint16_t)before[i];
+            for (int t = 0; t < tiles[i]; ++t) {
+                s.expert[before[i] + t] = (uint16_t)(2 * p + i);
+                s.rows[before[i] + t] = (uint16_t)min(count[i] - XR * t, XR);
             }
         }
-        // a pair that begins a tile is marked
-        if (e != INT32_MAX) s.sorted[less + same] = (uint16_t)(p | (same % XR == 0 ? 0x8000 : 0));
-    }
-    const int n = __syncthreads_count(e != INT32_MAX);
-    const bool head = p < n && (s.sorted[p] & 0x8000);
-    const uint64_t heads = __ballot(head);
-    if (p < kPairs && lane_id() == 0) s.heads[wave_id()] = __popcll(heads);
-    __syncthreads();
-    if (p < kPairs) {
-        int before = 0, all = 0;
-#pragma unroll
-        for (int w = 0; w < kPairs / kWave; ++w) {
-            if (w < wave_id()) before += s.heads[w];
-            all += s.heads[w];
-        }
-        if (head) {
-            s.first[before + __popcll(heads & ((1ull << lane_id()) - 1))] = (uint16_t)p;
-            s.sorted[p] &= 0x7FFF;
-        }
-        if (p == 0) s.first[all] = (uint16_t)n, s.tiles = all;
     }
     __syncthreads();
+    if (e >= 0) s.row[s.base[e] + same / XR][same % XR] = (uint8_t)p;
+    __syncthreads();
+    return e;
 }
 
 // ---- a wave's own stream of operands -------------------------------------------------------------------
@@ -117,54 +150,64 @@ __device__ __forceinline__ T* uniform(T* p) {
 
 // ---- up products and SwiGLU ----------------------------------------------------------------------------
 
-// A block: one tile of pairs, one group of 64 columns of v.  Wave (cw, ks): 16 of the columns (their gate rows and up
-// rows, 32 weight rows), every KS-th k-tile.
-template <int XR, int KS>
+// A block: one tile of pairs, one group of 64 columns of v; a wave 16 of the columns (their gate rows and up rows, 32
+// weight rows).  Two stages a wave, so that four blocks share a CU: while one sorts or finishes, the others stream
+// (three stages, two blocks a CU: 49 us against 43 for 32 tokens x 8 of 64 experts, H = 2048, I = 1024).
+template <int XR>
 struct UpShape {
-    static constexpr int NW = 4 * KS, kStage = 4096 + 128 * XR, kCopies = 4 + XR / 8;
-    static constexpr int R = KS == 1 && XR == 8 ? 4 : 3;
-    static constexpr size_t kLds = (size_t)NW * R * kStage;
-    static_assert(kLds >= sizeof(PairTiles) && kLds >= 4 * 2 * 1024 * (KS - 1) + 1024, "the ring holds what comes before and after it");
+    static constexpr int R = 2, kStage = 4096 + 128 * XR, kCopies = 4 + XR / 8;
+    static constexpr size_t kLds = 4 * R * kStage;
+    static_assert(kLds >= sizeof(PairTiles<XR>), "the lists fit in the ring");
 };
 
-template <typename TI, int XR, int KS, bool kOnce>
-__global__ __launch_bounds__(256 * KS) void layer_up_kernel(const int8_t* __restrict__ xq, const float* __restrict__ ascale,
+template <typename TI, int XR, bool kOnce>
+__global__ __launch_bounds__(256) void layer_up_kernel(const int8_t* __restrict__ xq, const float* __restrict__ ascale,
                                                             const TI* __restrict__ ids, int P, int topk, int E,
                                                             const int8_t* __restrict__ up, const float* __restrict__ up_scales, int H,
                                                             int I, int groups, int8_t* __restrict__ hq, float* __restrict__ hscale) {
-    using S = UpShape<XR, KS>;
+    using S = UpShape<XR>;
     constexpr int R = S::R, C = S::kCopies;
     __shared__ __attribute__((aligned(1024))) char smem[S::kLds];
     const int tile = blockIdx.x / groups, group = blockIdx.x - tile * groups;
     const int lane = lane_id(), wave = wave_id(), l16 = lane & 15, kg = lane >> 4;
-    const int cw = wave % 4, ks0 = wave / 4;
-    PairTiles& s = *reinterpret_cast<PairTiles*>(smem);
+    PairTiles<XR>& s = *reinterpret_cast<PairTiles<XR>*>(smem);
     sort_pairs<XR>(ids, P, E, s);
     if (tile >= s.tiles) return;
-    const int first = s.first[tile], rows = s.first[tile + 1] - first;
-    const int expert = __builtin_amdgcn_readfirstlane(s.ids[s.sorted[first]]);
-    const int pair = s.sorted[first + min(l16, rows - 1)];  // of this lane's row
+    const int rows = s.rows[tile], expert = __builtin_amdgcn_readfirstlane(s.expert[tile]);
+    const int pair = s.row[tile][min(l16, rows - 1)];  // of this lane's row
     uint32_t xoff[XR / 8], woff[2];
 #pragma unroll
     for (int i = 0; i < XR / 8; ++i) {
         const int r = 8 * i + lane / 8;
-        xoff[i] = (uint32_t)(s.sorted[first + min(r, rows - 1)] / topk) * (uint32_t)H + 16u * copied_chunk(r);
+        xoff[i] = (uint32_t)(s.row[tile][min(r, rows - 1)] / topk) * (uint32_t)H + 16u * copied_chunk(r);
+    }
+    const int i0 = group * kGroup + 16 * wave;
+    // the scales, asked for before the operands
+    float a = 0.0f;
+    float4 sg = {}, su = {};
+    if (i0 < I) {  // (I % 16 == 0: all of a wave's columns are there, or none)
+        a = ascale[pair / topk];
+        sg = *reinterpret_cast<const float4*>(up_scales + (size_t)expert * 2 * I + i0 + 4 * kg);
+        su = *reinterpret_cast<const float4*>(up_scales + (size_t)expert * 2 * I + I + i0 + 4 * kg);
     }
     __syncthreads();  // the lists are read: the ring may overwrite them
 
-    const int i0 = group * kGroup + 16 * cw;
     i32x4_t acc[2] = {};
-    if (i0 < I) {  // (I % 16 == 0: all of a wave's columns are there, or none)
-        const int KT = (H + 127) / 128, T = (KT - ks0 + KS - 1) / KS;
+    if (i0 < I) {
+        const int T = (H + 127) / 128;
         const int8_t* gate = uniform(up + ((size_t)expert * 2 * I + i0) * H);
         const int8_t* other = uniform(gate + (size_t)I * H);
 #pragma unroll
         for (int i = 0; i < 2; ++i) woff[i] = (uint32_t)(8 * i + lane / 8) * (uint32_t)H + 16u * copied_chunk(8 * i + lane / 8);
         char* ring = smem + wave * R * S::kStage;
         const uint32_t ring_lds = lds_addr(ring);
+        // k-tiles from a place of the wave's own on: blocks in step with one another would all ask the same part of the
+        // memory channels (rows of a power of two)
+        const int turn = (int)((blockIdx.x * 5 + wave * 3) % (unsigned)T);
+        auto k_tile = [&](int t) __attribute__((always_inline)) { return t + turn < T ? t + turn : t + turn - T; };
         auto issue = [&](int t, int slot) __attribute__((always_inline)) {
             const bool there = t < T;
-            const int kt = there ? t * KS + ks0 : 0;
+            const int kt = there ? k_tile(t) : 0;
             const uint32_t lds = ring_lds + (uint32_t)(slot * S::kStage);
             const int left = H - kt * 128;
 #pragma unroll
@@ -184,7 +227,7 @@ __global__ __launch_bounds__(256 * KS) void layer_up_kernel(const int8_t* __rest
             issue(t + R - 1, ahead);
             wait_vm<(R - 1) * C>();
             const char* w = ring + slot * S::kStage;
-            const int chunks = (H - (t * KS + ks0) * 128) / 16;
+            const int chunks = (H - k_tile(t) * 128) / 16;
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
                 i32x4_t x = fragment(w + 4096, l16 % XR, 4 * ks + kg);
@@ -198,47 +241,27 @@ __global__ __launch_bounds__(256 * KS) void layer_up_kernel(const int8_t* __rest
         }
         wait_vm<0>();
     }
-    __syncthreads();  // no copy is in flight
+    __syncthreads();  // no copy is in flight: the ring's memory is free
 
-    // the k-tiles' sums joined (exact integers), in the ring's memory
     float* tops = reinterpret_cast<float*>(smem);  // [4][16]
-    i32x4_t* sums = reinterpret_cast<i32x4_t*>(smem + 1024);
-    if constexpr (KS > 1) {
-        if (ks0 > 0) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) sums[(((ks0 - 1) * 4 + cw) * 2 + i) * 64 + lane] = acc[i];
-        }
-        __syncthreads();
-        if (ks0 == 0) {
-#pragma unroll
-            for (int o = 0; o < KS - 1; ++o)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) acc[i] += sums[((o * 4 + cw) * 2 + i) * 64 + lane];
-        }
-    }
     // lane (l16, kg): row l16, columns i0 + 4 kg ..
     float v[4] = {0, 0, 0, 0};
-    if (ks0 == 0) {
-        uint32_t m = 0;
-        if (i0 < I) {
-            const float a = ascale[pair / topk];
-            const float4 sg = *reinterpret_cast<const float4*>(up_scales + (size_t)expert * 2 * I + i0 + 4 * kg);
-            const float4 su = *reinterpret_cast<const float4*>(up_scales + (size_t)expert * 2 * I + I + i0 + 4 * kg);
-            const float g4[4] = {sg.x, sg.y, sg.z, sg.w}, u4[4] = {su.x, su.y, su.z, su.w};
+    uint32_t m = 0;
+    if (i0 < I) {
+        const float g4[4] = {sg.x, sg.y, sg.z, sg.w}, u4[4] = {su.x, su.y, su.z, su.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float g = (float)acc[0][i] * g4[i] * a, u = (float)acc[1][i] * u4[i] * a;
-                v[i] = g / (1.0f + expf(-g)) * u;
-                m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-            }
+        for (int i = 0; i < 4; ++i) {
+            const float g = (float)acc[0][i] * g4[i] * a, u = (float)acc[1][i] * u4[i] * a;
+            v[i] = g / (1.0f + expf(-g)) * u;
+            m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
         }
-        m = max(m, (uint32_t)__shfl_xor((int)m, 16));
-        m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-        if (kg == 0) tops[16 * cw + l16] = __uint_as_float(m);
     }
+    m = max(m, (uint32_t)__shfl_xor((int)m, 16));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+    if (kg == 0) tops[16 * wave + l16] = __uint_as_float(m);
     __syncthreads();
-    if (ks0 > 0 || l16 >= rows) return;
-    uint32_t m = __float_as_uint(tops[l16]);
+    if (l16 >= rows) return;
+    m = __float_as_uint(tops[l16]);
 #pragma unroll
     for (int i = 1; i < 4; ++i) m = max(m, __float_as_uint(tops[16 * i + l16]));
     const float b = scale_i8(__uint_as_float(m));
@@ -248,35 +271,46 @@ __global__ __launch_bounds__(256 * KS) void layer_up_kernel(const int8_t* __rest
         for (int i = 0; i < 4; ++i) q |= code_i8(v[i], b) << (8 * i);
     }
     if (i0 < I) *reinterpret_cast<uint32_t*>(hq + (size_t)pair * I + i0 + 4 * kg) = q;
-    if (cw == 0 && kg == 0) hscale[(size_t)pair * groups + group] = b;
+    if (wave == 0 && kg == 0) hscale[(size_t)pair * groups + group] = b;
 }
 
 // ---- down products and the weighted sum ----------------------------------------------------------------
 
-// A block: 16 columns of y for every token.  Its waves share the tiles of pairs, each cut into `parts` of K; a tile's
-// part is added by one wave, kept in LDS, and the parts and choices are added at the end, in order.
+// A block: kCols columns of y for every token.  Its waves share the tiles of pairs, each cut into parts of K; a
+// tile's part is added by one wave, kept in LDS, and the parts and choices are added at the end, in order.
+// kCols = 8 (XR = 8): a stage is two k-tiles, the first in the matrix instruction's rows and columns 0..7, the
+// second in 8..15; the sums of rows with columns of the other k-tile are not used.  Twice the blocks, where 16
+// columns a block would leave CUs idle.
 constexpr int kDownWaves = 8, kDownRows = 256;  // rows of sums that LDS has room for
-template <int XR>
+template <int XR, int kCols>
 struct DownShape {
-    static constexpr int kScales = 2048 + 128 * XR, kStage = kScales + 256, kCopies = 2 + XR / 8 + 1;
-    static constexpr int R = XR == 8 ? 5 : 4;
+    static constexpr int kTiles = 16 / kCols;                      // k-tiles of a stage
+    static constexpr int kX = 2048, kScales = kX + 128 * XR * kTiles, kStage = kScales + 256;
+    static constexpr int kCopies = 2 + XR / 8 * kTiles + 1;
+    static constexpr int R = 3;  // (four or five: no faster)
+    static_assert(kTiles == 1 || XR == 8, "rows of one k-tile in each half");
 };
 
-template <typename TO, typename TI, int XR, bool kOnce>
+template <typename TO, typename TI, int XR, int kCols, bool kOnce>
 __global__ __launch_bounds__(64 * kDownWaves) void layer_down_kernel(const int8_t* __restrict__ hq, const float* __restrict__ hscale,
                                                                      const TI* __restrict__ ids, int T, int topk,
                                                                      const float* __restrict__ weights, int E,
                                                                      const int8_t* __restrict__ down,
                                                                      const float* __restrict__ down_scales, int H, int I, int groups,
                                                                      TO* __restrict__ y) {
-    using S = DownShape<XR>;
-    constexpr int R = S::R, C = S::kCopies;
+    using S = DownShape<XR, kCols>;
+    constexpr int R = S::R, C = S::kCopies, KW = S::kTiles;
     __shared__ __attribute__((aligned(1024))) char smem[kDownWaves * R * S::kStage];
     __shared__ float4 sums[kDownRows][4];
-    __shared__ PairTiles s;
+    __shared__ PairTiles<XR> s;
+    __shared__ float pair_weight[kPairs];  // zero, and its sums not read, for a pair with no expert
+    __shared__ uint8_t pair_there[kPairs];
     const int lane = lane_id(), wave = wave_id(), l16 = lane & 15, kg = lane >> 4;
-    const int n0 = blockIdx.x * 16, P = T * topk, KT = (I + 127) / 128;
-    sort_pairs<XR>(ids, P, E, s);
+    const int n0 = blockIdx.x * kCols, P = T * topk, KT = (I + 128 * KW - 1) / (128 * KW);  // (of stages)
+    float pw = 0.0f;
+    if ((int)threadIdx.x < P) pw = weights[threadIdx.x];
+    const int e0 = sort_pairs<XR>(ids, P, E, s);
+    if ((int)threadIdx.x < P) pair_weight[threadIdx.x] = pw, pair_there[threadIdx.x] = e0 >= 0;
     const int tiles = __builtin_amdgcn_readfirstlane(s.tiles);
 
     // the parts of K (a power of two) that leave the busiest wave least to do
@@ -289,10 +323,13 @@ __global__ __launch_bounds__(64 * kDownWaves) void layer_down_kernel(const int8_
     }
     const int units = tiles << log;
 
+    // What a lane copies of a stage: weight rows (stage half kt2, column r) in 16 of 128 bytes, activation rows alike, and
+    // lanes 0.. of the last copy the groups' scales [k-tile][row][2], lanes 48.. the columns' own.
     struct Stream {
         int unit, kt, end;  // none left: unit >= units
-        const int8_t* w;    // of the k-tile
-        uint32_t xoff[XR / 8], soff;
+        const int8_t* w;    // of the unit
+        uint32_t xoff[XR / 8];
+        const float* scale;
     };
     auto begin = [&](Stream& it, int unit) __attribute__((always_inline)) {
         it.unit = unit;
@@ -301,88 +338,95 @@ __global__ __launch_bounds__(64 * kDownWaves) void layer_down_kernel(const int8_
         const int tile = unit >> log, part = unit & ((1 << log) - 1);
         it.kt = (KT * part) >> log;
         it.end = (KT * (part + 1)) >> log;
-        const int first = s.first[tile], rows = s.first[tile + 1] - first;
-        const int expert = __builtin_amdgcn_readfirstlane(s.ids[s.sorted[first]]);
+        const int rows = s.rows[tile], expert = __builtin_amdgcn_readfirstlane(s.expert[tile]);
         it.w = uniform(down + ((size_t)expert * H + n0) * I);
 #pragma unroll
-        for (int i = 0; i < XR / 8; ++i) {
-            const int r = 8 * i + lane / 8;
-            it.xoff[i] = (uint32_t)s.sorted[first + min(r, rows - 1)] * (uint32_t)I + 16u * copied_chunk(r);
-        }
-        it.soff = (uint32_t)s.sorted[first + min(lane / 2 % XR, rows - 1)] * (uint32_t)groups;
+        for (int i = 0; i < XR / 8; ++i) it.xoff[i] = (uint32_t)s.row[tile][min(8 * i + lane / 8, rows - 1)] * (uint32_t)I;
+        it.scale = lane < 48 ? hscale + (uint32_t)s.row[tile][min(lane / 2 % XR, rows - 1)] * (uint32_t)groups
+                             : down_scales + (size_t)expert * H + n0 + (lane - 48) % kCols;
     };
-    uint32_t woff[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) woff[i] = (uint32_t)(8 * i + lane / 8) * (uint32_t)I + 16u * copied_chunk(8 * i + lane / 8);
     char* ring = smem + wave * R * S::kStage;
     const uint32_t ring_lds = lds_addr(ring);
     auto issue = [&](Stream& it, int slot) __attribute__((always_inline)) {
         const bool there = it.unit < units;
         const uint32_t lds = ring_lds + (uint32_t)(slot * S::kStage);
-        const int left = I - it.kt * 128;
-        const int8_t* w = there ? it.w + it.kt * 128 : down;
-        const int8_t* x = there ? hq + it.kt * 128 : hq;
+        // LDS row 8 j + lane / 8 of 16, in k-tile j of the stage (KW = 2), its chunk c at 16 c of the k-tile; chunks past I
+        // read the row's last one
+        auto at = [&](int j) __attribute__((always_inline)) {
+            const int k = (it.kt * KW + (KW == 2 ? j : 0)) * 128 + 16 * copied_chunk(8 * j + lane / 8);
+            return (uint32_t)min(k, I - 16);
+        };
+        const int8_t* w = there ? it.w : down;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            copy_weights<kOnce>(there ? woff[i] - past_end(copied_chunk(8 * i + lane / 8), left) : 0, w, lds + 1024 * i);
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t row = KW == 2 ? lane / 8 : 8 * j + lane / 8;
+            copy_weights<kOnce>(there ? row * (uint32_t)I + at(j) : 0, w, lds + 1024 * j);
+        }
 #pragma unroll
-        for (int i = 0; i < XR / 8; ++i)
-            dma16(there ? it.xoff[i] - past_end(copied_chunk(8 * i + lane / 8), left) : 0, x, lds + 2048 + 1024 * i);
-        dma4(there ? 4 * (it.soff + (uint32_t)min(2 * it.kt + (lane & 1), groups - 1)) : 0, hscale, lds + S::kScales);
-        if (there && ++it.kt == it.end) begin(it, it.unit + kDownWaves);
+        for (int j = 0; j < XR / 8 * KW; ++j) dma16(there ? it.xoff[KW == 2 ? 0 : j] + at(j) : 0, hq, lds + S::kX + 1024 * j);
+        const int group = min(2 * (it.kt * KW + (KW == 2 ? lane / 16 : 0)) + (lane & 1), groups - 1);
+        const bool last = there && ++it.kt == it.end;
+        // (the columns' scales with a unit's last stage only: asked for with each, they cost 40% more time)
+        dma4_at(!there || (lane >= 48 && !last) ? hscale : it.scale + (lane < 48 ? group : 0), lds + S::kScales);
+        if (last) begin(it, it.unit + kDownWaves);
     };
 
-    Stream ahead, now;
+    Stream ahead;
     begin(ahead, wave);
-    begin(now, wave);
+    int unit = ahead.unit, kt = ahead.kt, end = ahead.end;
 #pragma unroll
     for (int t = 0; t < R - 1; ++t) issue(ahead, t);
     int slot = 0, next = R - 1;
     float acc[4] = {0, 0, 0, 0};
-    while (now.unit < units) {
+    const int half = KW == 2 ? l16 / 8 : 0;  // the k-tile of this lane's row
+    while (unit < units) {
         issue(ahead, next);
         wait_vm<(R - 1) * C>();
         const char* w = ring + slot * S::kStage;
-        const int chunks = (I - now.kt * 128) / 16;
-        const float2 b = *reinterpret_cast<const float2*>(w + S::kScales + 8 * (l16 % XR));
+        const int chunks = (I - (kt * KW + half) * 128) / 16;
+        const float2 b = *reinterpret_cast<const float2*>(w + S::kScales + 64 * (KW == 2 ? half : 0) + 8 * (l16 % XR));
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-            i32x4_t x = fragment(w + 2048, l16 % XR, 4 * ks + kg);
+            i32x4_t x = fragment(w + S::kX, KW == 2 ? l16 : l16 % XR, 4 * ks + kg);
             if (4 * ks + kg >= chunks) x = i32x4_t{0, 0, 0, 0};
             const i32x4_t sum = __builtin_amdgcn_mfma_i32_16x16x64_i8(fragment(w, l16, 4 * ks + kg), x, i32x4_t{0, 0, 0, 0}, 0, 0, 0);
             // (a group past the last has no chunks: its scale, the last one's, meets a sum of zero)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf((float)sum[i], ks == 0 ? b.x : b.y, acc[i]);
         }
+        if (++kt == end) {  // the unit's sums, times the columns' scales
+            const int tile = unit >> log, part = unit & ((1 << log) - 1), rows = s.rows[tile];
+            const float4 sn = *reinterpret_cast<const float4*>(w + S::kScales + 192 + 16 * (KW == 2 ? kg % 2 : kg));
+            float4 o = make_float4(acc[0] * sn.x, acc[1] * sn.y, acc[2] * sn.z, acc[3] * sn.w);
+            if constexpr (KW == 2) {  // columns 4 (kg % 2).. of row l16 % 8: in lanes (l16, kg) and (l16 + 8, kg + 2)
+                const int other = (lane + 40) & 63;
+                o.x += __shfl(o.x, other), o.y += __shfl(o.y, other), o.z += __shfl(o.z, other), o.w += __shfl(o.w, other);
+                if (l16 < min(rows, 8) && kg < 2) sums[part * P + s.row[tile][l16]][kg] = o;
+            } else {
+                if (l16 < rows) sums[part * P + s.row[tile][l16]][kg] = o;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i] = 0.0f;
+            unit += kDownWaves;
+            const int p = unit & ((1 << log) - 1);
+            kt = (KT * p) >> log;
+            end = (KT * (p + 1)) >> log;
+        }
         reads_done();
         slot = slot + 1 == R ? 0 : slot + 1;
         next = next + 1 == R ? 0 : next + 1;
-        if (++now.kt == now.end) {
-            const int tile = now.unit >> log, part = now.unit & ((1 << log) - 1);
-            const int first = s.first[tile], rows = s.first[tile + 1] - first;
-            if (l16 < rows) sums[part * P + s.sorted[first + l16]][kg] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] = 0.0f;
-            now.unit += kDownWaves;
-            if (now.unit < units) {
-                const int p = now.unit & ((1 << log) - 1);
-                now.kt = (KT * p) >> log;
-                now.end = (KT * (p + 1)) >> log;
-            }
-        }
     }
     wait_vm<0>();
     __syncthreads();
-    const int t = threadIdx.x / 16, c = threadIdx.x % 16;
+    const int t = threadIdx.x / kCols, c = threadIdx.x % kCols;
     if (t >= T) return;
     const float* part_sums = reinterpret_cast<const float*>(sums);
     float out = 0.0f;
-    for (int j = 0; j < topk; ++j) {
-        const int p = t * topk + j, e = s.ids[p];
-        if (e == INT32_MAX) continue;
+    for (int p = t * topk; p < (t + 1) * topk; ++p) {
+        if (!pair_there[p]) continue;
         float o = part_sums[p * 16 + c];
         for (int i = 1; i < 1 << log; ++i) o += part_sums[(i * P + p) * 16 + c];
-        out = __builtin_fmaf(weights[p], o * down_scales[(size_t)e * H + n0 + c], out);
+        out = __builtin_fmaf(pair_weight[p], o, out);
     }
     y[(size_t)t * H + n0 + c] = from_f32<TO>(out);
 }
@@ -398,32 +442,31 @@ hipError_t launch_expert_layer_w8a8(int dtype, const int8_t* xq, const float* as
                                     const int8_t* down, const float* down_scales, int64_t H, int64_t I, void* y, int8_t* hq,
                                     float* hscale, hipStream_t stream) {
     const int64_t P = T * topk, groups = (I + kGroup - 1) / kGroup;
-    auto run = [&](auto id, auto xr, auto ks, auto once) {
+    auto run = [&](auto id, auto xr, auto cols, auto once) {
         using TI = decltype(id);
-        constexpr int XR = decltype(xr)::value, KS = decltype(ks)::value;
+        constexpr int XR = decltype(xr)::value, kCols = decltype(cols)::value;
         constexpr bool kOnce = decltype(once)::value;
         const TI* idt = static_cast<const TI*>(ids);
-        hipLaunchKernelGGL((layer_up_kernel<TI, XR, KS, kOnce>), dim3((unsigned)(expert_tiles(P, E, XR) * groups)), dim3(256 * KS), 0,
+        hipLaunchKernelGGL((layer_up_kernel<TI, XR, kOnce>), dim3((unsigned)(expert_tiles(P, E, XR) * groups)), dim3(256), 0,
                            stream, xq, ascale, idt, (int)P, (int)topk, (int)E, up, up_scales, (int)H, (int)I, (int)groups, hq, hscale);
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
         return with_act_type(dtype, [&](auto t) {
             using TO = decltype(t);
-            hipLaunchKernelGGL((layer_down_kernel<TO, TI, XR, kOnce>), dim3((unsigned)(H / 16)), dim3(64 * kDownWaves), 0, stream, hq,
-                               hscale, idt, (int)T, (int)topk, weights, (int)E, down, down_scales, (int)H, (int)I, (int)groups,
-                               static_cast<TO*>(y));
+            hipLaunchKernelGGL((layer_down_kernel<TO, TI, XR, kCols, kOnce>), dim3((unsigned)(H / kCols)), dim3(64 * kDownWaves), 0,
+                               stream, hq, hscale, idt, (int)T, (int)topk, weights, (int)E, down, down_scales, (int)H, (int)I,
+                               (int)groups, static_cast<TO*>(y));
             return hipGetLastError();
         });
     };
+    using I8 = std::integral_constant<int, 8>;
+    using I16 = std::integral_constant<int, 16>;
     const double weight_bytes = 3.0 * (double)std::min(P, E) * (double)H * (double)I;
-    auto with_once = [&](auto id, auto xr, auto ks) {
-        return weight_bytes >= kOnceBytes ? run(id, xr, ks, std::true_type{}) : run(id, xr, ks, std::false_type{});
-    };
-    auto with_ks = [&](auto id, auto xr) {
-        const bool few = std::min(P, E) * groups < 512;
-        return few ? with_once(id, xr, std::integral_constant<int, 2>{}) : with_once(id, xr, std::integral_constant<int, 1>{});
+    auto with_once = [&](auto id, auto xr, auto cols) {
+        return weight_bytes >= kOnceBytes ? run(id, xr, cols, std::true_type{}) : run(id, xr, cols, std::false_type{});
     };
     auto with_rows = [&](auto id) {
-        return T <= 8 || P <= 4 * E ? with_ks(id, std::integral_constant<int, 8>{}) : with_ks(id, std::integral_constant<int, 16>{});
+        if (T > 8 && P > 4 * E) return with_once(id, I16{}, I16{});
+        return H < 16 * 256 ? with_once(id, I8{}, I8{}) : with_once(id, I8{}, I16{});
     };
     return id_bits == 32 ? with_rows(int32_t{}) : with_rows(int64_t{});
 }

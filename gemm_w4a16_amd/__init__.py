@@ -385,7 +385,7 @@ def w4a16_expert_layer_workspace_bytes(T: int, topk: int, I: int) -> int:
 
 
 def _mx4_scale_bytes(rows: int, K: int) -> int:
-    return (K + 255) // 256 * ((rows + 15) // 16 * 16) * 8
+    return (K + 255) // 256 * ((rows + 31) // 32) * 256
 
 
 def w4a16_quantize_rows_mx4(act: int, x, M: int, K: int, xq, xscales, stream=None) -> None:
@@ -454,7 +454,7 @@ def alloc_packed(fmt: int, N: int, K: int, device="cuda"):
                 None)
     if fmt == W4A16_FMT_MX4_B32_E8M0:  # (rows' codes and scales as well, with M for N)
         return (torch.empty((N, K // 2), dtype=torch.uint8, device=device),
-                torch.empty(((K + 255) // 256, (N + 15) // 16 * 16, 8), dtype=torch.uint8, device=device),
+                torch.empty(((K + 255) // 256, (N + 31) // 32, 4, 16, 2, 2), dtype=torch.uint8, device=device),
                 None)
     if fmt == W4A16_FMT_G128_ZP_FP16:
         return (torch.empty((N, K // 8), dtype=torch.int32, device=device),

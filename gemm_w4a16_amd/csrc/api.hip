@@ -155,7 +155,7 @@ w4a16_status_t check_w4a4(w4a16_format_t fmt, w4a16_dtype_t out, int64_t M, cons
     if (w4a16_status_t st = check_shape(fmt, N, K); st != W4A16_OK) return st;
     if (M <= 0 || M > kMaxDim || !valid_dtype(out) || !aligned16(y)) return W4A16_ERR_INVALID;
     if (w4a16_status_t st = check_packed(fmt, codes, scales, mins); st != W4A16_OK) return st;
-    return fmt == W4A16_FMT_MX4_B32_E8M0 ? W4A16_OK : W4A16_ERR_UNSUPPORTED;
+    return fmt == W4A16_FMT_MX4_B32_E8M0 && w4a16::w4a4_fits_grid(M, N) ? W4A16_OK : W4A16_ERR_UNSUPPORTED;
 }
 
 // The W4A4 workspace: the codes of x, then their scales (both 16-byte aligned).
@@ -760,7 +760,8 @@ w4a16_status_t w4a16_gemm_w4a4(w4a16_format_t fmt, w4a16_dtype_t out, const uint
 }
 
 size_t w4a16_w4a4_workspace_bytes(w4a16_format_t fmt, int64_t M, int64_t N, int64_t K) {
-    if (fmt != W4A16_FMT_MX4_B32_E8M0 || check_shape(fmt, N, K) != W4A16_OK || M <= 0 || M > kMaxDim) return 0;
+    if (fmt != W4A16_FMT_MX4_B32_E8M0 || check_shape(fmt, N, K) != W4A16_OK || M <= 0 || M > kMaxDim || !w4a16::w4a4_fits_grid(M, N))
+        return 0;
     return W4A4Workspace(M, K).needed;
 }
 

@@ -198,6 +198,7 @@ hipError_t launch_add_rmsnorm_backward(int dtype, const void* dy, const void* dh
 hipError_t launch_quant_mx4(int dtype, const void* x, int64_t M, int64_t K, uint8_t* codes, uint8_t* scales, hipStream_t stream);
 hipError_t launch_dequant_mx4(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K, int dtype, void* out,
                               hipStream_t stream);
+bool w4a4_fits_grid(int64_t M, int64_t N);
 hipError_t launch_gemm_w4a4(int dtype, const uint8_t* xq, const uint8_t* xscales, int64_t M, const uint8_t* codes,
                             const uint8_t* scales, int64_t N, int64_t K, void* y, hipStream_t stream);
 

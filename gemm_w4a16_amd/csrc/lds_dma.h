@@ -41,6 +41,10 @@ __device__ __forceinline__ void dma4(uint32_t voff, const void* sbase, uint32_t 
                      "n"(kImm)
                      : "memory", "m0", "scc");
 }
+// Lane l's 16 bytes at an address of its own to LDS byte lds + 16 l.
+__device__ __forceinline__ void dma16_at(const void* p, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(lds) : "memory", "m0");
+}
 // Lane l's dword at an address of its own to LDS byte lds + 4 l.
 __device__ __forceinline__ void dma4_at(const void* p, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(p), "s"(lds) : "memory", "m0");

@@ -2,9 +2,11 @@
 //
 // A block is 32 consecutive values of a row: a power of two 2^(s - 127), s one byte (255: the block is not a number),
 // and 32 elements of four bits (e2m1: a sign and the magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6).  codes [rows][K/2], byte j
-// of a row holding value 2j in its low half; scales [K/256 rounded up][rows rounded up to 16][8], byte b of row r in
-// k-tile t belonging to block 8 t + b.  So the scales of a tile's rows are one run of memory for each 256 of K, in
-// whole 128-byte lines, and 8 bytes of a row are what a matrix-core step pair of 256 takes.
+// of a row holding value 2j in its low half.  scales [K/256 rounded up][rows / 32 rounded up][64][4]: for each 256 of K
+// (a k-tile) and 32 rows, a word for each lane of a wave, in the order the matrix instructions take them.  Lane
+// l of a 16 x 128 operand holds row l % 16 and block l / 16 of the instruction's four; its word has the bytes of rows
+// l % 16 (bytes 0, 1) and 16 + l % 16 (bytes 2, 3), of the k-tile's first (0, 2) and second (1, 3) 128.  So a lane
+// reads one word for four operands, no byte is moved, and the scales of a tile's rows are one run of memory.
 #pragma once
 
 #include "device_common.h"
@@ -13,9 +15,13 @@ namespace w4a16 {
 
 constexpr int kMx4Block = 32;   // values that share a scale
 constexpr int kMx4TileK = 256;  // values of a row in a k-tile: 128 bytes of codes, 8 scales
-__host__ __device__ constexpr int64_t mx4_rows(int64_t rows) { return (rows + 15) / 16 * 16; }  // that scales has room for
+__host__ __device__ constexpr int64_t mx4_groups(int64_t rows) { return (rows + 31) / 32; }  // of 32 rows: 256 bytes a k-tile
 __host__ __device__ constexpr int64_t mx4_ktiles(int64_t K) { return (K + kMx4TileK - 1) / kMx4TileK; }
-constexpr size_t mx4_scale_bytes(int64_t rows, int64_t K) { return (size_t)mx4_ktiles(K) * (size_t)mx4_rows(rows) * 8; }
+constexpr size_t mx4_scale_bytes(int64_t rows, int64_t K) { return (size_t)mx4_ktiles(K) * (size_t)mx4_groups(rows) * 256; }
+// Where the scale of row r's block b lies; groups: mx4_groups of the array's rows.
+__device__ __forceinline__ int64_t mx4_scale_at(int64_t groups, int64_t r, int b) {
+    return ((b / 8) * groups + r / 32) * 256 + (b % 4 * 16 + r % 16) * 4 + r / 16 % 2 * 2 + b / 4 % 2;
+}
 
 // The scale's byte for a block whose largest magnitude has these fp32 bits: floor(log2 max) less 2, the largest
 // element's exponent, not below -127; 255 for a block with an infinity or NaN.

@@ -19,7 +19,7 @@ template <typename T>
 __global__ __launch_bounds__(256) void quant_mx4_kernel(const T* __restrict__ x, int64_t M, int K, uint8_t* __restrict__ codes,
                                                         uint8_t* __restrict__ scales) {
     const int K8 = K / 8;
-    const int64_t units = M * K8, Mp = mx4_rows(M);
+    const int64_t units = M * K8, groups = mx4_groups(M);
     for (int64_t u0 = (int64_t)blockIdx.x * 256; u0 < units; u0 += (int64_t)gridDim.x * 256) {
         const int64_t m0 = u0 / K8;
         const uint32_t in = (uint32_t)(u0 - m0 * K8) + threadIdx.x;  // units from row m0's first
@@ -54,10 +54,9 @@ __global__ __launch_bounds__(256) void quant_mx4_kernel(const T* __restrict__ x,
         *reinterpret_cast<uint32_t*>(codes + m * (K / 2) + 4 * c) = w;
         if (c % 4 == 0) {
             const int b = c / 4;
-            uint8_t* at = scales + ((b / 8) * Mp + m) * 8;
-            at[b % 8] = (uint8_t)s;
+            scales[mx4_scale_at(groups, m, b)] = (uint8_t)s;
             if (b + 1 == K / 32) {  // the last k-tile's blocks past K
-                for (int i = b % 8 + 1; i < 8; ++i) at[i] = 0;
+                for (int i = b + 1; i % 8 != 0; ++i) scales[mx4_scale_at(groups, m, i)] = 0;
             }
         }
     }
@@ -68,7 +67,7 @@ template <typename T>
 __global__ __launch_bounds__(256) void dequant_mx4_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                                                           int64_t M, int K, T* __restrict__ out) {
     const int K8 = K / 8;
-    const int64_t units = M * K8, Mp = mx4_rows(M);
+    const int64_t units = M * K8, groups = mx4_groups(M);
     for (int64_t u0 = (int64_t)blockIdx.x * 256; u0 < units; u0 += (int64_t)gridDim.x * 256) {
         const int64_t m0 = u0 / K8;
         const uint32_t in = (uint32_t)(u0 - m0 * K8) + threadIdx.x;
@@ -76,7 +75,7 @@ __global__ __launch_bounds__(256) void dequant_mx4_kernel(const uint8_t* __restr
         const int c = (int)(in % (uint32_t)K8);
         if (m >= M) continue;
         const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + m * (K / 2) + 4 * c);
-        const float f = mx4_factor(scales[((c / 32) * Mp + m) * 8 + c / 4 % 8]);
+        const float f = mx4_factor(scales[mx4_scale_at(groups, m, c / 4)]);
         float v[8];
         auto two = [&](int j, f32x2_t p) __attribute__((always_inline)) { v[2 * j] = p.x * f, v[2 * j + 1] = p.y * f; };
         two(0, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0));

@@ -2,73 +2,378 @@
 // instructions.
 //
 //     y[m][n] = sum_b 2^(sx[m][b] + sw[n][b] - 254) sum_{k in block b} p[m][k] q[n][k]
-// with the products of elements exact and the sums in fp32, rounded once to the output type.
+// with the products of elements exact and the sums in fp32, rounded once to the output type.  An instruction
+// multiplies 16 rows by 16 columns over 128 of K, each lane's 32 elements with the scale of their block; the order of
+// additions follows from the sizes alone, so results are bitwise reproducible.
 #include <algorithm>
+#include <cmath>
+#include <cstddef>
+#include <type_traits>
+#include <utility>
 
 #include "experts.h"
 #include "launch.h"
+#include "lds_dma.h"
 #include "mx4.h"
 
 namespace w4a16 {
 
 namespace {
 
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4v_t __attribute__((ext_vector_type(4)));
 
-// A wave computes 16 rows x 64 columns from operands in global memory.
-template <typename TO>
-__global__ __launch_bounds__(256) void w4a4_simple_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restrict__ xscales, int M,
-                                                          const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-                                                          int N, int K, TO* __restrict__ y) {
-    const int lane = lane_id(), l16 = lane & 15, kg = lane >> 4;
-    const int64_t n_tiles = (N + 63) / 64, tiles = n_tiles * ((M + 15) / 16);
-    const int64_t Mp = mx4_rows(M), Np = mx4_rows(N);
-    for (int64_t t = (int64_t)blockIdx.x * 4 + wave_id(); t < tiles; t += (int64_t)gridDim.x * 4) {
-        const int m0 = (int)(t / n_tiles) * 16, n0 = (int)(t % n_tiles) * 64;
-        const int m = min(m0 + l16, M - 1);
-        f32x4v_t acc[4] = {};
-        for (int k0 = 0; k0 < K; k0 += 128) {
-            const int b = k0 / 32 + kg;
-            const bool there = b < K / 32;
-            auto frag = [&](const uint8_t* rows, int64_t r) __attribute__((always_inline)) {
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (there) v = *reinterpret_cast<const uint4*>(rows + r * (K / 2) + b * 16);
-                return i32x8_t{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
-            };
-            auto scale = [&](const uint8_t* s, int64_t rows, int64_t r) __attribute__((always_inline)) {
-                return there ? (int)s[((int64_t)(b / 8) * rows + r) * 8 + b % 8] : 127;
-            };
-            const i32x8_t xf = frag(xq, m);
-            const int xs = scale(xscales, Mp, m);
-#pragma unroll
-            for (int a = 0; a < 4; ++a) {
-                const int n = min(n0 + 16 * a + l16, N - 1);
-                acc[a] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(codes, n), xf, acc[a], 4, 4, 0, scale(scales, Np, n), 0,
-                                                                         xs);
-            }
-        }
-        if (m0 + l16 >= M) continue;
-#pragma unroll
-        for (int a = 0; a < 4; ++a)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int n = n0 + 16 * a + 4 * kg + e;
-                if (n < N) y[(int64_t)(m0 + l16) * N + n] = from_f32<TO>(acc[a][e]);
-            }
+template <int... I, typename F>
+__device__ __forceinline__ void each(std::integer_sequence<int, I...>, F f) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+
+// acc += the product of 16 weight rows and 16 activation rows over 128 of K; byte kWSel of a lane's word of scales is
+// that of its weight block, kXSel alike.
+template <int kWSel, int kXSel>
+__device__ __forceinline__ f32x4v_t mfma(i32x4_t w, i32x4_t x, f32x4v_t acc, int wscale, int xscale) {
+    const i32x8_t a = __builtin_shufflevector(w, w, 0, 1, 2, 3, -1, -1, -1, -1);
+    const i32x8_t b = __builtin_shufflevector(x, x, 0, 1, 2, 3, -1, -1, -1, -1);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, 4, kWSel, wscale, kXSel, xscale);  // (4: e2m1)
+}
+constexpr int kOnes = 0x7F7F7F7F;  // scales of one, for blocks past K (their elements are zero)
+
+// ---- tiles --------------------------------------------------------------------------------------
+
+// A block computes BM rows x BN columns in WM x WN waves of (16 TM) x (16 TN), each doubled WK times along K.  K is
+// taken in stages of WK k-tiles of 256 (128 bytes of codes a row); the waves of index wk along K multiply k-tile wk of a
+// stage, and their sums are added at the end, in order.  Operands and scales reach LDS by direct copies into a ring
+// of R stages.
+template <int WM_, int WN_, int WK_, int TM_, int TN_, int R_>
+struct Tiling {
+    static constexpr int WM = WM_, WN = WN_, WK = WK_, TM = TM_, TN = TN_, R = R_;
+    static constexpr int BM = 16 * TM * WM, BN = 16 * TN * WN, NW = WM * WN * WK;
+    static constexpr int kTileBytes = (BM + BN) * 128;  // one k-tile: BN rows of weights, then BM rows of x
+    static constexpr int GW = (BN + 31) / 32, GX = (BM + 31) / 32;  // groups of scales: weights', then x's
+    static constexpr int kScaleBytes = (GW + GX) * 256;
+    static constexpr int kCodes = WK * kTileBytes;  // of a stage; the scales of its k-tiles lie behind them
+    static constexpr int kScaleCopies = (WK * kScaleBytes + 1023) / 1024;
+    static constexpr int kStage = kCodes + 1024 * kScaleCopies;
+    static constexpr int CW = (kCodes / 1024 + NW - 1) / NW;      // copies of 1 KB by a wave (the last ones may be made twice)
+    static constexpr int SW = (kScaleCopies + NW - 1) / NW;
+};
+
+template <typename TO, typename C>
+__global__ __launch_bounds__(64 * C::NW) void w4a4_tile_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restrict__ xscales,
+                                                               int M, const uint8_t* __restrict__ codes,
+                                                               const uint8_t* __restrict__ scales, int N, int stride,
+                                                               TO* __restrict__ y, int n_tiles, int group) {
+    constexpr int TM = C::TM, TN = C::TN, R = C::R, BM = C::BM, BN = C::BN, CW = C::CW, SW = C::SW, G = CW + SW;
+    constexpr int kTileCopies = C::kTileBytes / 1024;  // of one k-tile
+    __shared__ __attribute__((aligned(1024))) char smem[R * C::kStage];
+    const int lane = lane_id(), wave = wave_id();
+    const int l16 = lane & 15, kg = lane >> 4;
+    const int wn = wave % C::WN, wk = wave / C::WN % C::WK, wm = wave / (C::WN * C::WK);
+
+    // This block's tile.  Blocks go to the XCDs in turn: each XCD takes a contiguous eighth of the tile
+    // sequence, which walks `group` row tiles at a time, rows first, so that the blocks of one XCD share
+    // operands in its L2.
+    int row0, tn;
+    {
+        const int m_tiles = (M + BM - 1) / BM, total = m_tiles * n_tiles, b = blockIdx.x;
+        const int xcd = b & 7, each = total >> 3, rest = total & 7;
+        const int s = xcd * each + min(xcd, rest) + (b >> 3);
+        const int g = s / (group * n_tiles), in = s - g * group * n_tiles;
+        const int rows = min(group, m_tiles - g * group);
+        tn = in / rows;
+        row0 = (g * group + in - tn * rows) * BM;
     }
+    const int n0 = tn * BN;
+    const int S = stride;  // bytes of a row of codes
+    const int KT = (S + 127) / 128, T = (KT + C::WK - 1) / C::WK;
+    const uint8_t* wbase = codes + (size_t)n0 * S;
+    const uint8_t* xbase = xq + (size_t)row0 * S;
+    const uint32_t lds0 = lds_addr(smem);
+
+    // This wave's copies j = CW wave + i of a stage's codes: copy jj = j % kTileCopies of k-tile j / kTileCopies, rows
+    // 8 jj + lane / 8 of [weights; x].  LDS slot lane % 8 of a row takes its 16-byte chunk
+    // slot ^ ((row >> 1) & 7), so that the fragment reads below meet no bank twice.  Rows past the end
+    // read the last row; they are never stored.
+    uint32_t voff[CW];
+#pragma unroll
+    for (int i = 0; i < CW; ++i) {
+        const int jj = min(CW * wave + i, C::kCodes / 1024 - 1) % kTileCopies;
+        const int r = 8 * jj + lane / 8, chunk = (lane % 8) ^ ((r >> 1) & 7);
+        const int row = jj < BN / 8 ? min(r, N - 1 - n0) : min(r - BN, M - 1 - row0);
+        voff[i] = (uint32_t)row * (uint32_t)S + 16u * chunk;
+    }
+    // ... and its 16 bytes of the stage's scales: groups past the last read the last one
+    const char* sptr[SW];
+    int64_t sstep[SW];
+    int stile[SW];
+#pragma unroll
+    for (int i = 0; i < SW; ++i) {
+        const int c = min(64 * min(SW * wave + i, C::kScaleCopies - 1) + lane, C::WK * C::kScaleBytes / 16 - 1);
+        const int g = c / 16 % (C::GW + C::GX);
+        const int64_t gw = mx4_groups(N), gx = mx4_groups(M);
+        stile[i] = c / 16 / (C::GW + C::GX);
+        const bool w = g < C::GW;
+        const int64_t at = w ? min((int64_t)(n0 / 32 + g), gw - 1) : min((int64_t)(row0 / 32 + g - C::GW), gx - 1);
+        sptr[i] = reinterpret_cast<const char*>(w ? scales : xscales) + at * 256 + c % 16 * 16;
+        sstep[i] = (w ? gw : gx) * 256;
+    }
+    // copy i of stage t into ring slot `slot`; the last k-tile's chunks past K, and k-tiles past the last, read what is there
+    // (their products are masked).  Stages past the last read one line over and over: each stage is then the same
+    // number of copies, and every wait below is a constant.
+    auto copy = [&](int t, int slot, int i) __attribute__((always_inline)) {
+        if (i < CW) {
+            const int j = min(CW * wave + i, C::kCodes / 1024 - 1), jj = j % kTileCopies;
+            const int kt = min(t * C::WK + j / kTileCopies, KT - 1);
+            const uint8_t* base = (jj < BN / 8 ? wbase : xbase) + (size_t)kt * 128;
+            uint32_t off = voff[i];
+            const int left = S - kt * 128;
+            if (left < 128) {
+                const int r = 8 * jj + lane / 8, chunk = (lane % 8) ^ ((r >> 1) & 7);
+                off -= (uint32_t)max(16 * chunk - (left - 16), 0);
+            }
+            if (t >= T) base = wbase, off = 0;
+            dma16(off, base, lds0 + (uint32_t)(slot * C::kStage + 1024 * j));
+        } else {
+            const int s = i - CW, j = min(SW * wave + s, C::kScaleCopies - 1);
+            const int kt = min(t * C::WK + stile[s], KT - 1);
+            dma16_at(sptr[s] + (t >= T ? 0 : kt * sstep[s]), lds0 + (uint32_t)(slot * C::kStage + C::kCodes + 1024 * j));
+        }
+    };
+
+    // fragment of row tile rt at k-step ks of a k-tile: chunk 4 ks + kg of row 16 rt + l16
+    const char* frag0 = smem + wk * C::kTileBytes + 128 * l16;
+    const int sw = (l16 >> 1) & 7;
+    auto next_slot = [](int s) __attribute__((always_inline)) { return s + 1 >= R ? s + 1 - R : s + 1; };
+    auto read = [&](int slot, int ks, int rt) __attribute__((always_inline)) {
+        return *reinterpret_cast<const i32x4_t*>(frag0 + slot * C::kStage + 2048 * rt + 16 * ((4 * ks + kg) ^ sw));
+    };
+    const int w_rt = TN * wn, x_rt = BN / 16 + TM * wm;
+    // words of scales: of two row tiles each (TN, TM even), or the half of one that is this row tile's
+    constexpr int NS = (TN + 1) / 2, MS = (TM + 1) / 2;
+    const char* scale0 = smem + C::kCodes + wk * C::kScaleBytes + 4 * lane;
+    auto read_scale = [&](int slot, int i) __attribute__((always_inline)) {
+        const int g = i < NS ? TN * wn / 2 + i : C::GW + TM * wm / 2 + i - NS;
+        return *reinterpret_cast<const int*>(scale0 + slot * C::kStage + 256 * g);
+    };
+    const int w_shift = TN == 1 ? 16 * ((n0 / 16 + wn) & 1) : 0, x_shift = TM == 1 ? 16 * ((row0 / 16 + wm) & 1) : 0;
+
+    f32x4v_t acc[TN][TM];
+#pragma unroll
+    for (int a = 0; a < TN; ++a)
+#pragma unroll
+        for (int b = 0; b < TM; ++b) acc[a][b] = f32x4v_t{0, 0, 0, 0};
+    i32x4_t wf[2][TN], xf[2][TM];
+    int sc[NS + MS], sc_next[NS + MS];  // of this stage's k-tile (both k-steps), and of the next's
+
+    // the products of k-step ks, with `reads` reads spread over the first three quarters of them and `copies` copies
+    // over all
+    auto multiply = [&](auto step, auto reads, auto read, auto copies, auto copy) __attribute__((always_inline)) {
+        constexpr int ks = decltype(step)::value, H = TM * TN, HR = (3 * H + 3) / 4;
+        constexpr int nr = decltype(reads)::value, nc = decltype(copies)::value;
+        each(std::make_integer_sequence<int, H>{}, [&](auto index) __attribute__((always_inline)) {
+            constexpr int i = decltype(index)::value, a = i / TM, b = i % TM;
+#pragma unroll
+            for (int u = (i * nr + HR - 1) / HR; u < min(nr, ((i + 1) * nr + HR - 1) / HR); ++u) read(u);
+#pragma unroll
+            for (int u = (i * nc + H - 1) / H; u < ((i + 1) * nc + H - 1) / H; ++u) copy(u);
+            acc[a][b] = mfma<(TN == 1 ? 0 : a % 2 * 2) + ks, (TM == 1 ? 0 : b % 2 * 2) + ks>(wf[ks][a], xf[ks][b], acc[a][b], sc[a / 2],
+                                                                                             sc[NS + b / 2]);
+            if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+            if (i == 0) __builtin_amdgcn_s_setprio(1);
+            if (i == H - 1) __builtin_amdgcn_s_setprio(0);
+        });
+    };
+    // read u of a stage in ring slot `slot`: fragments, and with the first k-step's the scales
+    auto read_step = [&](int slot, int ks, int u) __attribute__((always_inline)) {
+        if (u < TM) {
+            xf[ks][u] = read(slot, ks, x_rt + u);
+        } else if (u < TM + TN) {
+            wf[ks][u - TM] = read(slot, ks, w_rt + u - TM);
+        } else {
+            const int i = u - TM - TN;
+            sc_next[i] = read_scale(slot, i) >> (i < NS ? w_shift : x_shift);
+        }
+    };
+    auto take_scales = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < NS + MS; ++i) sc[i] = sc_next[i];
+    };
+    constexpr int kReads = TM + TN, kFirst = kReads + NS + MS;
+    // Behind stage t's barrier its slot takes stage t + R, G copies: kEarly of them under the stage's second k-step,
+    // the others under the next stage's first (where the ring holds more than two stages; else the next barrier
+    // would wait for copies just made).
+    constexpr int kEarly = R > 2 ? G / 2 : G, kLate = G - kEarly;
+    using NReads = std::integral_constant<int, kReads>;
+    using NFirst = std::integral_constant<int, kFirst>;
+    using NEarly = std::integral_constant<int, kEarly>;
+    using NLate = std::integral_constant<int, kLate>;
+    using Zero = std::integral_constant<int, 0>;
+    using One = std::integral_constant<int, 1>;
+    auto none = [](int) {};
+
+    static_assert(R * G < 64, "the wait counts");
+#pragma unroll
+    for (int u = 0; u < R * G - kLate; ++u) copy(u / G, u / G, u % G);
+    wait_vm<(R - 1) * G - kLate>();
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kFirst; ++u) read_step(0, 0, u);
+    take_scales();
+
+    // Stage t: its first k-step's fragments and its scales are in registers.  The second's are read under the first's
+    // products; then the stage is no longer needed: behind the barrier, which also waits for stage t + 1, its slot takes the
+    // next copies, and the next stage's first fragments are read, under the second k-step's products.
+    int slot = 0;
+    if (row0 + 16 * TM * wm < M) {
+        for (int t = 0; t + 1 < T; ++t) {
+            const int next = next_slot(slot);
+            const int before = slot == 0 ? R - 1 : slot - 1;  // stage t + R - 1's slot
+            multiply(Zero{}, NReads{}, [&](int u) __attribute__((always_inline)) { read_step(slot, 1, u); }, NLate{},
+                     [&](int u) __attribute__((always_inline)) { copy(t + R - 1, before, kEarly + u); });
+            wait_vm<(R - 2) * G>();
+            __syncthreads();
+            multiply(One{}, NFirst{}, [&](int u) __attribute__((always_inline)) { read_step(next, 0, u); }, NEarly{},
+                     [&](int u) __attribute__((always_inline)) { copy(t + R, slot, u); });
+            take_scales();
+            slot = next;
+        }
+        // the last stage: blocks past K (and k-tiles past the last) count as zero
+#pragma unroll
+        for (int u = 0; u < kReads; ++u) read_step(slot, 1, u);
+        const int chunks = (S - ((T - 1) * C::WK + wk) * 128) / 16;
+        auto mask = [&](int ks) __attribute__((always_inline)) {
+            if (4 * ks + kg < chunks) return;
+#pragma unroll
+            for (int b = 0; b < TM; ++b) xf[ks][b] = i32x4_t{0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < NS + MS; ++i) sc[i] = kOnes;  // (a lane's second block lies past its first)
+        };
+        mask(0);
+        multiply(Zero{}, Zero{}, none, Zero{}, none);
+        mask(1);
+        multiply(One{}, Zero{}, none, Zero{}, none);
+    } else {  // no row of this wave's is there: it only makes its copies
+        for (int t = 0; t + 1 < T; ++t) {
+            const int before = slot == 0 ? R - 1 : slot - 1;
+#pragma unroll
+            for (int u = 0; u < kLate; ++u) copy(t + R - 1, before, kEarly + u);
+            wait_vm<(R - 2) * G>();
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < kEarly; ++u) copy(t + R, slot, u);
+            slot = next_slot(slot);
+        }
+    }
+
+    wait_vm<0>();
+    __syncthreads();  // no copy is in flight, and every wave is done with the stages
+    if constexpr (C::WK > 1) {
+        constexpr int kWaves = C::WM * C::WN;
+        static_assert((C::WK - 1) * kWaves * TM * TN * 1024 <= R * C::kStage, "the sums fit in the stages");
+        f32x4v_t* sums = reinterpret_cast<f32x4v_t*>(smem);
+        const int w = wm * C::WN + wn;
+        if (wk > 0) {
+#pragma unroll
+            for (int i = 0; i < TM * TN; ++i) sums[(((wk - 1) * kWaves + w) * TM * TN + i) * 64 + lane] = acc[i / TM][i % TM];
+        }
+        __syncthreads();
+        if (wk > 0) return;
+#pragma unroll
+        for (int o = 0; o < C::WK - 1; ++o)
+#pragma unroll
+            for (int i = 0; i < TM * TN; ++i) acc[i / TM][i % TM] += sums[((o * kWaves + w) * TM * TN + i) * 64 + lane];
+    }
+
+    // 16 rows at a time through this wave's own part of LDS
+    constexpr int kPitch = 16 * TN * sizeof(TO) + 16;
+    constexpr int kOut0 = C::WK > 1 ? (C::WK - 1) * C::WM * C::WN * TM * TN * 1024 : 0;  // behind the waves' sums
+    static_assert(kOut0 + C::WM * C::WN * 16 * kPitch <= R * C::kStage, "the rows fit in the stages");
+    char* buf = smem + kOut0 + (wm * C::WN + wn) * 16 * kPitch;
+    const int nw = n0 + 16 * TN * wn;
+#pragma unroll
+    for (int b = 0; b < TM; ++b) {
+        const int mb = row0 + 16 * (TM * wm + b);
+        if (mb >= M) break;
+#pragma unroll
+        for (int a = 0; a < TN; ++a) {
+            Pack<TO, 4> o;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o.v[e] = from_f32<TO>(acc[a][b][e]);
+            *reinterpret_cast<Pack<TO, 4>*>(buf + l16 * kPitch + (16 * a + 4 * kg) * sizeof(TO)) = o;
+        }
+        wave_lds_sync();
+        store_rows<TO, TN>(buf, y, N, mb, nw, M);
+        wave_lds_sync();
+    }
+}
+
+struct Product {
+    const uint8_t *xq, *xscales;
+    int64_t M;
+    const uint8_t *codes, *scales;
+    int64_t N, K;
+    hipStream_t stream;
+};
+
+template <typename C>
+int64_t launch_blocks(int64_t M, int64_t N) {
+    return ((N + C::BN - 1) / C::BN) * ((M + C::BM - 1) / C::BM);
+}
+template <typename C>
+bool fits_grid(int64_t M, int64_t N) {
+    return launch_blocks<C>(M, N) < ((int64_t)1 << 31) / (64 * C::NW);  // the grid's threads
+}
+
+template <typename C, typename TO>
+hipError_t launch_tiles(const Product& p, TO* y) {
+    constexpr int kGroup = C::BM < 256 ? 1024 / C::BM : 4;  // row tiles walked together: about 1024 rows
+    hipLaunchKernelGGL((w4a4_tile_kernel<TO, C>), dim3((unsigned)launch_blocks<C>(p.M, p.N)), dim3(64 * C::NW), 0, p.stream, p.xq,
+                       p.xscales, (int)p.M, p.codes, p.scales, (int)p.N, (int)(p.K / 2), y, (int)((p.N + C::BN - 1) / C::BN), kGroup);
+    return hipGetLastError();
+}
+
+using T256x256 = Tiling<2, 4, 1, 8, 4, 2>;
+using T128x256 = Tiling<2, 4, 1, 4, 4, 3>;
+using T128x128 = Tiling<2, 4, 1, 4, 2, 4>;
+using T64x128 = Tiling<2, 4, 1, 2, 2, 3>;
+using T64x64 = Tiling<2, 2, 1, 2, 2, 4>;
+using T32x32 = Tiling<2, 2, 2, 1, 1, 4>;
+using T16x64 = Tiling<1, 4, 1, 1, 1, 4>;
+using T16x32 = Tiling<1, 2, 2, 1, 1, 4>;
+using T16x16 = Tiling<1, 1, 4, 1, 1, 4>;
+
+template <typename F>
+void each_tiling(F f) {
+    f(0, T256x256{});
+    f(1, T128x256{});
+    f(2, T128x128{});
+    f(3, T64x128{});
+    f(4, T64x64{});
+    f(5, T32x32{});
+    f(6, T16x64{});
+    f(7, T16x32{});
+    f(8, T16x16{});
 }
 
 }  // namespace
 
+bool w4a4_fits_grid(int64_t M, int64_t N) { return fits_grid<T256x256>(M, N); }
+
 hipError_t launch_gemm_w4a4(int dtype, const uint8_t* xq, const uint8_t* xscales, int64_t M, const uint8_t* codes,
                             const uint8_t* scales, int64_t N, int64_t K, void* y, hipStream_t stream) {
     return with_act_type(dtype, [&](auto t) {
-        using T = decltype(t);
-        const int64_t tiles = ((N + 63) / 64) * ((M + 15) / 16);
-        hipLaunchKernelGGL((w4a4_simple_kernel<T>), dim3((unsigned)std::min<int64_t>((tiles + 3) / 4, kMaxGridBlocks)), dim3(256), 0,
-                           stream, xq, xscales, (int)M, codes, scales, (int)N, (int)K, static_cast<T*>(y));
-        return hipGetLastError();
+        using TO = decltype(t);
+        const Product p{xq, xscales, M, codes, scales, N, K, stream};
+#ifndef TILING
+#define TILING (M > 512 && fits_grid<T256x256>(M, N) ? 0 : M > 64 ? 2 : M > 32 ? 4 : M > 16 ? 5 : N >= 8192 ? 7 : 8)
+#endif
+        const int want = TILING;
+        hipError_t e = hipErrorInvalidConfiguration;
+        each_tiling([&](int i, auto tiling) {
+            if (i == want) e = launch_tiles<decltype(tiling)>(p, static_cast<TO*>(y));
+        });
+        return e;
     });
 }
 

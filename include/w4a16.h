@@ -92,10 +92,11 @@ typedef enum {
      * power of two X = 2^(floor(log2 max|w|) - 2), its exponent not below -127, and elements with a sign, two exponent
      * bits and a mantissa bit, of magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6 (codes 0..7, 8..15 negative)
      * codes  uint8 [N][K/2]     byte j of a row = element of k = 2j (low nibble) and k = 2j+1 (high nibble)
-     * scales uint8 [T][N'][8]   T = K/256 and N' = N/16 x 16, both rounded up; byte (t, n, b) = 127 + log2 X of
-     *                           row n's block 8t + b, or 255 (NaN) for a block that holds an infinity or NaN
-     *                           (its elements 0).  Bytes past K are 0, those of rows past N are neither written
-     *                           nor of any effect.
+     * scales uint8 [T][G][4][16][2][2], T = K/256 and G = N/32, both rounded up: the byte 127 + log2 X of row n's
+     *                           block b (of 32 along K) is at [b/8][n/32][b%4][n%16][n/16%2][b/4%2], the order in
+     *                           which the matrix instructions take them; 255 (NaN) for a block that holds an
+     *                           infinity or NaN (its elements 0).  Blocks past K have 0; bytes of rows past N are
+     *                           neither written nor of any effect.
      * mins   unused (pass NULL)
      * element = w / X to nearest, ties to even, magnitudes past 6 becoming 6; w_hat = element X; K % 32 == 0.  For
      * the W4A4 calls (the 16-bit products return ERR_UNSUPPORTED).  Weights need not be finite. */

@@ -57,10 +57,10 @@ def test_refused(call, n):
 
 
 def test_sizes():
-    assert w.w4a16_packed_sizes(MX4, 14336, 4096) == (14336 * 2048, 16 * 14336 * 8, 0)
-    assert w.w4a16_packed_sizes(MX4, 1, 32) == (16, 128, 0)
-    assert w.w4a16_packed_sizes(MX4, 17, 288) == (17 * 144, 2 * 32 * 8, 0)
-    assert w.w4a16_w4a4_workspace_bytes(MX4, 17, 5, 288) == 17 * 144 + 2 * 32 * 8
+    assert w.w4a16_packed_sizes(MX4, 14336, 4096) == (14336 * 2048, 16 * 448 * 256, 0)
+    assert w.w4a16_packed_sizes(MX4, 1, 32) == (16, 256, 0)
+    assert w.w4a16_packed_sizes(MX4, 17, 288) == (17 * 144, 2 * 256, 0)
+    assert w.w4a16_w4a4_workspace_bytes(MX4, 17, 5, 288) == 17 * 144 + 2 * 256
     for bad in [(W8, 4, 8, 32), (MX4, 0, 8, 32), (MX4, 4, 8, 40), (MX4, 4, 0, 32), (MX4, 4, 8, WIDE)]:
         assert w.w4a16_w4a4_workspace_bytes(*bad) == 0
     assert w.w4a16_gemm_workspace_bytes(MX4, 300, 256, 4096) == 0 and w.w4a16_prepared_bytes(MX4, 8, 64) == 0
@@ -68,7 +68,7 @@ def test_sizes():
     for bad in [(0, 2, 80), (3, 0, 80), (3, 2, 0), (3, 2, 40), (TOKENS + 1, 1, 80), (3, PAIRS, 80)]:
         assert w.w4a16_expert_layer_workspace_bytes(*bad) == 0
     codes, scales, mins = w.alloc_packed(MX4, 17, 288, device="cpu")
-    assert codes.shape == (17, 144) and scales.shape == (2, 32, 8) and mins is None
+    assert codes.shape == (17, 144) and scales.shape == (2, 1, 4, 16, 2, 2) and mins is None
     assert (codes.numel(), scales.numel()) == w.w4a16_packed_sizes(MX4, 17, 288)[:2]
 
 
@@ -81,7 +81,7 @@ def test_check_weights():
 
 M, N, K = 5, 17, 288
 T, P, E, H, I = 3, 6, 4, 32, 80
-SCALES = lambda rows, k: (U8, (k + 255) // 256 * ((rows + 15) // 16 * 16) * 8)
+SCALES = lambda rows, k: (U8, (k + 255) // 256 * ((rows + 31) // 32) * 256)
 
 
 def calls(a):

@@ -126,18 +126,14 @@ __global__ __launch_bounds__(64 * C::NW) void w4a4_tile_kernel(const uint8_t* __
             const int j = min(CW * wave + i, C::kCodes / 1024 - 1), jj = j % kTileCopies;
             const int kt = min(t * C::WK + j / kTileCopies, KT - 1);
             const uint8_t* base = (jj < BN / 8 ? wbase : xbase) + (size_t)kt * 128;
-            uint32_t off = voff[i];
-            const int left = S - kt * 128;
-            if (left < 128) {
-                const int r = 8 * jj + lane / 8, chunk = (lane % 8) ^ ((r >> 1) & 7);
-                off -= (uint32_t)max(16 * chunk - (left - 16), 0);
-            }
-            if (t >= T) base = wbase, off = 0;
+            // (no branches: the compiler would move products across them, and past the barriers)
+            const int over = 16 * ((lane % 8) ^ ((4 * jj + lane / 16) & 7)) + 16 - (S - kt * 128);
+            const uint32_t off = (voff[i] - (uint32_t)max(over, 0)) & (t < T ? ~0u : 0u);
             dma16(off, base, lds0 + (uint32_t)(slot * C::kStage + 1024 * j));
         } else {
             const int s = i - CW, j = min(SW * wave + s, C::kScaleCopies - 1);
             const int kt = min(t * C::WK + stile[s], KT - 1);
-            dma16_at(sptr[s] + (t >= T ? 0 : kt * sstep[s]), lds0 + (uint32_t)(slot * C::kStage + C::kCodes + 1024 * j));
+            dma16_at(sptr[s] + kt * sstep[s], lds0 + (uint32_t)(slot * C::kStage + C::kCodes + 1024 * j));
         }
     };
 
@@ -163,22 +159,28 @@ __global__ __launch_bounds__(64 * C::NW) void w4a4_tile_kernel(const uint8_t* __
     for (int a = 0; a < TN; ++a)
 #pragma unroll
         for (int b = 0; b < TM; ++b) acc[a][b] = f32x4v_t{0, 0, 0, 0};
-    i32x4_t wf[2][TN], xf[2][TM];
+    // Activation fragments of wide wave tiles are read in place, each behind the products that take it; narrow ones
+    // are read a step ahead into registers of their own.  (Both for 128 x 64 spill.)
+    constexpr bool kInPlace = TM >= 4;
+    i32x4_t wf[2][TN], xf[kInPlace ? 1 : 2][TM];
     int sc[NS + MS], sc_next[NS + MS];  // of this stage's k-tile (both k-steps), and of the next's
 
-    // the products of k-step ks, with `reads` reads spread over the first three quarters of them and `copies` copies
-    // over all
+    // The products of k-step ks, rows of x one after another, with `reads` reads and `copies` copies among them: the copies
+    // and, where fragments have registers of their own, the reads spread over all and over the first three quarters;
+    // else x fragment b behind its products, the others within the first half.
     auto multiply = [&](auto step, auto reads, auto read, auto copies, auto copy) __attribute__((always_inline)) {
-        constexpr int ks = decltype(step)::value, H = TM * TN, HR = (3 * H + 3) / 4;
+        constexpr int ks = decltype(step)::value, H = TM * TN, HR = kInPlace ? (H + 1) / 2 : (3 * H + 3) / 4;
         constexpr int nr = decltype(reads)::value, nc = decltype(copies)::value;
+        constexpr int first = kInPlace && nr > 0 ? TM : 0;  // (reads 0.. TM - 1 are the x fragments)
         each(std::make_integer_sequence<int, H>{}, [&](auto index) __attribute__((always_inline)) {
-            constexpr int i = decltype(index)::value, a = i / TM, b = i % TM;
+            constexpr int i = decltype(index)::value, a = i % TN, b = i / TN, n = nr - first;
 #pragma unroll
-            for (int u = (i * nr + HR - 1) / HR; u < min(nr, ((i + 1) * nr + HR - 1) / HR); ++u) read(u);
+            for (int u = (i * n + HR - 1) / HR; u < min(n, ((i + 1) * n + HR - 1) / HR); ++u) read(first + u);
 #pragma unroll
             for (int u = (i * nc + H - 1) / H; u < ((i + 1) * nc + H - 1) / H; ++u) copy(u);
-            acc[a][b] = mfma<(TN == 1 ? 0 : a % 2 * 2) + ks, (TM == 1 ? 0 : b % 2 * 2) + ks>(wf[ks][a], xf[ks][b], acc[a][b], sc[a / 2],
-                                                                                             sc[NS + b / 2]);
+            acc[a][b] = mfma<(TN == 1 ? 0 : a % 2 * 2) + ks, (TM == 1 ? 0 : b % 2 * 2) + ks>(
+                wf[ks][a], xf[kInPlace ? 0 : ks][b], acc[a][b], sc[a / 2], sc[NS + b / 2]);
+            if (first > 0 && a == TN - 1) read(b);
             if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
             if (i == 0) __builtin_amdgcn_s_setprio(1);
             if (i == H - 1) __builtin_amdgcn_s_setprio(0);
@@ -187,7 +189,7 @@ __global__ __launch_bounds__(64 * C::NW) void w4a4_tile_kernel(const uint8_t* __
     // read u of a stage in ring slot `slot`: fragments, and with the first k-step's the scales
     auto read_step = [&](int slot, int ks, int u) __attribute__((always_inline)) {
         if (u < TM) {
-            xf[ks][u] = read(slot, ks, x_rt + u);
+            xf[kInPlace ? 0 : ks][u] = read(slot, ks, x_rt + u);
         } else if (u < TM + TN) {
             wf[ks][u - TM] = read(slot, ks, w_rt + u - TM);
         } else {
@@ -239,18 +241,23 @@ __global__ __launch_bounds__(64 * C::NW) void w4a4_tile_kernel(const uint8_t* __
             slot = next;
         }
         // the last stage: blocks past K (and k-tiles past the last) count as zero
+        if constexpr (!kInPlace) {
 #pragma unroll
-        for (int u = 0; u < kReads; ++u) read_step(slot, 1, u);
+            for (int u = 0; u < kReads; ++u) read_step(slot, 1, u);
+        }
         const int chunks = (S - ((T - 1) * C::WK + wk) * 128) / 16;
         auto mask = [&](int ks) __attribute__((always_inline)) {
             if (4 * ks + kg < chunks) return;
 #pragma unroll
-            for (int b = 0; b < TM; ++b) xf[ks][b] = i32x4_t{0, 0, 0, 0};
+            for (int b = 0; b < TM; ++b) xf[kInPlace ? 0 : ks][b] = i32x4_t{0, 0, 0, 0};
 #pragma unroll
             for (int i = 0; i < NS + MS; ++i) sc[i] = kOnes;  // (a lane's second block lies past its first)
         };
         mask(0);
-        multiply(Zero{}, Zero{}, none, Zero{}, none);
+        if constexpr (kInPlace)
+            multiply(Zero{}, NReads{}, [&](int u) __attribute__((always_inline)) { read_step(slot, 1, u); }, Zero{}, none);
+        else
+            multiply(Zero{}, Zero{}, none, Zero{}, none);
         mask(1);
         multiply(One{}, Zero{}, none, Zero{}, none);
     } else {  // no row of this wave's is there: it only makes its copies

@@ -774,10 +774,8 @@ w4a16_status_t w4a16_matmul_w4a4(w4a16_format_t fmt, w4a16_dtype_t act, const vo
     if (workspace_bytes < w.needed) return W4A16_ERR_INVALID;
     uint8_t* base = static_cast<uint8_t*>(workspace);
     w4a16::clear_stale_error();
-    if (const hipError_t e = w4a16::launch_quant_mx4((int)act, x, M, K, base, base + w.scales, stream); e != hipSuccess)
-        return from_hip(e);
-    return from_hip(w4a16::launch_gemm_w4a4((int)act, base, base + w.scales, M, static_cast<const uint8_t*>(codes),
-                                            static_cast<const uint8_t*>(scales), N, K, y, stream));
+    return from_hip(w4a16::launch_matmul_w4a4((int)act, x, M, static_cast<const uint8_t*>(codes),
+                                              static_cast<const uint8_t*>(scales), N, K, y, base, base + w.scales, stream));
 }
 
 int64_t w4a16_expert_layer_max_tokens(void) { return w4a16::kLayerTokens; }

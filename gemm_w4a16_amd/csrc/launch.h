@@ -201,6 +201,9 @@ hipError_t launch_dequant_mx4(const uint8_t* codes, const uint8_t* scales, int64
 bool w4a4_fits_grid(int64_t M, int64_t N);
 hipError_t launch_gemm_w4a4(int dtype, const uint8_t* xq, const uint8_t* xscales, int64_t M, const uint8_t* codes,
                             const uint8_t* scales, int64_t N, int64_t K, void* y, hipStream_t stream);
+// The product of activations x quantized on the way (xq and xscales hold them where a launch of its own does).
+hipError_t launch_matmul_w4a4(int dtype, const void* x, int64_t M, const uint8_t* codes, const uint8_t* scales, int64_t N, int64_t K,
+                              void* y, uint8_t* xq, uint8_t* xscales, hipStream_t stream);
 
 // A few tokens' whole pass through their experts; hq [T topk][I] and hscale (expert_layer_scale_bytes of it) hold the
 // experts' activations between the two launches.

@@ -315,6 +315,155 @@ __global__ __launch_bounds__(64 * C::NW) void w4a4_tile_kernel(const uint8_t* __
     }
 }
 
+// ---- few rows -----------------------------------------------------------------------------------
+
+// Up to 16 rows: a block computes 16 columns, its waves every kWaves-th k-tile each, from a ring of its own in LDS (R
+// stages of one k-tile), with no barrier until their sums are added, in the order of waves.  TX uint8_t: rows in
+// the format (kRows of them staged).  Else activations, one or two rows, that each lane quantizes as the block
+// that it multiplies: a block's 32 values are one lane's part of an operand, so nothing is exchanged.
+template <typename TX, int kRows>
+struct RowShape {
+    static constexpr bool kFused = !std::is_same_v<TX, uint8_t>;
+    static constexpr int kXBytes = kFused ? kRows * kMx4TileK * (int)sizeof(TX) : kRows * 128;
+    static constexpr int kScales = 2048, kX = kScales + 1024, kStage = kX + kXBytes;  // weights, scales, rows
+    static constexpr int kOwn = kFused ? kRows * 256 : 0;  // a wave's codes [row][128] and scales, behind the ring
+    static constexpr int kXCopies = kXBytes / 1024, kCopies = 2 + 1 + kXCopies;
+    static constexpr int R = 2;  // (three or four: fewer blocks a CU, 0-20% slower)
+    static_assert(kXBytes % 1024 == 0, "whole copies");
+};
+
+template <typename TO, typename TX, int kRows, int kWaves, bool kOnce>
+__global__ __launch_bounds__(64 * kWaves) void w4a4_rows_kernel(const TX* __restrict__ x, const uint8_t* __restrict__ xscales,
+                                                                   int M, const uint8_t* __restrict__ codes,
+                                                                   const uint8_t* __restrict__ scales, int N, int S,
+                                                                   TO* __restrict__ y) {
+    using C = RowShape<TX, kRows>;
+    constexpr int R = C::R;
+    __shared__ __attribute__((aligned(1024))) char smem[kWaves * (R * C::kStage + C::kOwn)];
+    const int lane = lane_id(), wave = wave_id(), l16 = lane & 15, kg = lane >> 4;
+    const int n0 = blockIdx.x * 16, KT = (S + 127) / 128, T = (KT - wave + kWaves - 1) / kWaves;
+    char* ring = smem + wave * R * C::kStage;
+    const uint32_t ring_lds = lds_addr(ring);
+    const uint8_t* wbase = codes + (size_t)n0 * S;
+    // this lane's 16 bytes of the scales: the weights' in lanes 0..15, x's in the others
+    const int64_t gw = mx4_groups(N);
+    const bool of_x = !C::kFused && lane >= 16;
+    const char* sptr = reinterpret_cast<const char*>(of_x ? xscales : scales + n0 / 32 * (int64_t)256) + lane % 16 * 16;
+    const int64_t sstep = of_x ? 256 : gw * 256;  // (one group of rows)
+
+    // LDS slot lane % 8 of a row takes its 16-byte chunk slot ^ ((row >> 1) & 7)
+    auto chunk_of = [&](int r) __attribute__((always_inline)) { return (lane % 8) ^ ((r >> 1) & 7); };
+    auto issue = [&](int t, int slot) __attribute__((always_inline)) {
+        const int kt = min(t * kWaves + wave, KT - 1);  // (past the last: as many copies of the last)
+        const uint32_t lds = ring_lds + (uint32_t)(slot * C::kStage);
+        const int last = S - 16;  // of a row; chunks past K read it (their products are masked)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = 8 * i + lane / 8;
+            const uint32_t off = (uint32_t)min(r, N - 1 - n0) * (uint32_t)S + (uint32_t)min(kt * 128 + 16 * chunk_of(r), last);
+            if constexpr (kOnce)
+                dma16_once(off, wbase, lds + 1024 * i);
+            else
+                dma16(off, wbase, lds + 1024 * i);
+        }
+        dma16_at(sptr + kt * sstep, lds + C::kScales);
+        if constexpr (C::kFused) {
+            constexpr int kRowBytes = kMx4TileK * sizeof(TX);  // of a row in a k-tile
+#pragma unroll
+            for (int i = 0; i < C::kXCopies; ++i) {
+                const int b = 1024 * i + 16 * lane, r = min(b / kRowBytes, M - 1);
+                const int at = min(kt * kRowBytes + b % kRowBytes, 2 * S * (int)sizeof(TX) - 16);
+                dma16((uint32_t)r * (uint32_t)(2 * S * sizeof(TX)) + (uint32_t)at, x, lds + C::kX + 1024 * i);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < C::kXCopies; ++i) {
+                const int r = 8 * i + lane / 8;
+                dma16((uint32_t)min(r, M - 1) * (uint32_t)S + (uint32_t)min(kt * 128 + 16 * chunk_of(r), last), x, lds + C::kX + 1024 * i);
+            }
+        }
+    };
+    f32x4v_t acc = {0, 0, 0, 0};
+    const int w_shift = 16 * ((n0 / 16) & 1), sw = (l16 >> 1) & 7;
+#pragma unroll
+    for (int t = 0; t < R - 1; ++t) issue(t, t);
+    int slot = 0;
+    for (int t = 0; t < T; ++t) {
+        issue(t + R - 1, slot + R - 1 >= R ? slot - 1 : slot + R - 1);
+        wait_vm<(R - 1) * C::kCopies>();
+        const char* w = ring + slot * C::kStage;
+        const int chunks = (S - (t * kWaves + wave) * 128) / 16;
+        int ws = *reinterpret_cast<const int*>(w + C::kScales + 4 * lane) >> w_shift;
+        int xs = 0;
+        char* own = smem + kWaves * R * C::kStage + wave * C::kOwn;
+        if constexpr (C::kFused) {
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const Pack<TX, 4> v = *reinterpret_cast<const Pack<TX, 4>*>(w + C::kX + r * (int)(kMx4TileK * sizeof(TX)) + lane * (int)(4 * sizeof(TX)));
+                float f[4];
+                uint32_t top = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] = to_f32(v.v[j]), top = max(top, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+                top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, kDppQuadXor1, 0xF, 0xF, false));
+                top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, kDppQuadXor2, 0xF, 0xF, false));
+                top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, kDppRowHalfMirror, 0xF, 0xF, false));
+                const uint32_t s = mx4_scale(top);
+                const float inv = mx4_inverse(s);
+                uint32_t q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, f[0] * inv, f[1] * inv, 1.0f, 0);
+                q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, f[2] * inv, f[3] * inv, 1.0f, 1);
+                *reinterpret_cast<uint16_t*>(own + 256 * r + 2 * lane) = s == 255 ? 0 : (uint16_t)q;
+                if (lane % 8 == 0) own[256 * r + 128 + lane / 8 % 4 * 2 + lane / 32] = (char)s;
+            }
+            wave_lds_sync();
+            xs = *reinterpret_cast<const uint16_t*>(own + 256 * min(l16, kRows - 1) + 128 + 2 * kg);
+        } else {
+            xs = *reinterpret_cast<const int*>(w + C::kScales + 256 + 4 * lane);
+        }
+        each(std::make_integer_sequence<int, 2>{}, [&](auto step) __attribute__((always_inline)) {
+            constexpr int ks = decltype(step)::value;
+            const i32x4_t wf = *reinterpret_cast<const i32x4_t*>(w + 128 * l16 + 16 * ((4 * ks + kg) ^ sw));
+            i32x4_t xf;
+            if constexpr (C::kFused) {
+                xf = *reinterpret_cast<const i32x4_t*>(own + 256 * min(l16, kRows - 1) + 16 * (4 * ks + kg));
+            } else {
+                const int r = l16 % kRows;
+                xf = *reinterpret_cast<const i32x4_t*>(w + C::kX + 128 * r + 16 * ((4 * ks + kg) ^ ((r >> 1) & 7)));
+            }
+            if (4 * ks + kg >= chunks) xf = i32x4_t{0, 0, 0, 0}, xs = ws = kOnes;  // (a lane's second block lies past its first)
+            acc = mfma<ks, ks>(wf, xf, acc, ws, xs);
+        });
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the stage is read, copies may overwrite it
+        slot = slot + 1 == R ? 0 : slot + 1;
+    }
+    wait_vm<0>();
+    __syncthreads();
+    f32x4v_t* sums = reinterpret_cast<f32x4v_t*>(smem);
+    sums[wave * 64 + lane] = acc;
+    __syncthreads();
+    if (wave > 0 || l16 >= M) return;
+    acc = sums[lane];
+#pragma unroll
+    for (int i = 1; i < kWaves; ++i) acc += sums[i * 64 + lane];
+    TO* out = y + (size_t)l16 * N + n0 + 4 * kg;
+    Pack<TO, 4> o;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o.v[e] = from_f32<TO>(acc[e]);
+    if (N % 4 == 0) {
+        if (n0 + 4 * kg < N) *reinterpret_cast<Pack<TO, 4>*>(out) = o;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (n0 + 4 * kg + e < N) out[e] = o.v[e];
+    }
+}
+
+// Rows quantized inside the product: one or two, and three or four of few and short columns (4096 x 4096 5.0 us
+// against 5.5 in two launches, 1024 x 1024 3.4 against 5.0; 14336 x 4096 11.8 against 10.3, 4096 x 14336 10.8 against
+// 10.0: every block quantizes them).
+constexpr int64_t kFewRows = 16;
+bool fused_rows(int64_t M, int64_t N, int64_t K) { return M <= 2 || (M <= 4 && N * K <= ((int64_t)1 << 25)); }
+
+
 struct Product {
     const uint8_t *xq, *xscales;
     int64_t M;
@@ -340,15 +489,30 @@ hipError_t launch_tiles(const Product& p, TO* y) {
     return hipGetLastError();
 }
 
+// Few rows x, in the format or as activations.  Eight waves a block where they leave each CU two blocks at the most, for
+// the shorter chain of k-tiles (one row of 4096 x 14336 8.5 us against 10.1), else four, of which more blocks fit a CU
+// (14336 x 4096 9.1 against 9.8).
+template <typename TO, typename TX, int kRows>
+hipError_t launch_rows(const Product& p, const TX* x, TO* y) {
+    const int64_t blocks = (p.N + 15) / 16;
+    auto run = [&](auto waves, auto once) {
+        constexpr int kWaves = decltype(waves)::value;
+        hipLaunchKernelGGL((w4a4_rows_kernel<TO, TX, kRows, kWaves, decltype(once)::value>), dim3((unsigned)blocks), dim3(64 * kWaves), 0,
+                           p.stream, x, p.xscales, (int)p.M, p.codes, p.scales, (int)p.N, (int)(p.K / 2), y);
+        return hipGetLastError();
+    };
+    if (blocks <= 512) return run(std::integral_constant<int, 8>{}, std::false_type{});
+    const bool once = (double)p.N * (double)p.K / 2 >= kOnceBytes;
+    return once ? run(std::integral_constant<int, 4>{}, std::true_type{}) : run(std::integral_constant<int, 4>{}, std::false_type{});
+}
+
 using T256x256 = Tiling<2, 4, 1, 8, 4, 2>;
 using T128x256 = Tiling<2, 4, 1, 4, 4, 3>;
 using T128x128 = Tiling<2, 4, 1, 4, 2, 4>;
 using T64x128 = Tiling<2, 4, 1, 2, 2, 3>;
 using T64x64 = Tiling<2, 2, 1, 2, 2, 4>;
+using T32x64 = Tiling<2, 4, 1, 1, 1, 4>;
 using T32x32 = Tiling<2, 2, 2, 1, 1, 4>;
-using T16x64 = Tiling<1, 4, 1, 1, 1, 4>;
-using T16x32 = Tiling<1, 2, 2, 1, 1, 4>;
-using T16x16 = Tiling<1, 1, 4, 1, 1, 4>;
 
 template <typename F>
 void each_tiling(F f) {
@@ -357,10 +521,25 @@ void each_tiling(F f) {
     f(2, T128x128{});
     f(3, T64x128{});
     f(4, T64x64{});
-    f(5, T32x32{});
-    f(6, T16x64{});
-    f(7, T16x32{});
-    f(8, T16x16{});
+    f(5, T32x64{});
+    f(6, T32x32{});
+}
+
+template <typename TO>
+hipError_t launch_product(const Product& p, TO* y) {
+    const int64_t M = p.M, N = p.N;
+    (void)N;
+#ifndef TILING
+#define TILING (M > 512 && fits_grid<T256x256>(M, N) ? 0 : M > 64 ? 2 : M > 32 ? 4 : 6)
+#endif
+    if (M <= 8) return launch_rows<TO, uint8_t, 8>(p, p.xq, y);
+    if (M <= kFewRows) return launch_rows<TO, uint8_t, 16>(p, p.xq, y);
+    const int want = TILING;
+    hipError_t e = hipErrorInvalidConfiguration;
+    each_tiling([&](int i, auto tiling) {
+        if (i == want) e = launch_tiles<decltype(tiling)>(p, y);
+    });
+    return e;
 }
 
 }  // namespace
@@ -371,16 +550,19 @@ hipError_t launch_gemm_w4a4(int dtype, const uint8_t* xq, const uint8_t* xscales
                             const uint8_t* scales, int64_t N, int64_t K, void* y, hipStream_t stream) {
     return with_act_type(dtype, [&](auto t) {
         using TO = decltype(t);
+        return launch_product<TO>(Product{xq, xscales, M, codes, scales, N, K, stream}, static_cast<TO*>(y));
+    });
+}
+
+hipError_t launch_matmul_w4a4(int dtype, const void* x, int64_t M, const uint8_t* codes, const uint8_t* scales, int64_t N, int64_t K,
+                              void* y, uint8_t* xq, uint8_t* xscales, hipStream_t stream) {
+    return with_act_type(dtype, [&](auto t) {
+        using T = decltype(t);
         const Product p{xq, xscales, M, codes, scales, N, K, stream};
-#ifndef TILING
-#define TILING (M > 512 && fits_grid<T256x256>(M, N) ? 0 : M > 64 ? 2 : M > 32 ? 4 : M > 16 ? 5 : N >= 8192 ? 7 : 8)
-#endif
-        const int want = TILING;
-        hipError_t e = hipErrorInvalidConfiguration;
-        each_tiling([&](int i, auto tiling) {
-            if (i == want) e = launch_tiles<decltype(tiling)>(p, static_cast<TO*>(y));
-        });
-        return e;
+        if (M <= 2) return launch_rows<T, T, 2>(p, static_cast<const T*>(x), static_cast<T*>(y));
+        if (fused_rows(M, N, K)) return launch_rows<T, T, 4>(p, static_cast<const T*>(x), static_cast<T*>(y));
+        if (const hipError_t e = launch_quant_mx4(dtype, x, M, K, xq, xscales, stream); e != hipSuccess) return e;
+        return launch_product<T>(p, static_cast<T*>(y));
     });
 }
 

@@ -8,7 +8,7 @@
 // Gradients, of y = norm(h) for the h that was stored (g = dy w, r from h):
 //     dx = r (g - h r^2 sum_n(g h) / N) + dh,   dw_n = sum_t dy h r.
 //
-// Bytes bound all of these for many rows, and a row's chain of two reductions for few.  A row stays in registers
+// Bytes bound all of these for many rows, and a row's chain of loads and reductions for few.  A row stays in registers
 // between its passes (kKeep units of 16 bytes a thread); what a long row has beyond that is read again, from the
 // caches.
 #include <algorithm>
@@ -22,38 +22,43 @@ namespace w4a16 {
 
 namespace {
 
-constexpr int kKeep = 4;  // units of a row that a thread holds
-
 template <typename T>
 constexpr int kUnit = 16 / (int)sizeof(T);
 
-// Unit c of a row of N elements as fp32: elements past the row's end are zero.  kAny: rows start at any element.
-template <bool kAny, typename T>
-__device__ __forceinline__ void load_row_unit(const T* row, int c, int N, float (&f)[kUnit<T>]) {
+// Unit c of a row of N elements: elements past the row's end are zero.  kAny: rows start at any element; kStream: past
+// the caches' usual order.
+template <bool kStream, bool kAny, typename T>
+__device__ __forceinline__ Pack<T, kUnit<T>> load_row_unit(const T* row, int c, int N) {
     constexpr int V = kUnit<T>;
+    if (!kAny || (c + 1) * V <= N) return load_unit<kStream, kAny, V>(row + c * V);
     Pack<T, V> u;
-    if (!kAny || (c + 1) * V <= N) {
-        u = load_unit<false, kAny, V>(row + c * V);
-    } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) u.v[j] = c * V + j < N ? row[c * V + j] : from_f32<T>(0.0f);
-    }
-#pragma unroll
-    for (int j = 0; j < V; ++j) f[j] = to_f32(u.v[j]);
+    for (int j = 0; j < V; ++j) u.v[j] = c * V + j < N ? row[c * V + j] : from_f32<T>(0.0f);
+    return u;
 }
-template <bool kAny, typename T>
+template <bool kStream, bool kAny, typename T>
 __device__ __forceinline__ void store_row_unit(T* row, int c, int N, const float (&f)[kUnit<T>]) {
     constexpr int V = kUnit<T>;
     Pack<T, V> u;
 #pragma unroll
     for (int j = 0; j < V; ++j) u.v[j] = from_f32<T>(f[j]);
     if (!kAny || (c + 1) * V <= N) {
-        store_unit<false, kAny>(row + c * V, u);
+        store_unit<kStream, kAny>(row + c * V, u);
     } else {
 #pragma unroll
         for (int j = 0; j < V; ++j)
             if (c * V + j < N) row[c * V + j] = u.v[j];
     }
+}
+template <typename T, int V>
+__device__ __forceinline__ void widen(const Pack<T, V>& u, float (&f)[V]) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = to_f32(u.v[j]);
+}
+template <typename T, int V>
+__device__ __forceinline__ void add(const Pack<T, V>& u, float (&f)[V]) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] += to_f32(u.v[j]);
 }
 
 // A sum or maximum over the threads of a row, the same in each: lanes, then waves in order.  red: a word per wave.
@@ -69,6 +74,20 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
         for (int w = 1; w < kWaves; ++w) v += red[w];
     }
     return v;
+}
+// (two sums at once)
+template <int kWaves>
+__device__ __forceinline__ void row_sums(float& a, float& b, float2* red) {
+    a = wave_sum(a);
+    b = wave_sum(b);
+    if constexpr (kWaves > 1) {
+        __syncthreads();
+        if (lane_id() == 0) red[wave_id()] = make_float2(a, b);
+        __syncthreads();
+        a = red[0].x, b = red[0].y;
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) a += red[w].x, b += red[w].y;
+    }
 }
 // (of magnitudes' bits, which order like the magnitudes, infinity above every finite value and NaN above infinity)
 template <int kWaves>
@@ -114,11 +133,12 @@ __device__ __forceinline__ void codes_i8(const float (&v)[V], float a, float inv
 
 // x, residual, h and y may be the same memory: a thread reads a unit of x and residual before it writes that unit of h
 // and y, in each pass, and no other thread's.
-template <typename T, int kWaves, bool kI8, bool kAny>
-__global__ __launch_bounds__(256) void add_rmsnorm_kernel(const T* x, const T* residual, int64_t rows, int N,
-                                                          const T* __restrict__ weight, float eps, T* h, T* y,
-                                                          int8_t* __restrict__ xq, float* __restrict__ ascale) {
-    constexpr int V = kUnit<T>, kThreads = 64 * kWaves, kRows = 4 / kWaves;
+template <typename T, int kWaves, int kKeep, bool kI8, bool kAny, bool kStream>
+__global__ __launch_bounds__(kWaves == 1 ? 256 : 64 * kWaves) void add_rmsnorm_kernel(const T* x, const T* residual, int64_t rows,
+                                                                                      int N, const T* __restrict__ weight, float eps,
+                                                                                      T* h, T* y, int8_t* __restrict__ xq,
+                                                                                      float* __restrict__ ascale) {
+    constexpr int V = kUnit<T>, kThreads = 64 * kWaves, kRows = kWaves == 1 ? 4 : 1;
     __shared__ float red[kWaves];
     const int tid = kWaves == 1 ? lane_id() : (int)threadIdx.x;
     const int units = (N + V - 1) / V;
@@ -127,25 +147,29 @@ __global__ __launch_bounds__(256) void add_rmsnorm_kernel(const T* x, const T* r
         if (kWaves == 1 && m >= rows) continue;
         const T* xr = x + m * N;
         const T* rr = residual ? residual + m * N : nullptr;
+        // s of a unit that is read again
         auto sum_unit = [&](int c, float (&s)[V]) __attribute__((always_inline)) {
-            load_row_unit<kAny>(xr, c, N, s);
-            if (rr) {
-                float a[V];
-                load_row_unit<kAny>(rr, c, N, a);
-#pragma unroll
-                for (int j = 0; j < V; ++j) s[j] += a[j];
-            }
+            widen(load_row_unit<false, kAny>(xr, c, N), s);
+            if (rr) add(load_row_unit<false, kAny>(rr, c, N), s);
         };
-        float keep[kKeep][V], ss = 0.0f;
+        // every load of the row, and of the weight, before anything waits for one
+        Pack<T, V> xu[kKeep], ru[kKeep], wu[kKeep];
 #pragma unroll
         for (int i = 0; i < kKeep; ++i) {
             const int c = tid + kThreads * i;
-            if (c < units) {
-                sum_unit(c, keep[i]);
-            } else {
+            xu[i] = c < units ? load_row_unit<kStream, kAny>(xr, c, N) : Pack<T, V>{};
+            if (rr) ru[i] = c < units ? load_row_unit<kStream, kAny>(rr, c, N) : Pack<T, V>{};
+        }
 #pragma unroll
-                for (int j = 0; j < V; ++j) keep[i][j] = 0.0f;
-            }
+        for (int i = 0; i < kKeep; ++i) {
+            const int c = tid + kThreads * i;
+            if (weight && c < units) wu[i] = load_row_unit<false, kAny>(weight, c, N);
+        }
+        float keep[kKeep][V], ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i) {
+            widen(xu[i], keep[i]);
+            if (rr) add(ru[i], keep[i]);
         }
 #pragma unroll
         for (int i = 0; i < kKeep; ++i)
@@ -160,27 +184,28 @@ __global__ __launch_bounds__(256) void add_rmsnorm_kernel(const T* x, const T* r
         ss = row_sum<kWaves>(ss, red);
         const float r = 1.0f / sqrtf(ss / (float)N + eps);
         // s -> v
-        auto scaled = [&](int c, float (&s)[V]) __attribute__((always_inline)) {
-            float w[V];
-            if (weight) load_row_unit<kAny>(weight, c, N, w);
+        auto scaled = [&](const Pack<T, V>& w, float (&s)[V]) __attribute__((always_inline)) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) s[j] = weight ? s[j] * r * w[j] : s[j] * r;
+            for (int j = 0; j < V; ++j) s[j] = weight ? s[j] * r * to_f32(w.v[j]) : s[j] * r;
+        };
+        auto weight_unit = [&](int c) __attribute__((always_inline)) {
+            return weight ? load_row_unit<false, kAny>(weight, c, N) : Pack<T, V>{};
         };
         if constexpr (!kI8) {
-            auto out = [&](int c, float (&s)[V]) __attribute__((always_inline)) {
-                if (h) store_row_unit<kAny>(h + m * N, c, N, s);
-                scaled(c, s);
-                store_row_unit<kAny>(y + m * N, c, N, s);
+            auto out = [&](int c, const Pack<T, V>& w, float (&s)[V]) __attribute__((always_inline)) {
+                if (h) store_row_unit<kStream, kAny>(h + m * N, c, N, s);
+                scaled(w, s);
+                store_row_unit<kStream, kAny>(y + m * N, c, N, s);
             };
 #pragma unroll
             for (int i = 0; i < kKeep; ++i) {
                 const int c = tid + kThreads * i;
-                if (c < units) out(c, keep[i]);
+                if (c < units) out(c, wu[i], keep[i]);
             }
             for (int c = tid + kThreads * kKeep; c < units; c += kThreads) {
                 float s[V];
                 sum_unit(c, s);
-                out(c, s);
+                out(c, weight_unit(c), s);
             }
         } else {
             uint32_t top = 0;
@@ -192,15 +217,15 @@ __global__ __launch_bounds__(256) void add_rmsnorm_kernel(const T* x, const T* r
             for (int i = 0; i < kKeep; ++i) {
                 const int c = tid + kThreads * i;
                 if (c < units) {
-                    if (h) store_row_unit<kAny>(h + m * N, c, N, keep[i]);
-                    scaled(c, keep[i]);
+                    if (h) store_row_unit<kStream, kAny>(h + m * N, c, N, keep[i]);
+                    scaled(wu[i], keep[i]);
                     widest(keep[i]);
                 }
             }
             for (int c = tid + kThreads * kKeep; c < units; c += kThreads) {
                 float s[V];
                 sum_unit(c, s);
-                scaled(c, s);
+                scaled(weight_unit(c), s);
                 widest(s);
             }
             const float a = scale_i8(__uint_as_float(row_max<kWaves>(top, red))), inv = 1.0f / a;
@@ -220,8 +245,8 @@ __global__ __launch_bounds__(256) void add_rmsnorm_kernel(const T* x, const T* r
             for (int c = tid + kThreads * kKeep; c < units; c += kThreads) {
                 float s[V];
                 sum_unit(c, s);
-                if (h) store_row_unit<kAny>(h + m * N, c, N, s);
-                scaled(c, s);
+                if (h) store_row_unit<kStream, kAny>(h + m * N, c, N, s);
+                scaled(weight_unit(c), s);
                 codes(c, s);
             }
             if (lane_id() == 0) ascale[m] = a;  // (every wave's is the same)
@@ -231,63 +256,85 @@ __global__ __launch_bounds__(256) void add_rmsnorm_kernel(const T* x, const T* r
 
 // ---- gradients ----------------------------------------------------------------------------------
 
-// dx, and this block's part of dweight: a block takes rows blockIdx.x, + gridDim.x, ..., and a thread the same columns
-// of each, so that the columns' sums stay in its registers (N at most kThreads kUnits V) and leave once, to part
-// [blocks][N].  The order of additions does not depend on timing.
+// dx, and this block's part of dweight.  kWaves waves take a row (one: each its own), rows in turn, and a thread the
+// same columns of each, so that the columns' sums stay in its registers (N at most 64 kWaves kUnits V); waves of their own
+// rows add theirs in LDS at the end, in order.  A block's part leaves once, to part [blocks][N].  The order of additions
+// does not depend on timing.
+constexpr int kGradWaves = 8;  // of a block
 template <typename T, int kWaves, int kUnits, bool kAny>
-__global__ __launch_bounds__(64 * kWaves) void add_rmsnorm_backward_kernel(const T* dy, const T* dh, const T* __restrict__ h,
-                                                                           int64_t rows, int N, const T* __restrict__ weight,
-                                                                           float eps, T* dx, float* __restrict__ part) {
-    constexpr int V = kUnit<T>, kThreads = 64 * kWaves;
-    __shared__ float red[kWaves];
-    const int tid = threadIdx.x, units = (N + V - 1) / V;
-    float w[kUnits][V], dw[kUnits][V];
+__global__ __launch_bounds__(64 * kGradWaves) void add_rmsnorm_backward_kernel(const T* dy, const T* dh, const T* __restrict__ h,
+                                                                               int64_t rows, int N, const T* __restrict__ weight,
+                                                                               float eps, T* dx, float* __restrict__ part) {
+    constexpr int V = kUnit<T>, kThreads = 64 * kWaves, kRows = kGradWaves / kWaves;
+    static_assert(kWaves == 1 || kWaves == kGradWaves, "a wave or the block takes a row");
+    __shared__ float2 red[kWaves];
+    __shared__ float sums[kRows > 1 ? kRows * 64 * kUnits * V : 1];
+    const int tid = kWaves == 1 ? lane_id() : (int)threadIdx.x, units = (N + V - 1) / V;
+    Pack<T, V> w[kUnits];
+    float dw[kUnits][V];
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
         const int c = tid + kThreads * i;
 #pragma unroll
-        for (int j = 0; j < V; ++j) dw[i][j] = 0.0f, w[i][j] = 1.0f;
-        if (weight && c < units) load_row_unit<kAny>(weight, c, N, w[i]);
+        for (int j = 0; j < V; ++j) dw[i][j] = 0.0f, w[i].v[j] = from_f32<T>(1.0f);
+        if (weight && c < units) w[i] = load_row_unit<false, kAny>(weight, c, N);
     }
-    for (int64_t m = blockIdx.x; m < rows; m += gridDim.x) {
-        float g[kUnits][V], hv[kUnits][V], ss = 0.0f, gh = 0.0f;
+    const int64_t first = (int64_t)blockIdx.x * kRows + (kWaves == 1 ? wave_id() : 0);
+    for (int64_t m = first; m < rows; m += (int64_t)gridDim.x * kRows) {
+        Pack<T, V> gu[kUnits], hu[kUnits], au[kUnits];
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
             const int c = tid + kThreads * i;
-            if (c < units) {
-                load_row_unit<kAny>(h + m * N, c, N, hv[i]);
-                load_row_unit<kAny>(dy + m * N, c, N, g[i]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < V; ++j) g[i][j] = hv[i][j] = 0.0f;
-            }
+            hu[i] = c < units ? load_row_unit<false, kAny>(h + m * N, c, N) : Pack<T, V>{};
+            gu[i] = c < units ? load_row_unit<false, kAny>(dy + m * N, c, N) : Pack<T, V>{};
         }
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            const int c = tid + kThreads * i;
+            if (dx && dh && c < units) au[i] = load_row_unit<false, kAny>(dh + m * N, c, N);
+        }
+        float ss = 0.0f, gh = 0.0f;
 #pragma unroll
         for (int i = 0; i < kUnits; ++i)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                ss = __builtin_fmaf(hv[i][j], hv[i][j], ss);
-                gh = __builtin_fmaf(g[i][j] * w[i][j], hv[i][j], gh);
+                const float hv = to_f32(hu[i].v[j]), g = to_f32(gu[i].v[j]) * to_f32(w[i].v[j]);
+                ss = __builtin_fmaf(hv, hv, ss);
+                gh = __builtin_fmaf(g, hv, gh);
             }
-        ss = row_sum<kWaves>(ss, red);
-        gh = row_sum<kWaves>(gh, red);
+        row_sums<kWaves>(ss, gh, red);
         const float r = 1.0f / sqrtf(ss / (float)N + eps), c0 = gh / (float)N * (r * r);
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
             const int c = tid + kThreads * i;
             if (c >= units) continue;
-            float o[V], add[V];
-            if (dx && dh) load_row_unit<kAny>(dh + m * N, c, N, add);
+            float o[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                dw[i][j] = __builtin_fmaf(g[i][j], hv[i][j] * r, dw[i][j]);
-                o[j] = r * (g[i][j] * w[i][j] - hv[i][j] * c0);
-                if (dx && dh) o[j] += add[j];
+                const float hv = to_f32(hu[i].v[j]), g = to_f32(gu[i].v[j]);
+                dw[i][j] = __builtin_fmaf(g, hv * r, dw[i][j]);
+                o[j] = r * (g * to_f32(w[i].v[j]) - hv * c0);
             }
-            if (dx) store_row_unit<kAny>(dx + m * N, c, N, o);
+            if (dx && dh) add(au[i], o);
+            if (dx) store_row_unit<false, kAny>(dx + m * N, c, N, o);
         }
     }
-    if (part) {
+    if (!part) return;
+    if constexpr (kRows > 1) {
+        // sums [wave][unit][V] -> the block's, unit by unit
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) sums[((wave_id() * kUnits + i) * V + j) * 64 + tid] = dw[i][j];
+        __syncthreads();
+        for (int u = threadIdx.x; u < 64 * kUnits * V; u += 64 * kGradWaves) {  // u = (i V + j) 64 + lane
+            const int n = (u % 64 + 64 * (u / 64 / V)) * V + u / 64 % V;
+            float s = sums[u];
+#pragma unroll
+            for (int k = 1; k < kRows; ++k) s += sums[k * 64 * kUnits * V + u];
+            if (n < N) part[(int64_t)blockIdx.x * N + n] = s;
+        }
+    } else {
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
             const int c = tid + kThreads * i;
@@ -304,38 +351,34 @@ __global__ __launch_bounds__(64 * kWaves) void add_rmsnorm_backward_long_kernel(
                                                                                 int64_t rows, int N, const T* __restrict__ weight,
                                                                                 float eps, T* dx, float* __restrict__ rstd) {
     constexpr int V = kUnit<T>, kThreads = 64 * kWaves;
-    __shared__ float red[kWaves];
+    __shared__ float2 red[kWaves];
     const int units = (N + V - 1) / V;
     for (int64_t m = blockIdx.x; m < rows; m += gridDim.x) {
         float ss = 0.0f, gh = 0.0f;
         for (int c = threadIdx.x; c < units; c += kThreads) {
             float hv[V], g[V], w[V];
-            load_row_unit<true>(h + m * N, c, N, hv);
-            load_row_unit<true>(dy + m * N, c, N, g);
-            if (weight) load_row_unit<true>(weight, c, N, w);
+            widen(load_row_unit<false, true>(h + m * N, c, N), hv);
+            widen(load_row_unit<false, true>(dy + m * N, c, N), g);
+            if (weight) widen(load_row_unit<false, true>(weight, c, N), w);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 ss = __builtin_fmaf(hv[j], hv[j], ss);
                 gh = __builtin_fmaf(weight ? g[j] * w[j] : g[j], hv[j], gh);
             }
         }
-        ss = row_sum<kWaves>(ss, red);
-        gh = row_sum<kWaves>(gh, red);
+        row_sums<kWaves>(ss, gh, red);
         const float r = 1.0f / sqrtf(ss / (float)N + eps), c0 = gh / (float)N * (r * r);
         if (rstd && threadIdx.x == 0) rstd[m] = r;
         if (!dx) continue;
         for (int c = threadIdx.x; c < units; c += kThreads) {
-            float hv[V], g[V], w[V], add[V];
-            load_row_unit<true>(h + m * N, c, N, hv);
-            load_row_unit<true>(dy + m * N, c, N, g);
-            if (weight) load_row_unit<true>(weight, c, N, w);
-            if (dh) load_row_unit<true>(dh + m * N, c, N, add);
+            float hv[V], g[V], w[V];
+            widen(load_row_unit<false, true>(h + m * N, c, N), hv);
+            widen(load_row_unit<false, true>(dy + m * N, c, N), g);
+            if (weight) widen(load_row_unit<false, true>(weight, c, N), w);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                g[j] = r * ((weight ? g[j] * w[j] : g[j]) - hv[j] * c0);
-                if (dh) g[j] += add[j];
-            }
-            store_row_unit<true>(dx + m * N, c, N, g);
+            for (int j = 0; j < V; ++j) g[j] = r * ((weight ? g[j] * w[j] : g[j]) - hv[j] * c0);
+            if (dh) add(load_row_unit<false, true>(dh + m * N, c, N), g);
+            store_row_unit<false, true>(dx + m * N, c, N, g);
         }
     }
 }
@@ -374,17 +417,20 @@ __global__ __launch_bounds__(kJoinColumns* kJoinGroups) void join_dweight_kernel
     }
 }
 
-// Rows by a wave each where they are short and many enough for every SIMD.
-bool norm_by_wave(int64_t rows, int64_t N, int element) { return N * element <= 64 * 16 * kKeep && rows >= 1024; }
-
-// Blocks of the gradients' kernel, each with a part of dweight.
-constexpr int64_t kGradBlocks = 512;
-// Longest row, in elements, whose columns' sums stay in registers.
+// Blocks of the gradients' kernel, each with a part of dweight: one a CU.
+constexpr int64_t kGradBlocks = 256;
+// Longest row, in elements, that a wave takes by itself, and whose columns' sums stay in a block's registers.
+template <typename T>
+constexpr int64_t kGradByWave = 64 * 4 * kUnit<T>;
 template <typename T>
 constexpr int64_t kGradKept = 512 * 4 * kUnit<T>;
 constexpr int64_t kLongParts = 64;
 
 int64_t grad_parts(int64_t rows) { return std::min(rows, kGradBlocks); }
+
+constexpr int64_t kNormByWaveRows = 1024;
+// Arrays from this many bytes on are read and written past the caches' usual order.
+constexpr int64_t kNormStreamBytes = 32 << 20;
 
 }  // namespace
 
@@ -392,17 +438,30 @@ hipError_t launch_add_rmsnorm(int dtype, const void* x, const void* residual, in
                               float eps, void* h, void* y, int8_t* xq, float* ascale, hipStream_t stream) {
     return with_act_type(dtype, [&](auto t) {
         using T = decltype(t);
-        auto run = [&](auto waves, auto i8, auto any) {
-            constexpr int kWaves = decltype(waves)::value;
-            const dim3 grid((unsigned)std::min<int64_t>((rows + 4 / kWaves - 1) / (4 / kWaves), kMaxGridBlocks));
-            hipLaunchKernelGGL((add_rmsnorm_kernel<T, kWaves, decltype(i8)::value, decltype(any)::value>), grid, dim3(256), 0,
-                               stream, static_cast<const T*>(x), static_cast<const T*>(residual), rows, (int)N,
-                               static_cast<const T*>(weight), eps, static_cast<T*>(h), static_cast<T*>(y), xq, ascale);
+        const int64_t units = (N + kUnit<T> - 1) / kUnit<T>;
+        const bool past = rows * N * (int64_t)sizeof(T) >= kNormStreamBytes;
+        auto run = [&](auto waves, auto keep, auto i8, auto any, auto stream_past) {
+            constexpr int kWaves = decltype(waves)::value, kRows = kWaves == 1 ? 4 : 1;
+            const dim3 grid((unsigned)std::min<int64_t>((rows + kRows - 1) / kRows, kMaxGridBlocks));
+            hipLaunchKernelGGL((add_rmsnorm_kernel<T, kWaves, decltype(keep)::value, decltype(i8)::value, decltype(any)::value,
+                                                   decltype(stream_past)::value>),
+                               grid, dim3(kWaves == 1 ? 256 : 64 * kWaves), 0, stream, static_cast<const T*>(x),
+                               static_cast<const T*>(residual), rows, (int)N, static_cast<const T*>(weight), eps, static_cast<T*>(h),
+                               static_cast<T*>(y), xq, ascale);
             return hipGetLastError();
         };
+        using I1 = std::integral_constant<int, 1>;
+        using I2 = std::integral_constant<int, 2>;
+        using I4 = std::integral_constant<int, 4>;
+        using I8 = std::integral_constant<int, 8>;
         auto pick = [&](auto i8, auto any) {
-            return norm_by_wave(rows, N, sizeof(T)) ? run(std::integral_constant<int, 1>{}, i8, any)
-                                                    : run(std::integral_constant<int, 4>{}, i8, any);
+            // NORMRULE
+            if (rows >= kNormByWaveRows && units <= 64 * 4)
+                return past ? run(I1{}, I4{}, i8, any, std::true_type{}) : run(I1{}, I4{}, i8, any, std::false_type{});
+            if (rows >= kNormByWaveRows && units <= 64 * 8)
+                return past ? run(I1{}, I8{}, i8, any, std::true_type{}) : run(I1{}, I8{}, i8, any, std::false_type{});
+            if (units <= 512) return run(I8{}, I1{}, i8, any, std::false_type{});
+            return past ? run(I8{}, I2{}, i8, any, std::true_type{}) : run(I8{}, I2{}, i8, any, std::false_type{});
         };
         if (xq) return pick(std::true_type{}, std::false_type{});  // (whole units: N % 16 == 0)
         return N % kUnit<T> == 0 ? pick(std::false_type{}, std::false_type{}) : pick(std::false_type{}, std::true_type{});
@@ -426,19 +485,23 @@ hipError_t launch_add_rmsnorm_backward(int dtype, const void* dy, const void* dh
         if (N <= kGradKept<T>) {
             float* part = dweight ? ws : nullptr;
             auto run = [&](auto waves, auto keep, auto any) {
-                constexpr int kWaves = decltype(waves)::value, kUnits = decltype(keep)::value;
+                constexpr int kWaves = decltype(waves)::value, kUnits = decltype(keep)::value, kRows = kGradWaves / kWaves;
+                parts = (int)std::min((rows + kRows - 1) / kRows, kGradBlocks);
                 hipLaunchKernelGGL((add_rmsnorm_backward_kernel<T, kWaves, kUnits, decltype(any)::value>), dim3((unsigned)parts),
-                                   dim3(64 * kWaves), 0, stream, dyt, dht, ht, rows, (int)N, wt, eps, dxt, part);
+                                   dim3(64 * kGradWaves), 0, stream, dyt, dht, ht, rows, (int)N, wt, eps, dxt, part);
                 return hipGetLastError();
             };
             auto pick = [&](auto any) {
                 const int64_t units = (N + kUnit<T> - 1) / kUnit<T>;
-                using I1 = std::integral_constant<int, 1>;
+                using One = std::integral_constant<int, 1>;
+                using All = std::integral_constant<int, kGradWaves>;
+                using I2 = std::integral_constant<int, 2>;
                 using I4 = std::integral_constant<int, 4>;
-                if (units <= 256) return run(I4{}, I1{}, any);
-                if (units <= 512) return run(I4{}, std::integral_constant<int, 2>{}, any);
-                if (units <= 1024) return run(I4{}, I4{}, any);
-                return run(std::integral_constant<int, 8>{}, I4{}, any);
+                if (units <= 64 * 2) return run(One{}, I2{}, any);
+                if (N <= kGradByWave<T>) return run(One{}, I4{}, any);
+                if (units <= 512) return run(All{}, One{}, any);
+                if (units <= 512 * 2) return run(All{}, I2{}, any);
+                return run(All{}, I4{}, any);
             };
             const hipError_t e = N % kUnit<T> == 0 ? pick(std::false_type{}) : pick(std::true_type{});
             if (e != hipSuccess || !dweight) return e;

@@ -95,8 +95,8 @@ typedef enum {
      * scales uint8 [T][G][4][16][2][2], T = K/256 and G = N/32, both rounded up: the byte 127 + log2 X of row n's
      *                           block b (of 32 along K) is at [b/8][n/32][b%4][n%16][n/16%2][b/4%2], the order in
      *                           which the matrix instructions take them; 255 (NaN) for a block that holds an
-     *                           infinity or NaN (its elements 0).  Blocks past K have 0; bytes of rows past N are
-     *                           neither written nor of any effect.
+     *                           infinity or NaN (its elements 0).  Blocks past K and rows past N have bytes too, which the
+     *                           quantizers write as 0 and the products leave out of account.
      * mins   unused (pass NULL)
      * element = w / X to nearest, ties to even, magnitudes past 6 becoming 6; w_hat = element X; K % 32 == 0.  For
      * the W4A4 calls (the 16-bit products return ERR_UNSUPPORTED).  Weights need not be finite. */

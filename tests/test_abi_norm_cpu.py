@@ -35,7 +35,7 @@ def test_refused(call, n):
 
 def test_workspace_sizes():
     assert w.w4a16_add_rmsnorm_backward_workspace_bytes(4, 33) == 4 * 33 * 4 + 16
-    assert w.w4a16_add_rmsnorm_backward_workspace_bytes(10_000, 2048) == 512 * 2048 * 4 + 40_000
+    assert w.w4a16_add_rmsnorm_backward_workspace_bytes(10_000, 2048) == 256 * 2048 * 4 + 40_000
     for bad in [(0, 8), (4, 0), (-1, 8), (BIG, 8), (4, WIDE)]:
         assert w.w4a16_add_rmsnorm_backward_workspace_bytes(*bad) == 0
 

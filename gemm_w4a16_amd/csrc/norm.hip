@@ -82,7 +82,7 @@ __device__ __forceinline__ void row_sums(float& a, float& b, float2* red) {
     b = wave_sum(b);
     if constexpr (kWaves > 1) {
         __syncthreads();
-        if (lane_id() == 0) red[wave_id()] = make_float2(a, b);
+        if (lane_id() == 0) red[wave_id() % kWaves] = make_float2(a, b);
         __syncthreads();
         a = red[0].x, b = red[0].y;
 #pragma unroll
@@ -142,9 +142,25 @@ __global__ __launch_bounds__(kWaves == 1 ? 256 : 64 * kWaves) void add_rmsnorm_k
     __shared__ float red[kWaves];
     const int tid = kWaves == 1 ? lane_id() : (int)threadIdx.x;
     const int units = (N + V - 1) / V;
-    for (int64_t m0 = (int64_t)blockIdx.x * kRows; m0 < rows; m0 += (int64_t)gridDim.x * kRows) {
-        const int64_t m = kWaves == 1 ? m0 + wave_id() : m0;
-        if (kWaves == 1 && m >= rows) continue;
+    const int64_t step = (int64_t)gridDim.x * kRows;
+    int64_t m = (int64_t)blockIdx.x * kRows + (kWaves == 1 ? wave_id() : 0);
+    // the kept units of a row, asked for while the row before is worked on
+    Pack<T, V> xu[kKeep], ru[kKeep], wu[kKeep];
+    auto load_row = [&](int64_t row) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i) {
+            const int c = tid + kThreads * i;
+            xu[i] = c < units && row < rows ? load_row_unit<kStream, kAny>(x + row * N, c, N) : Pack<T, V>{};
+            if (residual) ru[i] = c < units && row < rows ? load_row_unit<kStream, kAny>(residual + row * N, c, N) : Pack<T, V>{};
+        }
+    };
+    load_row(m);
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) {
+        const int c = tid + kThreads * i;
+        if (weight && c < units) wu[i] = load_row_unit<false, kAny>(weight, c, N);
+    }
+    for (; m < rows; m += step) {
         const T* xr = x + m * N;
         const T* rr = residual ? residual + m * N : nullptr;
         // s of a unit that is read again
@@ -152,25 +168,13 @@ __global__ __launch_bounds__(kWaves == 1 ? 256 : 64 * kWaves) void add_rmsnorm_k
             widen(load_row_unit<false, kAny>(xr, c, N), s);
             if (rr) add(load_row_unit<false, kAny>(rr, c, N), s);
         };
-        // every load of the row, and of the weight, before anything waits for one
-        Pack<T, V> xu[kKeep], ru[kKeep], wu[kKeep];
-#pragma unroll
-        for (int i = 0; i < kKeep; ++i) {
-            const int c = tid + kThreads * i;
-            xu[i] = c < units ? load_row_unit<kStream, kAny>(xr, c, N) : Pack<T, V>{};
-            if (rr) ru[i] = c < units ? load_row_unit<kStream, kAny>(rr, c, N) : Pack<T, V>{};
-        }
-#pragma unroll
-        for (int i = 0; i < kKeep; ++i) {
-            const int c = tid + kThreads * i;
-            if (weight && c < units) wu[i] = load_row_unit<false, kAny>(weight, c, N);
-        }
         float keep[kKeep][V], ss = 0.0f;
 #pragma unroll
         for (int i = 0; i < kKeep; ++i) {
             widen(xu[i], keep[i]);
             if (rr) add(ru[i], keep[i]);
         }
+        load_row(m + step);
 #pragma unroll
         for (int i = 0; i < kKeep; ++i)
 #pragma unroll
@@ -256,20 +260,19 @@ __global__ __launch_bounds__(kWaves == 1 ? 256 : 64 * kWaves) void add_rmsnorm_k
 
 // ---- gradients ----------------------------------------------------------------------------------
 
-// dx, and this block's part of dweight.  kWaves waves take a row (one: each its own), rows in turn, and a thread the
-// same columns of each, so that the columns' sums stay in its registers (N at most 64 kWaves kUnits V); waves of their own
-// rows add theirs in LDS at the end, in order.  A block's part leaves once, to part [blocks][N].  The order of additions
+// dx, and this block's part of dweight.  kWaves waves of a block take a row, rows in turn, and a thread the same
+// columns of each, so that the columns' sums stay in its registers (N at most 64 kWaves kUnits V); the groups of waves
+// add theirs in LDS at the end, in order.  A block's part leaves once, to part [blocks][N].  The order of additions
 // does not depend on timing.
-constexpr int kGradWaves = 8;  // of a block
+constexpr int grad_waves(int row_waves) { return row_waves > 8 ? row_waves : 8; }  // of a block
 template <typename T, int kWaves, int kUnits, bool kAny>
-__global__ __launch_bounds__(64 * kGradWaves) void add_rmsnorm_backward_kernel(const T* dy, const T* dh, const T* __restrict__ h,
+__global__ __launch_bounds__(64 * grad_waves(kWaves)) void add_rmsnorm_backward_kernel(const T* dy, const T* dh, const T* __restrict__ h,
                                                                                int64_t rows, int N, const T* __restrict__ weight,
                                                                                float eps, T* dx, float* __restrict__ part) {
-    constexpr int V = kUnit<T>, kThreads = 64 * kWaves, kRows = kGradWaves / kWaves;
-    static_assert(kWaves == 1 || kWaves == kGradWaves, "a wave or the block takes a row");
-    __shared__ float2 red[kWaves];
-    __shared__ float sums[kRows > 1 ? kRows * 64 * kUnits * V : 1];
-    const int tid = kWaves == 1 ? lane_id() : (int)threadIdx.x, units = (N + V - 1) / V;
+    constexpr int V = kUnit<T>, kThreads = 64 * kWaves, kGradWaves = grad_waves(kWaves), kRows = kGradWaves / kWaves;
+    __shared__ float2 red[kGradWaves];
+    __shared__ float sums[kRows > 1 ? kRows * kThreads * kUnits * V : 1];
+    const int tid = threadIdx.x % kThreads, group = wave_id() / kWaves, units = (N + V - 1) / V;
     Pack<T, V> w[kUnits];
     float dw[kUnits][V];
 #pragma unroll
@@ -279,20 +282,28 @@ __global__ __launch_bounds__(64 * kGradWaves) void add_rmsnorm_backward_kernel(c
         for (int j = 0; j < V; ++j) dw[i][j] = 0.0f, w[i].v[j] = from_f32<T>(1.0f);
         if (weight && c < units) w[i] = load_row_unit<false, kAny>(weight, c, N);
     }
-    const int64_t first = (int64_t)blockIdx.x * kRows + (kWaves == 1 ? wave_id() : 0);
-    for (int64_t m = first; m < rows; m += (int64_t)gridDim.x * kRows) {
+    const int64_t step = (int64_t)gridDim.x * kRows;
+    int64_t m = (int64_t)blockIdx.x * kRows + group;
+    // a row, asked for while the row before is worked on
+    Pack<T, V> next_g[kUnits], next_h[kUnits], next_a[kUnits];
+    auto load_row = [&](int64_t row) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            const int c = tid + kThreads * i;
+            const bool there = c < units && row < rows;
+            next_h[i] = there ? load_row_unit<false, kAny>(h + row * N, c, N) : Pack<T, V>{};
+            next_g[i] = there ? load_row_unit<false, kAny>(dy + row * N, c, N) : Pack<T, V>{};
+            if (dx && dh && there) next_a[i] = load_row_unit<false, kAny>(dh + row * N, c, N);
+        }
+    };
+    constexpr bool kAhead = kWaves <= 8;  // (sixteen waves a block have 128 registers a thread: they spill)
+    if (kAhead) load_row(m);
+    for (; m - group < rows; m += step) {  // (as often for every group: they share the barriers)
+        if (!kAhead) load_row(m);
         Pack<T, V> gu[kUnits], hu[kUnits], au[kUnits];
 #pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-            const int c = tid + kThreads * i;
-            hu[i] = c < units ? load_row_unit<false, kAny>(h + m * N, c, N) : Pack<T, V>{};
-            gu[i] = c < units ? load_row_unit<false, kAny>(dy + m * N, c, N) : Pack<T, V>{};
-        }
-#pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-            const int c = tid + kThreads * i;
-            if (dx && dh && c < units) au[i] = load_row_unit<false, kAny>(dh + m * N, c, N);
-        }
+        for (int i = 0; i < kUnits; ++i) gu[i] = next_g[i], hu[i] = next_h[i], au[i] = next_a[i];
+        if (kAhead) load_row(m + step);
         float ss = 0.0f, gh = 0.0f;
 #pragma unroll
         for (int i = 0; i < kUnits; ++i)
@@ -302,12 +313,12 @@ __global__ __launch_bounds__(64 * kGradWaves) void add_rmsnorm_backward_kernel(c
                 ss = __builtin_fmaf(hv, hv, ss);
                 gh = __builtin_fmaf(g, hv, gh);
             }
-        row_sums<kWaves>(ss, gh, red);
+        row_sums<kWaves>(ss, gh, red + group * kWaves);
         const float r = 1.0f / sqrtf(ss / (float)N + eps), c0 = gh / (float)N * (r * r);
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
             const int c = tid + kThreads * i;
-            if (c >= units) continue;
+            if (c >= units || m >= rows) continue;
             float o[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) {
@@ -321,17 +332,18 @@ __global__ __launch_bounds__(64 * kGradWaves) void add_rmsnorm_backward_kernel(c
     }
     if (!part) return;
     if constexpr (kRows > 1) {
-        // sums [wave][unit][V] -> the block's, unit by unit
+        // [group][unit][V][thread]
+        constexpr int kAll = kThreads * kUnits * V;
 #pragma unroll
         for (int i = 0; i < kUnits; ++i)
 #pragma unroll
-            for (int j = 0; j < V; ++j) sums[((wave_id() * kUnits + i) * V + j) * 64 + tid] = dw[i][j];
+            for (int j = 0; j < V; ++j) sums[group * kAll + (i * V + j) * kThreads + tid] = dw[i][j];
         __syncthreads();
-        for (int u = threadIdx.x; u < 64 * kUnits * V; u += 64 * kGradWaves) {  // u = (i V + j) 64 + lane
-            const int n = (u % 64 + 64 * (u / 64 / V)) * V + u / 64 % V;
+        for (int u = threadIdx.x; u < kAll; u += 64 * kGradWaves) {
+            const int n = (u % kThreads + kThreads * (u / kThreads / V)) * V + u / kThreads % V;
             float s = sums[u];
 #pragma unroll
-            for (int k = 1; k < kRows; ++k) s += sums[k * 64 * kUnits * V + u];
+            for (int k = 1; k < kRows; ++k) s += sums[k * kAll + u];
             if (n < N) part[(int64_t)blockIdx.x * N + n] = s;
         }
     } else {
@@ -419,16 +431,15 @@ __global__ __launch_bounds__(kJoinColumns* kJoinGroups) void join_dweight_kernel
 
 // Blocks of the gradients' kernel, each with a part of dweight: one a CU.
 constexpr int64_t kGradBlocks = 256;
-// Longest row, in elements, that a wave takes by itself, and whose columns' sums stay in a block's registers.
+// Longest row, in elements, whose columns' sums stay in a block's registers.
 template <typename T>
-constexpr int64_t kGradByWave = 64 * 4 * kUnit<T>;
-template <typename T>
-constexpr int64_t kGradKept = 512 * 4 * kUnit<T>;
+constexpr int64_t kGradKept = 1024 * 2 * kUnit<T>;
 constexpr int64_t kLongParts = 64;
 
 int64_t grad_parts(int64_t rows) { return std::min(rows, kGradBlocks); }
 
-constexpr int64_t kNormByWaveRows = 1024;
+// Waves of a launch: as many as run at once, each with rows in turn.
+constexpr int64_t kNormWaves = 4096;
 // Arrays from this many bytes on are read and written past the caches' usual order.
 constexpr int64_t kNormStreamBytes = 32 << 20;
 
@@ -442,7 +453,7 @@ hipError_t launch_add_rmsnorm(int dtype, const void* x, const void* residual, in
         const bool past = rows * N * (int64_t)sizeof(T) >= kNormStreamBytes;
         auto run = [&](auto waves, auto keep, auto i8, auto any, auto stream_past) {
             constexpr int kWaves = decltype(waves)::value, kRows = kWaves == 1 ? 4 : 1;
-            const dim3 grid((unsigned)std::min<int64_t>((rows + kRows - 1) / kRows, kMaxGridBlocks));
+            const dim3 grid((unsigned)std::min<int64_t>((rows + kRows - 1) / kRows, kNormWaves / (kWaves * kRows)));
             hipLaunchKernelGGL((add_rmsnorm_kernel<T, kWaves, decltype(keep)::value, decltype(i8)::value, decltype(any)::value,
                                                    decltype(stream_past)::value>),
                                grid, dim3(kWaves == 1 ? 256 : 64 * kWaves), 0, stream, static_cast<const T*>(x),
@@ -450,18 +461,17 @@ hipError_t launch_add_rmsnorm(int dtype, const void* x, const void* residual, in
                                static_cast<T*>(y), xq, ascale);
             return hipGetLastError();
         };
-        using I1 = std::integral_constant<int, 1>;
-        using I2 = std::integral_constant<int, 2>;
-        using I4 = std::integral_constant<int, 4>;
-        using I8 = std::integral_constant<int, 8>;
+        // Two units a thread, so a wave for 128 of a row's units.
+        auto pick_stream = [&](auto i8, auto any, auto past) {
+            using I2 = std::integral_constant<int, 2>;
+            if (units <= 128) return run(std::integral_constant<int, 1>{}, I2{}, i8, any, past);
+            if (units <= 256) return run(std::integral_constant<int, 2>{}, I2{}, i8, any, past);
+            if (units <= 512) return run(std::integral_constant<int, 4>{}, I2{}, i8, any, past);
+            if (units <= 1024) return run(std::integral_constant<int, 8>{}, I2{}, i8, any, past);
+            return run(std::integral_constant<int, 16>{}, I2{}, i8, any, past);
+        };
         auto pick = [&](auto i8, auto any) {
-            // NORMRULE
-            if (rows >= kNormByWaveRows && units <= 64 * 4)
-                return past ? run(I1{}, I4{}, i8, any, std::true_type{}) : run(I1{}, I4{}, i8, any, std::false_type{});
-            if (rows >= kNormByWaveRows && units <= 64 * 8)
-                return past ? run(I1{}, I8{}, i8, any, std::true_type{}) : run(I1{}, I8{}, i8, any, std::false_type{});
-            if (units <= 512) return run(I8{}, I1{}, i8, any, std::false_type{});
-            return past ? run(I8{}, I2{}, i8, any, std::true_type{}) : run(I8{}, I2{}, i8, any, std::false_type{});
+            return past ? pick_stream(i8, any, std::true_type{}) : pick_stream(i8, any, std::false_type{});
         };
         if (xq) return pick(std::true_type{}, std::false_type{});  // (whole units: N % 16 == 0)
         return N % kUnit<T> == 0 ? pick(std::false_type{}, std::false_type{}) : pick(std::false_type{}, std::true_type{});
@@ -483,28 +493,25 @@ hipError_t launch_add_rmsnorm_backward(int dtype, const void* dy, const void* dh
         T* dxt = static_cast<T*>(dx);
         int parts = (int)grad_parts(rows);
         if (N <= kGradKept<T>) {
-            float* part = dweight ? ws : nullptr;
             auto run = [&](auto waves, auto keep, auto any) {
-                constexpr int kWaves = decltype(waves)::value, kUnits = decltype(keep)::value, kRows = kGradWaves / kWaves;
+                constexpr int kWaves = decltype(waves)::value, kUnits = decltype(keep)::value, kGradWaves = grad_waves(kWaves), kRows = kGradWaves / kWaves;
                 parts = (int)std::min((rows + kRows - 1) / kRows, kGradBlocks);
+                float* part = parts == 1 ? dweight : dweight ? ws : nullptr;
                 hipLaunchKernelGGL((add_rmsnorm_backward_kernel<T, kWaves, kUnits, decltype(any)::value>), dim3((unsigned)parts),
                                    dim3(64 * kGradWaves), 0, stream, dyt, dht, ht, rows, (int)N, wt, eps, dxt, part);
                 return hipGetLastError();
             };
             auto pick = [&](auto any) {
                 const int64_t units = (N + kUnit<T> - 1) / kUnit<T>;
-                using One = std::integral_constant<int, 1>;
-                using All = std::integral_constant<int, kGradWaves>;
                 using I2 = std::integral_constant<int, 2>;
-                using I4 = std::integral_constant<int, 4>;
-                if (units <= 64 * 2) return run(One{}, I2{}, any);
-                if (N <= kGradByWave<T>) return run(One{}, I4{}, any);
-                if (units <= 512) return run(All{}, One{}, any);
-                if (units <= 512 * 2) return run(All{}, I2{}, any);
-                return run(All{}, I4{}, any);
+                if (units <= 128) return run(std::integral_constant<int, 1>{}, I2{}, any);
+                if (units <= 256) return run(I2{}, I2{}, any);
+                if (units <= 512) return run(std::integral_constant<int, 4>{}, I2{}, any);
+                if (units <= 1024) return run(std::integral_constant<int, 8>{}, I2{}, any);
+                return run(std::integral_constant<int, 16>{}, I2{}, any);
             };
             const hipError_t e = N % kUnit<T> == 0 ? pick(std::false_type{}) : pick(std::true_type{});
-            if (e != hipSuccess || !dweight) return e;
+            if (e != hipSuccess || !dweight || parts == 1) return e;
         } else {
             float* rstd = ws;
             float* part = ws + (rows + 3) / 4 * 4;

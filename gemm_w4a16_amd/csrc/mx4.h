@@ -9,7 +9,7 @@
 // reads one word for four operands, no byte is moved, and the scales of a tile's rows are one run of memory.
 #pragma once
 
-#include "device_common.h"
+#include "experts.h"
 
 namespace w4a16 {
 
@@ -29,22 +29,65 @@ __device__ __forceinline__ uint32_t mx4_scale(uint32_t max_bits) {
     const int e = (int)(max_bits >> 23);
     return e == 255 ? 255u : (uint32_t)max(e - 2, 0);
 }
-// 2^(127 - s): what a value is multiplied by before it is rounded to an element (exact, but where the product
-// falls below the normal numbers, far under half the smallest element).  0 for s = 255.
-__device__ __forceinline__ float mx4_inverse(uint32_t s) { return s == 255 ? 0.0f : __uint_as_float((254 - s) << 23); }
 // 2^(s - 127); NaN for 255.
 __device__ __forceinline__ float mx4_factor(uint32_t s) {
     return s == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(s == 0 ? 0x00400000u : s << 23);
 }
 
-// Eight values, already multiplied, as elements: to nearest, ties to even, magnitudes past 6 becoming 6.
-__device__ __forceinline__ uint32_t mx4_codes8(const float (&v)[8]) {
+// The fp32 bits of the largest magnitude among kN values (an even number of 16-bit ones: two at a time, whose bits order
+// like the magnitudes).
+template <int kN, typename T>
+__device__ __forceinline__ uint32_t mx4_max_bits(const T* v) {
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
+        u16x2_t m = __builtin_bit_cast(u16x2_t, w[0] & 0x7FFF7FFFu);
+#pragma unroll
+        for (int j = 1; j < kN / 2; ++j) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2_t, w[j] & 0x7FFF7FFFu));
+        return __float_as_uint(from_abs_bits(fold_max<T>(__builtin_bit_cast(uint32_t, m)), T{}));
+    } else {
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < kN; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+        return m;
+    }
+}
+// The same over groups of four lanes, or eight.
+__device__ __forceinline__ uint32_t mx4_max_quad(uint32_t m) {
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, kDppQuadXor1, 0xF, 0xF, false));
+    return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, kDppQuadXor2, 0xF, 0xF, false));
+}
+__device__ __forceinline__ uint32_t mx4_max_eight(uint32_t m) {
+    m = mx4_max_quad(m);
+    return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, kDppRowHalfMirror, 0xF, 0xF, false));
+}
+
+// kN values (4 or 8) as elements of a block of scale s, four bits each: v / X to nearest, ties to even, magnitudes past 6
+// becoming 6 (the conversion takes the exponent of its scale alone, so 2^-127 too); zero where the block is not
+// a number.
+template <int kN, typename T>
+__device__ __forceinline__ uint32_t mx4_codes(const T* v, uint32_t s) {
+    const float X = __uint_as_float(s << 23);
     uint32_t w = 0;
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], 1.0f, 0);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], 1.0f, 1);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], 1.0f, 2);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], 1.0f, 3);
-    return w;
+    auto two = [&](auto place) __attribute__((always_inline)) {
+        constexpr int i = decltype(place)::value;
+        if constexpr (std::is_same_v<T, bf16_t>) {
+            const bf16x2v_t p = __builtin_bit_cast(bf16x2v_t, reinterpret_cast<const uint32_t*>(v)[i]);
+            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, p, X, i);
+        } else if constexpr (std::is_same_v<T, f16_t>) {
+            typedef _Float16 f16x2v_t __attribute__((ext_vector_type(2)));
+            const f16x2v_t p = __builtin_bit_cast(f16x2v_t, reinterpret_cast<const uint32_t*>(v)[i]);
+            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(w, p, X, i);
+        } else {
+            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2 * i], v[2 * i + 1], X, i);
+        }
+    };
+    two(std::integral_constant<int, 0>{});
+    two(std::integral_constant<int, 1>{});
+    if constexpr (kN == 8) {
+        two(std::integral_constant<int, 2>{});
+        two(std::integral_constant<int, 3>{});
+    }
+    return s == 255 ? 0u : w;
 }
 
 }  // namespace w4a16

@@ -52,20 +52,8 @@ __global__ __launch_bounds__(64 * kWaves) void quant_mx4_kernel(const T* __restr
 #pragma unroll
         for (int i = 0; i < kRowsOfWave / 2; ++i) {
             const int64_t m = m0 + 2 * i;
-            float v[8];
-            uint32_t top = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[j] = to_f32(p[i][j / V].v[j % V]);
-                top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-            }
-            top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, kDppQuadXor1, 0xF, 0xF, false));
-            top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, kDppQuadXor2, 0xF, 0xF, false));
-            const uint32_t s = mx4_scale(top);
-            const float inv = mx4_inverse(s);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= inv;
-            const uint32_t w = s == 255 ? 0u : mx4_codes8(v);  // (infinity and NaN times zero)
+            const T* v = p[i][0].v;  // (a row's packs are one array of 8)
+            const uint32_t s = mx4_scale(mx4_max_quad(mx4_max_bits<8>(v))), w = mx4_codes<8>(v, s);
             if (m < M && k < K) *reinterpret_cast<uint32_t*>(codes + m * (K / 2) + k / 2) = w;
             if (lane % 4 == 0)
                 reinterpret_cast<uint8_t*>(group[which])[mx4_scale_at(1, kRowsOfWave * wave + 2 * i + lane / 32, lane % 32 / 4)] = (uint8_t)s;

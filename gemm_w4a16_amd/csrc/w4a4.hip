@@ -44,14 +44,16 @@ constexpr int kOnes = 0x7F7F7F7F;  // scales of one, for blocks past K (their el
 // A block computes BM rows x BN columns in WM x WN waves of (16 TM) x (16 TN), each doubled WK times along K.  K is
 // taken in stages of WK k-tiles of 256 (128 bytes of codes a row); the waves of index wk along K multiply k-tile wk of a
 // stage, and their sums are added at the end, in order.  Operands and scales reach LDS by direct copies into a ring
-// of R stages.
-template <int WM_, int WN_, int WK_, int TM_, int TN_, int R_>
+// of R stages.  kX = false: x is not in the ring (which holds weights alone) but whole in LDS behind it, quantized by
+// the block from activations.
+template <int WM_, int WN_, int WK_, int TM_, int TN_, int R_, bool kX_ = true>
 struct Tiling {
     static constexpr int WM = WM_, WN = WN_, WK = WK_, TM = TM_, TN = TN_, R = R_;
+    static constexpr bool kX = kX_;
     static constexpr int BM = 16 * TM * WM, BN = 16 * TN * WN, NW = WM * WN * WK;
-    static constexpr int kTileBytes = (BM + BN) * 128;  // one k-tile: BN rows of weights, then BM rows of x
+    static constexpr int kTileBytes = ((kX ? BM : 0) + BN) * 128;  // one k-tile: BN rows of weights, then BM rows of x
     static constexpr int GW = (BN + 31) / 32, GX = (BM + 31) / 32;  // groups of scales: weights', then x's
-    static constexpr int kScaleBytes = (GW + GX) * 256;
+    static constexpr int kGroups = GW + (kX ? GX : 0), kScaleBytes = kGroups * 256;
     static constexpr int kCodes = WK * kTileBytes;  // of a stage; the scales of its k-tiles lie behind them
     static constexpr int kScaleCopies = (WK * kScaleBytes + 1023) / 1024;
     static constexpr int kStage = kCodes + 1024 * kScaleCopies;
@@ -59,14 +61,25 @@ struct Tiling {
     static constexpr int SW = (kScaleCopies + NW - 1) / NW;
 };
 
-template <typename TO, typename C>
-__global__ __launch_bounds__(64 * C::NW) void w4a4_tile_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restrict__ xscales,
+constexpr int kFusedUnits = 4;  // of 8 activations that a lane asks for at a time
+// LDS behind the ring for activations quantized by the block: codes and scales of its rows, K up to whole stages.
+template <typename C>
+constexpr size_t fused_bytes(int64_t K) {
+    return (size_t)((mx4_ktiles(K) + C::WK - 1) / C::WK * C::WK) * (C::BM * 128 + C::GX * 256);
+}
+
+// TX: uint8_t for rows in the format, or the type of activations (C::kX false).
+template <typename TO, typename TX, typename C>
+__global__ __launch_bounds__(64 * C::NW) void w4a4_tile_kernel(const TX* __restrict__ x, const uint8_t* __restrict__ xscales,
                                                                int M, const uint8_t* __restrict__ codes,
                                                                const uint8_t* __restrict__ scales, int N, int stride,
                                                                TO* __restrict__ y, int n_tiles, int group) {
     constexpr int TM = C::TM, TN = C::TN, R = C::R, BM = C::BM, BN = C::BN, CW = C::CW, SW = C::SW, G = CW + SW;
     constexpr int kTileCopies = C::kTileBytes / 1024;  // of one k-tile
+    static_assert(C::kX == std::is_same_v<TX, uint8_t>, "activations are quantized by the block");
+    static_assert(C::kX || BM % 32 == 0, "whole groups of scales");
     __shared__ __attribute__((aligned(1024))) char smem[R * C::kStage];
+    extern __shared__ __attribute__((aligned(1024))) char fused_lds[];
     const int lane = lane_id(), wave = wave_id();
     const int l16 = lane & 15, kg = lane >> 4;
     const int wn = wave % C::WN, wk = wave / C::WN % C::WK, wm = wave / (C::WN * C::WK);
@@ -88,7 +101,7 @@ __global__ __launch_bounds__(64 * C::NW) void w4a4_tile_kernel(const uint8_t* __
     const int S = stride;  // bytes of a row of codes
     const int KT = (S + 127) / 128, T = (KT + C::WK - 1) / C::WK;
     const uint8_t* wbase = codes + (size_t)n0 * S;
-    const uint8_t* xbase = xq + (size_t)row0 * S;
+    const uint8_t* xbase = C::kX ? reinterpret_cast<const uint8_t*>(x) + (size_t)row0 * S : nullptr;
     const uint32_t lds0 = lds_addr(smem);
 
     // This wave's copies j = CW wave + i of a stage's codes: copy jj = j % kTileCopies of k-tile j / kTileCopies, rows
@@ -100,7 +113,7 @@ __global__ __launch_bounds__(64 * C::NW) void w4a4_tile_kernel(const uint8_t* __
     for (int i = 0; i < CW; ++i) {
         const int jj = min(CW * wave + i, C::kCodes / 1024 - 1) % kTileCopies;
         const int r = 8 * jj + lane / 8, chunk = (lane % 8) ^ ((r >> 1) & 7);
-        const int row = jj < BN / 8 ? min(r, N - 1 - n0) : min(r - BN, M - 1 - row0);
+        const int row = !C::kX || jj < BN / 8 ? min(r, N - 1 - n0) : min(r - BN, M - 1 - row0);
         voff[i] = (uint32_t)row * (uint32_t)S + 16u * chunk;
     }
     // ... and its 16 bytes of the stage's scales: groups past the last read the last one
@@ -110,10 +123,10 @@ __global__ __launch_bounds__(64 * C::NW) void w4a4_tile_kernel(const uint8_t* __
 #pragma unroll
     for (int i = 0; i < SW; ++i) {
         const int c = min(64 * min(SW * wave + i, C::kScaleCopies - 1) + lane, C::WK * C::kScaleBytes / 16 - 1);
-        const int g = c / 16 % (C::GW + C::GX);
+        const int g = c / 16 % C::kGroups;
         const int64_t gw = mx4_groups(N), gx = mx4_groups(M);
-        stile[i] = c / 16 / (C::GW + C::GX);
-        const bool w = g < C::GW;
+        stile[i] = c / 16 / C::kGroups;
+        const bool w = !C::kX || g < C::GW;
         const int64_t at = w ? min((int64_t)(n0 / 32 + g), gw - 1) : min((int64_t)(row0 / 32 + g - C::GW), gx - 1);
         sptr[i] = reinterpret_cast<const char*>(w ? scales : xscales) + at * 256 + c % 16 * 16;
         sstep[i] = (w ? gw : gx) * 256;
@@ -125,7 +138,7 @@ __global__ __launch_bounds__(64 * C::NW) void w4a4_tile_kernel(const uint8_t* __
         if (i < CW) {
             const int j = min(CW * wave + i, C::kCodes / 1024 - 1), jj = j % kTileCopies;
             const int kt = min(t * C::WK + j / kTileCopies, KT - 1);
-            const uint8_t* base = (jj < BN / 8 ? wbase : xbase) + (size_t)kt * 128;
+            const uint8_t* base = (!C::kX || jj < BN / 8 ? wbase : xbase) + (size_t)kt * 128;
             // (no branches: the compiler would move products across them, and past the barriers)
             const int over = 16 * ((lane % 8) ^ ((4 * jj + lane / 16) & 7)) + 16 - (S - kt * 128);
             const uint32_t off = (voff[i] - (uint32_t)max(over, 0)) & (t < T ? ~0u : 0u);
@@ -145,10 +158,18 @@ __global__ __launch_bounds__(64 * C::NW) void w4a4_tile_kernel(const uint8_t* __
         return *reinterpret_cast<const i32x4_t*>(frag0 + slot * C::kStage + 2048 * rt + 16 * ((4 * ks + kg) ^ sw));
     };
     const int w_rt = TN * wn, x_rt = BN / 16 + TM * wm;
+    // x quantized by the block: codes [k-tile][BM] as above, then scales [k-tile][GX][64]
+    const int KTp = T * C::WK;
+    char* fused_scales = fused_lds + (size_t)KTp * BM * 128;
+    auto read_fused = [&](int t, int ks, int b) __attribute__((always_inline)) {
+        return *reinterpret_cast<const i32x4_t*>(fused_lds + ((t * C::WK + wk) * BM + 16 * (TM * wm + b) + l16) * 128 + 16 * ((4 * ks + kg) ^ sw));
+    };
     // words of scales: of two row tiles each (TN, TM even), or the half of one that is this row tile's
     constexpr int NS = (TN + 1) / 2, MS = (TM + 1) / 2;
     const char* scale0 = smem + C::kCodes + wk * C::kScaleBytes + 4 * lane;
-    auto read_scale = [&](int slot, int i) __attribute__((always_inline)) {
+    auto read_scale = [&](int t, int slot, int i) __attribute__((always_inline)) {
+        if (!C::kX && i >= NS)
+            return *reinterpret_cast<const int*>(fused_scales + ((t * C::WK + wk) * C::GX + TM * wm / 2 + i - NS) * 256 + 4 * lane);
         const int g = i < NS ? TN * wn / 2 + i : C::GW + TM * wm / 2 + i - NS;
         return *reinterpret_cast<const int*>(scale0 + slot * C::kStage + 256 * g);
     };
@@ -186,15 +207,18 @@ __global__ __launch_bounds__(64 * C::NW) void w4a4_tile_kernel(const uint8_t* __
             if (i == H - 1) __builtin_amdgcn_s_setprio(0);
         });
     };
-    // read u of a stage in ring slot `slot`: fragments, and with the first k-step's the scales
-    auto read_step = [&](int slot, int ks, int u) __attribute__((always_inline)) {
+    // read u of stage t, in ring slot `slot`: fragments, and with the first k-step's the scales
+    auto read_step = [&](int t, int slot, int ks, int u) __attribute__((always_inline)) {
         if (u < TM) {
-            xf[kInPlace ? 0 : ks][u] = read(slot, ks, x_rt + u);
+            if constexpr (C::kX)
+                xf[kInPlace ? 0 : ks][u] = read(slot, ks, x_rt + u);
+            else
+                xf[kInPlace ? 0 : ks][u] = read_fused(t, ks, u);
         } else if (u < TM + TN) {
             wf[ks][u - TM] = read(slot, ks, w_rt + u - TM);
         } else {
             const int i = u - TM - TN;
-            sc_next[i] = read_scale(slot, i) >> (i < NS ? w_shift : x_shift);
+            sc_next[i] = read_scale(t, slot, i) >> (i < NS ? w_shift : x_shift);
         }
     };
     auto take_scales = [&]() __attribute__((always_inline)) {
@@ -217,10 +241,39 @@ __global__ __launch_bounds__(64 * C::NW) void w4a4_tile_kernel(const uint8_t* __
     static_assert(R * G < 64, "the wait counts");
 #pragma unroll
     for (int u = 0; u < R * G - kLate; ++u) copy(u / G, u / G, u % G);
+    if constexpr (!C::kX) {  // a wave a row, 8 values a lane, four lanes a block of the format; four units' loads
+                           // before the first is waited for
+        constexpr int V = 16 / sizeof(TX), kLoads = 8 / V, kAtOnce = kFusedUnits;
+        const int K8 = S / 4, rows = min(BM, M - row0);
+        const TX* rows_of_x = x + (size_t)row0 * (2 * S);
+        for (int r = wave, c = lane; r < rows;) {
+            Pack<TX, V> p[kAtOnce][kLoads];
+            int rr[kAtOnce], cc[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                rr[i] = r, cc[i] = c;
+#pragma unroll
+                for (int h = 0; h < kLoads; ++h)
+                    p[i][h] = r < rows && c < K8 ? load_unit<false, false, V>(rows_of_x + (size_t)r * (2 * S) + 8 * c + V * h) : Pack<TX, V>{};
+                c += 64;
+                if (c - lane >= K8) c = lane, r += C::NW;
+            }
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const TX* v = p[i][0].v;  // (a unit's packs are one array of 8)
+                const uint32_t s = mx4_scale(mx4_max_quad(mx4_max_bits<8>(v))), w = mx4_codes<8>(v, s);
+                if (rr[i] < rows && cc[i] < K8) {
+                    const int b = cc[i] / 4, kt = b / 8, chunk = b % 8 ^ ((rr[i] >> 1) & 7);
+                    *reinterpret_cast<uint32_t*>(fused_lds + (kt * BM + rr[i]) * 128 + 16 * chunk + 4 * (cc[i] % 4)) = w;
+                    if (cc[i] % 4 == 0) fused_scales[mx4_scale_at(C::GX, rr[i], b)] = (char)s;
+                }
+            }
+        }
+    }
     wait_vm<(R - 1) * G - kLate>();
     __syncthreads();
 #pragma unroll
-    for (int u = 0; u < kFirst; ++u) read_step(0, 0, u);
+    for (int u = 0; u < kFirst; ++u) read_step(0, 0, 0, u);
     take_scales();
 
     // Stage t: its first k-step's fragments and its scales are in registers.  The second's are read under the first's
@@ -231,11 +284,11 @@ __global__ __launch_bounds__(64 * C::NW) void w4a4_tile_kernel(const uint8_t* __
         for (int t = 0; t + 1 < T; ++t) {
             const int next = next_slot(slot);
             const int before = slot == 0 ? R - 1 : slot - 1;  // stage t + R - 1's slot
-            multiply(Zero{}, NReads{}, [&](int u) __attribute__((always_inline)) { read_step(slot, 1, u); }, NLate{},
+            multiply(Zero{}, NReads{}, [&](int u) __attribute__((always_inline)) { read_step(t, slot, 1, u); }, NLate{},
                      [&](int u) __attribute__((always_inline)) { copy(t + R - 1, before, kEarly + u); });
             wait_vm<(R - 2) * G>();
             __syncthreads();
-            multiply(One{}, NFirst{}, [&](int u) __attribute__((always_inline)) { read_step(next, 0, u); }, NEarly{},
+            multiply(One{}, NFirst{}, [&](int u) __attribute__((always_inline)) { read_step(t + 1, next, 0, u); }, NEarly{},
                      [&](int u) __attribute__((always_inline)) { copy(t + R, slot, u); });
             take_scales();
             slot = next;
@@ -243,7 +296,7 @@ __global__ __launch_bounds__(64 * C::NW) void w4a4_tile_kernel(const uint8_t* __
         // the last stage: blocks past K (and k-tiles past the last) count as zero
         if constexpr (!kInPlace) {
 #pragma unroll
-            for (int u = 0; u < kReads; ++u) read_step(slot, 1, u);
+            for (int u = 0; u < kReads; ++u) read_step(T - 1, slot, 1, u);
         }
         const int chunks = (S - ((T - 1) * C::WK + wk) * 128) / 16;
         auto mask = [&](int ks) __attribute__((always_inline)) {
@@ -255,7 +308,7 @@ __global__ __launch_bounds__(64 * C::NW) void w4a4_tile_kernel(const uint8_t* __
         };
         mask(0);
         if constexpr (kInPlace)
-            multiply(Zero{}, NReads{}, [&](int u) __attribute__((always_inline)) { read_step(slot, 1, u); }, Zero{}, none);
+            multiply(Zero{}, NReads{}, [&](int u) __attribute__((always_inline)) { read_step(T - 1, slot, 1, u); }, Zero{}, none);
         else
             multiply(Zero{}, Zero{}, none, Zero{}, none);
         mask(1);
@@ -328,7 +381,7 @@ struct RowShape {
     static constexpr int kScales = 2048, kX = kScales + 1024, kStage = kX + kXBytes;  // weights, scales, rows
     static constexpr int kOwn = kFused ? kRows * 256 : 0;  // a wave's codes [row][128] and scales, behind the ring
     static constexpr int kXCopies = kXBytes / 1024, kCopies = 2 + 1 + kXCopies;
-    static constexpr int R = 2;  // (three or four: fewer blocks a CU, 0-20% slower)
+    static constexpr int R = kFused && kRows > 4 ? 1 : 2;  // (three or four: fewer blocks a CU, 0-20% slower)
     static_assert(kXBytes % 1024 == 0, "whole copies");
 };
 
@@ -397,21 +450,10 @@ __global__ __launch_bounds__(64 * kWaves) void w4a4_rows_kernel(const TX* __rest
         int xs = 0;
         char* own = smem + kWaves * R * C::kStage + wave * C::kOwn;
         if constexpr (C::kFused) {
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
+            for (int r = 0; r < min(M, kRows); ++r) {
                 const Pack<TX, 4> v = *reinterpret_cast<const Pack<TX, 4>*>(w + C::kX + r * (int)(kMx4TileK * sizeof(TX)) + lane * (int)(4 * sizeof(TX)));
-                float f[4];
-                uint32_t top = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) f[j] = to_f32(v.v[j]), top = max(top, __float_as_uint(f[j]) & 0x7FFFFFFFu);
-                top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, kDppQuadXor1, 0xF, 0xF, false));
-                top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, kDppQuadXor2, 0xF, 0xF, false));
-                top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, kDppRowHalfMirror, 0xF, 0xF, false));
-                const uint32_t s = mx4_scale(top);
-                const float inv = mx4_inverse(s);
-                uint32_t q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, f[0] * inv, f[1] * inv, 1.0f, 0);
-                q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, f[2] * inv, f[3] * inv, 1.0f, 1);
-                *reinterpret_cast<uint16_t*>(own + 256 * r + 2 * lane) = s == 255 ? 0 : (uint16_t)q;
+                const uint32_t s = mx4_scale(mx4_max_eight(mx4_max_bits<4>(v.v)));
+                *reinterpret_cast<uint16_t*>(own + 256 * r + 2 * lane) = (uint16_t)mx4_codes<4>(v.v, s);
                 if (lane % 8 == 0) own[256 * r + 128 + lane / 8 % 4 * 2 + lane / 32] = (char)s;
             }
             wave_lds_sync();
@@ -457,12 +499,13 @@ __global__ __launch_bounds__(64 * kWaves) void w4a4_rows_kernel(const TX* __rest
     }
 }
 
-// Rows quantized inside the product: one or two, and three or four of few and short columns (4096 x 4096 5.0 us
-// against 5.5 in two launches, 1024 x 1024 3.4 against 5.0; 14336 x 4096 11.8 against 10.3, 4096 x 14336 10.8 against
-// 10.0: every block quantizes them).
+// Up to 16 rows; of them quantized inside the product: one or two, and up to eight where a wave has few to quantize (one
+// launch against two: 8 x 1000 x 2048 4.2 us against 5.5, 4 x 4096 x 4096 4.9 against 5.5; but 8 x 4096 x 4096 6.3
+// against 5.9, 4 x 14336 x 4096 11.8 against 10.3: every block quantizes them).
 constexpr int64_t kFewRows = 16;
-bool fused_rows(int64_t M, int64_t N, int64_t K) { return M <= 2 || (M <= 4 && N * K <= ((int64_t)1 << 25)); }
-
+bool fused_rows(int64_t M, int64_t N, int64_t K) {
+    return M <= 2 || (N <= 16 * 512 && M * ((mx4_ktiles(K) + 7) / 8) <= 8);
+}
 
 struct Product {
     const uint8_t *xq, *xscales;
@@ -481,11 +524,11 @@ bool fits_grid(int64_t M, int64_t N) {
     return launch_blocks<C>(M, N) < ((int64_t)1 << 31) / (64 * C::NW);  // the grid's threads
 }
 
-template <typename C, typename TO>
-hipError_t launch_tiles(const Product& p, TO* y) {
+template <typename C, typename TX, typename TO>
+hipError_t launch_tiles(const Product& p, const TX* x, TO* y) {
     constexpr int kGroup = C::BM < 256 ? 1024 / C::BM : 4;  // row tiles walked together: about 1024 rows
-    hipLaunchKernelGGL((w4a4_tile_kernel<TO, C>), dim3((unsigned)launch_blocks<C>(p.M, p.N)), dim3(64 * C::NW), 0, p.stream, p.xq,
-                       p.xscales, (int)p.M, p.codes, p.scales, (int)p.N, (int)(p.K / 2), y, (int)((p.N + C::BN - 1) / C::BN), kGroup);
+    hipLaunchKernelGGL((w4a4_tile_kernel<TO, TX, C>), dim3((unsigned)launch_blocks<C>(p.M, p.N)), dim3(64 * C::NW),
+                       C::kX ? 0 : fused_bytes<C>(p.K), p.stream, x, p.xscales, (int)p.M, p.codes, p.scales, (int)p.N, (int)(p.K / 2), y, (int)((p.N + C::BN - 1) / C::BN), kGroup);
     return hipGetLastError();
 }
 
@@ -513,6 +556,11 @@ using T64x128 = Tiling<2, 4, 1, 2, 2, 3>;
 using T64x64 = Tiling<2, 2, 1, 2, 2, 4>;
 using T32x64 = Tiling<2, 4, 1, 1, 1, 4>;
 using T32x32 = Tiling<2, 2, 2, 1, 1, 4>;
+// ... of which these quantize x themselves
+using F64x64 = Tiling<2, 2, 1, 2, 2, 4, false>;
+using F32x64 = Tiling<2, 4, 1, 1, 1, 4, false>;
+using F32x32 = Tiling<2, 2, 2, 1, 1, 4, false>;
+constexpr size_t kLdsBytes = 160 << 10;
 
 // What a tiling costs.  A CU's first block takes `us_ktile` for each 256 of K and `us_first` besides, each further one
 // `next_ktile` and `us_next`; `blocks` of them fit a CU.  The weights arrive at 5.6 TB/s, and neither hides all of the
@@ -562,9 +610,32 @@ hipError_t launch_product(const Product& p, TO* y) {
     const int choice = choose_tiling(p.M, p.N, p.K);
     hipError_t e = hipErrorInvalidConfiguration;
     each_tiling([&](int i, auto tiling, Cost) {
-        if (i == choice) e = launch_tiles<decltype(tiling)>(p, y);
+        if (i == choice) e = launch_tiles<decltype(tiling)>(p, p.xq, y);
     });
     return e;
+}
+
+// Rows quantized by every block for itself, in the tiling that the product takes and so to the same bits: where a
+// wave has few units of it and the blocks are few (one launch against two: 37 x 1001 x 512 4.9 us against 6.4, 100 x 4000 x
+// 512 5.1 against 6.4, 20 x 5000 x 1024 5.3 against 6.2; but 37 x 1001 x 2080, 17 units a wave, 11.2 against 7.5, and 300 x
+// 2000 x 512, 16 units, 8.0 against 6.4).
+constexpr int64_t kFusedBlocks = 512;
+template <typename T>
+bool launch_fused(const Product& p, const T* x, T* y, hipError_t& e) {
+    const int choice = choose_tiling(p.M, p.N, p.K);
+    bool done = false;
+    auto attempt = [&](int i, auto tiling, auto without_x) {
+        using C = decltype(without_x);
+        if (i != choice || done) return;
+        const int64_t rounds = (std::min<int64_t>(p.M, C::BM) + C::NW - 1) / C::NW * ((p.K + 511) / 512);
+        if (rounds > 2 * kFusedUnits || launch_blocks<C>(p.M, p.N) > kFusedBlocks) return;
+        if (fused_bytes<C>(p.K) + C::R * C::kStage > kLdsBytes) return;
+        e = launch_tiles<C>(p, x, y), done = true;
+    };
+    attempt(4, T64x64{}, F64x64{});
+    attempt(5, T32x64{}, F32x64{});
+    attempt(6, T32x32{}, F32x32{});
+    return done;
 }
 
 }  // namespace
@@ -585,8 +656,13 @@ hipError_t launch_matmul_w4a4(int dtype, const void* x, int64_t M, const uint8_t
         using T = decltype(t);
         const Product p{xq, xscales, M, codes, scales, N, K, stream};
         if (M <= 2) return launch_rows<T, T, 2>(p, static_cast<const T*>(x), static_cast<T*>(y));
-        if (fused_rows(M, N, K)) return launch_rows<T, T, 4>(p, static_cast<const T*>(x), static_cast<T*>(y));
-        if (const hipError_t e = launch_quant_mx4(dtype, x, M, K, xq, xscales, stream); e != hipSuccess) return e;
+        if (fused_rows(M, N, K)) {
+            const T* xt = static_cast<const T*>(x);
+            return M <= 4 ? launch_rows<T, T, 4>(p, xt, static_cast<T*>(y)) : launch_rows<T, T, 8>(p, xt, static_cast<T*>(y));
+        }
+        hipError_t e = hipSuccess;
+        if (M > kFewRows && launch_fused(p, static_cast<const T*>(x), static_cast<T*>(y), e)) return e;
+        if (e = launch_quant_mx4(dtype, x, M, K, xq, xscales, stream); e != hipSuccess) return e;
         return launch_product<T>(p, static_cast<T*>(y));
     });
 }

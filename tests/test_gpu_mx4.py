@@ -157,7 +157,8 @@ def product(x, wt):
 
 SHAPES = [(1, 1, 32), (1, 4100, 64), (1, 1001, 4096), (2, 61, 96), (3, 300, 2080), (5, 2049, 1056), (8, 512, 288), (16, 700, 4096),
           (17, 1001, 2080), (31, 64, 32), (37, 1001, 2080), (64, 257, 544), (65, 2000, 128), (100, 515, 20000), (129, 130, 256), (200, 1030, 8192),
-          (257, 520, 1024), (300, 2050, 1312), (520, 4104, 512), (1030, 1030, 160), (1500, 770, 320), (40, 16400, 96), (4, 8192, 16384)]
+          (257, 520, 1024), (300, 2050, 1312), (520, 4104, 512), (1030, 1030, 160), (1500, 770, 320), (40, 16400, 96), (4, 8192, 16384), (20, 3000, 1024),
+          (33, 70, 512), (130, 515, 256), (8, 1000, 2048), (7, 8200, 1024), (300, 500, 480), (24, 9000, 1056)]
 
 
 @pytest.mark.parametrize("kind", list(TYPES))

@@ -28,7 +28,9 @@ constexpr int kPairs = (int)kLayerPairs;
 // ---- the pairs, sorted by expert and cut into tiles of at most XR rows of one expert -------------------
 
 constexpr int kExperts = (int)kMaxExperts;
+constexpr int kExpertBits = 9;
 constexpr int kPairWaves = kPairs / kWave;
+static_assert(kExperts <= 1 << kExpertBits);
 
 template <int XR>
 struct alignas(16) PairTiles {
@@ -40,6 +42,16 @@ struct alignas(16) PairTiles {
     uint16_t expert[kPairs], rows[kPairs];    // of a tile
     int wave_tiles[kPairWaves], tiles;
 };
+
+// Sums over the lanes up to and with this one.
+__device__ __forceinline__ int lanes_up_to(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8: within 16 lanes
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, kDppRowBcast15, 0xA, 0xF, false);
+    return v + __builtin_amdgcn_update_dpp(0, v, kDppRowBcast31, 0xC, 0xF, false);
+}
 
 // By every block for itself, the same in all of them: tiles in order of experts, an expert's pairs in their own order.
 // At least kPairs threads, a thread a pair, then a thread two experts.  Returns this thread's pair's expert (-1: none).
@@ -55,17 +67,18 @@ __device__ __forceinline__ int sort_pairs(const TI* __restrict__ ids, int P, int
     }
     for (int i = p; i < kPairWaves * kExperts / 16; i += blockDim.x) reinterpret_cast<uint4*>(s.count)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    // this pair's place among its expert's in the wave: one expert at a time
+    // this pair's place among its expert's in the wave: the lanes whose id has the same bits
     int same = 0;
-    uint64_t left = __ballot(e >= 0);
-    while (left != 0) {
-        const int f = __builtin_amdgcn_readlane(e, __ffsll((unsigned long long)left) - 1);
-        const uint64_t m = __ballot(e == f);
-        if (e == f) {
-            same = __popcll(m & ((1ull << lane) - 1));
-            if ((m >> lane) == 1) s.count[wave][f] = (uint8_t)(same + 1);
-        }
-        left &= ~m;
+    uint64_t alike = __ballot(e >= 0);
+#pragma unroll
+    for (int b = 0; b < kExpertBits; ++b) {
+        const bool bit = (e >> b) & 1;
+        const uint64_t set = __ballot(bit);
+        alike &= bit ? set : ~set;
+    }
+    if (e >= 0) {
+        same = __popcll(alike & ((1ull << lane) - 1));
+        if ((alike >> lane) == 1) s.count[wave][e] = (uint8_t)(same + 1);
     }
     __syncthreads();
     int before[2], tiles[2], count[2];
@@ -80,12 +93,7 @@ __device__ __forceinline__ int sort_pairs(const TI* __restrict__ ids, int P, int
             for (int w = 0; w < kPairWaves; ++w) count[i] += s.count[w][2 * p + i];
             tiles[i] = (count[i] + XR - 1) / XR;
         }
-        int end = tiles[0] + tiles[1];
-#pragma unroll
-        for (int off = 1; off < kWave; off <<= 1) {
-            const int v = __shfl_up(end, off);
-            if (lane >= off) end += v;
-        }
+        const int end = lanes_up_to(tiles[0] + tiles[1]);
         if (lane == kWave - 1) s.wave_tiles[wave] = end;
         before[0] = end - tiles[0] - tiles[1];
     }

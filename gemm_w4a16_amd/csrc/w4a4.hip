@@ -46,6 +46,13 @@ constexpr int kOnes = 0x7F7F7F7F;  // scales of one, for blocks past K (their el
 // stage, and their sums are added at the end, in order.  Operands and scales reach LDS by direct copies into a ring
 // of R stages.  kX = false: x is not in the ring (which holds weights alone) but whole in LDS behind it, quantized by
 // the block from activations.
+//
+// What bounds it.  1024 x 14336 x 4096 takes 32-33 us in 256 x 256 tiles (3.7 PFLOP/s), 8192 rows 240 (4.0), 8192 cubed
+// 245 (4.5; hipBLASLt's product of this format 314).  A k-tile is 2048 cycles of matrix instructions a SIMD
+// beside 2080 of LDS reads and writes a CU, so neither hides all of the other: 1.3 us a k-tile without copies, 1.7 with
+// (timing-only copies; 0.9 by the products alone).  The outputs, which all blocks write at once, are 5 us of the 32,
+// scale copies 1.  Four waves of 128 x 128, one a SIMD, read a third less from LDS and take 40.  Few rows: the weights'
+// stream and a block's chain of k-tiles (64 rows 8.8 us, 256 rows 14).
 template <int WM_, int WN_, int WK_, int TM_, int TN_, int R_, bool kX_ = true>
 struct Tiling {
     static constexpr int WM = WM_, WN = WN_, WK = WK_, TM = TM_, TN = TN_, R = R_;
@@ -557,10 +564,8 @@ using T64x64 = Tiling<2, 2, 1, 2, 2, 4>;
 using T32x64 = Tiling<2, 4, 1, 1, 1, 4>;
 using T32x32 = Tiling<2, 2, 2, 1, 1, 4>;
 // ... of which these quantize x themselves
-using F64x64 = Tiling<2, 2, 1, 2, 2, 4, false>;
 using F32x64 = Tiling<2, 4, 1, 1, 1, 4, false>;
 using F32x32 = Tiling<2, 2, 2, 1, 1, 4, false>;
-constexpr size_t kLdsBytes = 160 << 10;
 
 // What a tiling costs.  A CU's first block takes `us_ktile` for each 256 of K and `us_first` besides, each further one
 // `next_ktile` and `us_next`; `blocks` of them fit a CU.  The weights arrive at 5.6 TB/s, and neither hides all of the
@@ -624,17 +629,14 @@ template <typename T>
 bool launch_fused(const Product& p, const T* x, T* y, hipError_t& e) {
     const int choice = choose_tiling(p.M, p.N, p.K);
     bool done = false;
-    auto attempt = [&](int i, auto tiling, auto without_x) {
-        using C = decltype(without_x);
-        if (i != choice || done) return;
-        const int64_t rounds = (std::min<int64_t>(p.M, C::BM) + C::NW - 1) / C::NW * ((p.K + 511) / 512);
-        if (rounds > 2 * kFusedUnits || launch_blocks<C>(p.M, p.N) > kFusedBlocks) return;
-        if (fused_bytes<C>(p.K) + C::R * C::kStage > kLdsBytes) return;
-        e = launch_tiles<C>(p, x, y), done = true;
+    auto attempt = [&](int i, auto tiling) {
+        using C = decltype(tiling);
+        const int64_t units = (std::min<int64_t>(p.M, C::BM) + C::NW - 1) / C::NW * ((p.K + 511) / 512);  // of a wave
+        if (i != choice || units > 2 * kFusedUnits || launch_blocks<C>(p.M, p.N) > kFusedBlocks) return;
+        e = launch_tiles<C>(p, x, y), done = true;  // (K is at most 1024 here: 17 KB of LDS behind the ring)
     };
-    attempt(4, T64x64{}, F64x64{});
-    attempt(5, T32x64{}, F32x64{});
-    attempt(6, T32x32{}, F32x32{});
+    attempt(5, F32x64{});
+    attempt(6, F32x32{});
     return done;
 }
 

@@ -252,3 +252,49 @@ def test_a_decode_step_of_all_together():
         from test_gpu_mx4 import product
         ref, mag = product(z.cpu(), wt)
         assert ((out.cpu().double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 1.01 * H * 2 * F * mag).all()
+
+
+def test_calls_on_two_streams_at_once():
+    """Layers, 4-bit products and gradients of two streams, each with a workspace of its own, issued in turn without a wait:
+    as each alone."""
+    mx4 = w.W4A16_FMT_MX4_B32_E8M0
+    T, topk, E, H, I = 12, 2, 6, 512, 320
+    jobs = []
+    for seed in (21, 22):
+        d = data(T, topk, E, H, I, seed, 0.1)
+        t = {k: v.cuda() for k, v in d.items() if isinstance(v, torch.Tensor)}
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        x = torch.randn((40, 1024), generator=g, device="cuda").to(torch.bfloat16)
+        wt = torch.randn((700, 1024), generator=g, device="cuda") * 0.05
+        codes, scales, _ = w.alloc_packed(mx4, 700, 1024)
+        w.w4a16_quantize_pack(mx4, wt, 700, 1024, codes, scales, None)
+        jobs.append((t, x, codes, scales, w.alloc_expert_layer_workspace(T, topk, I), w.alloc_w4a4_workspace(mx4, 40, 700, 1024),
+                     w.alloc_add_rmsnorm_backward_workspace(40, 1024)))
+
+    def run_on(job, s):
+        t, x, codes, scales, lws, pws, nws = job
+        y, z = (torch.empty(shape, dtype=torch.bfloat16, device="cuda") for shape in ((T, H), (40, 700)))
+        dx, dw = torch.empty_like(x), torch.empty(1024, device="cuda")
+        torch.cuda.synchronize()
+
+        def once():
+            w.w4a16_expert_layer_w8a8(W8, w.W4A16_BF16, t["xq"], t["ascale"], T, t["ids"], 64, topk, t["weights"], E, t["up"], t["us"], t["down"],
+                                      t["ds"], H, I, y, *lws, stream=s)
+            w.w4a16_matmul_w4a4(mx4, w.W4A16_BF16, x, 40, codes, scales, None, 700, 1024, z, *pws, stream=s)
+            w.w4a16_add_rmsnorm_backward(w.W4A16_BF16, x, None, x, 40, 1024, None, 1e-5, dx, dw, *nws, stream=s)
+        return once, (y, z, dx, dw)
+
+    alone = []
+    for job in jobs:
+        once, out = run_on(job, None)
+        once()
+        torch.cuda.synchronize()
+        alone.append(out)
+    streams = [torch.cuda.Stream() for _ in jobs]
+    both = [run_on(job, s) for job, s in zip(jobs, streams)]
+    for _ in range(20):
+        for once, _ in both:
+            once()
+    torch.cuda.synchronize()
+    for (_, out), ref in zip(both, alone):
+        assert all(torch.equal(a, b) for a, b in zip(out, ref))

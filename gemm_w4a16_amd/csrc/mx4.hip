@@ -16,9 +16,9 @@ namespace w4a16 {
 namespace {
 
 // Bytes bound both directions.  A block takes 32 rows of a k-tile, so that its scales, one group of 256 bytes, pass through
-// LDS and are whole lines of memory (written byte by byte they cost as much as the codes); a half wave takes a row
-// at a time, 8 values a lane, four lanes a block of the format.  14336 x 4096 fp32
-// 51 us (5.2 TB/s; a copy moves 5.0), bf16 28; back to bf16 24-31; 333 x 2080 3.2.
+// LDS and are whole lines of memory (written byte by byte they cost as much as the codes); a lane takes 16 bytes
+// of a row, so a wave two rows of 16-bit values or one of 32-bit ones.  14336 x 4096 fp32
+// 43-44 us (6.1 TB/s; a copy moves 5.1), bf16 28; back to bf16 24-31; 333 x 2080 3.2.  (32 bytes a lane of fp32: 50-53.)
 
 // Tile `tile`: k-tile kt of rows 32 g ..
 struct Tile {
@@ -30,7 +30,9 @@ struct Tile {
 template <typename T, int kWaves, bool kStream>
 __global__ __launch_bounds__(64 * kWaves) void quant_mx4_kernel(const T* __restrict__ x, int64_t M, int K, uint8_t* __restrict__ codes,
                                                         uint8_t* __restrict__ scales) {
-    constexpr int V = 16 / sizeof(T), kLoads = 8 / V, kRowsOfWave = 32 / kWaves;
+    constexpr int V = 16 / sizeof(T), kLanes = kMx4TileK / V, kAtOnce = kWave / kLanes;  // lanes a row, rows at once
+    constexpr int kBlockLanes = kMx4Block / V, kSteps = 32 / kWaves / kAtOnce;
+    static_assert(kSteps * kWaves * kAtOnce == 32, "a tile's rows");
     __shared__ uint32_t group[2][64];
     const int lane = lane_id(), wave = wave_id();
     const int KT = (int)mx4_ktiles(K);
@@ -38,25 +40,27 @@ __global__ __launch_bounds__(64 * kWaves) void quant_mx4_kernel(const T* __restr
     int which = 0;
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, which ^= 1) {
         const Tile at(tile, KT);
-        const int k = at.kt * kMx4TileK + 8 * (lane % 32);
-        const int64_t m0 = 32 * at.g + kRowsOfWave * wave + lane / 32;
-        // (K % 32 == 0: the four lanes of a block are there together or not at all; what is not there has scale 0)
-        Pack<T, V> p[kRowsOfWave / 2][kLoads];
+        const int k = at.kt * kMx4TileK + V * (lane % kLanes);
+        const int r0 = kSteps * kAtOnce * wave + lane / kLanes;
+        const int64_t m0 = 32 * at.g + r0;
+        // (K % 32 == 0: the lanes of a block are there together or not at all; what is not there has scale 0)
+        Pack<T, V> p[kSteps];
 #pragma unroll
-        for (int i = 0; i < kRowsOfWave / 2; ++i)
+        for (int i = 0; i < kSteps; ++i) {
+            const int64_t m = m0 + kAtOnce * i;
+            p[i] = m < M && k < K ? load_unit<kStream, false, V>(x + m * K + k) : Pack<T, V>{};
+        }
 #pragma unroll
-            for (int h = 0; h < kLoads; ++h) {
-                const int64_t m = m0 + 2 * i;
-                p[i][h] = m < M && k < K ? load_unit<kStream, false, V>(x + m * K + k + V * h) : Pack<T, V>{};
-            }
-#pragma unroll
-        for (int i = 0; i < kRowsOfWave / 2; ++i) {
-            const int64_t m = m0 + 2 * i;
-            const T* v = p[i][0].v;  // (a row's packs are one array of 8)
-            const uint32_t s = mx4_scale(mx4_max_quad(mx4_max_bits<8>(v))), w = mx4_codes<8>(v, s);
-            if (m < M && k < K) *reinterpret_cast<uint32_t*>(codes + m * (K / 2) + k / 2) = w;
-            if (lane % 4 == 0)
-                reinterpret_cast<uint8_t*>(group[which])[mx4_scale_at(1, kRowsOfWave * wave + 2 * i + lane / 32, lane % 32 / 4)] = (uint8_t)s;
+        for (int i = 0; i < kSteps; ++i) {
+            const int64_t m = m0 + kAtOnce * i;
+            const uint32_t top = mx4_max_bits<V>(p[i].v);
+            const uint32_t s = mx4_scale(kBlockLanes == 8 ? mx4_max_eight(top) : mx4_max_quad(top));
+            uint32_t w = mx4_codes<V>(p[i].v, s);
+            if constexpr (V == 4)  // two lanes' codes in the first one's word
+                w |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w, kDppQuadXor1, 0xF, 0xF, false) << 16;
+            if (m < M && k < K && lane % (8 / V) == 0) *reinterpret_cast<uint32_t*>(codes + m * (K / 2) + k / 2) = w;
+            if (lane % kBlockLanes == 0)
+                reinterpret_cast<uint8_t*>(group[which])[mx4_scale_at(1, r0 + kAtOnce * i, lane % kLanes / kBlockLanes)] = (uint8_t)s;
         }
         __syncthreads();  // (the other half of `group` takes the next tile's)
         if (threadIdx.x < 64)
@@ -108,7 +112,7 @@ __global__ __launch_bounds__(64 * kWaves) void dequant_mx4_kernel(const uint8_t*
 }
 
 // Few tiles by sixteen waves each, for the shorter chain (333 x 2080 fp16 3.2 us against 3.9 by four); else by eight (14336 x
-// 4096 fp32 51 against 56 by four, bf16 28 against 34 by sixteen); arrays from 64 MiB on past the caches' usual order.
+// 4096 bf16 28 us against 34 by sixteen); arrays from 64 MiB on past the caches' usual order.
 template <typename T, typename F>
 hipError_t with_shape(int64_t M, int64_t K, F f) {
     const int64_t tiles = mx4_groups(M) * mx4_ktiles(K);

@@ -118,6 +118,16 @@ def test_every_token_to_the_same_experts(T, topk, E):
     check(run(d, "f32"), d, "f32")
 
 
+# 63 to 65 pairs: one wave's, and the first that are not; some with no expert, some experts with one pair, some with many
+@pytest.mark.parametrize("T,topk", [(9, 7), (8, 8), (32, 2), (13, 5), (1, 64), (1, 65)])
+@pytest.mark.parametrize("E", [2, 7, 512])
+def test_about_a_wave_of_pairs(T, topk, E):
+    d = data(T, topk, E, 80, 48, 9)
+    d["ids"][0, topk // 2] = -1
+    d["ids"][-1, -1] = E
+    check(run(d, "f32"), d, "f32")
+
+
 @pytest.mark.parametrize("bits", [32, 64])
 def test_ids_out_of_range_and_no_experts_at_all(bits):
     d = data(6, 3, 5, 64, 96, 3, 0.0)

@@ -497,7 +497,9 @@ hipError_t launch_add_rmsnorm_backward(int dtype, const void* dy, const void* dh
         if (N <= kGradKept<T>) {
             auto run = [&](auto waves, auto keep, auto any) {
                 constexpr int kWaves = decltype(waves)::value, kUnits = decltype(keep)::value, kGradWaves = grad_waves(kWaves), kRows = kGradWaves / kWaves;
-                parts = (int)std::min((rows + kRows - 1) / kRows, kGradBlocks);
+                // Up to two rows for each group one block and no join (16 x 1024 bf16 5.6 us against 6.4, 16 x 500 fp32
+                // 4.1 against 5.6; at four rows each 8.0 against 6.5 and 5.7 against 5.6).
+                parts = rows <= 2 * kRows ? 1 : (int)std::min((rows + kRows - 1) / kRows, kGradBlocks);
                 float* part = parts == 1 ? dweight : dweight ? ws : nullptr;
                 hipLaunchKernelGGL((add_rmsnorm_backward_kernel<T, kWaves, kUnits, decltype(any)::value>), dim3((unsigned)parts),
                                    dim3(64 * kGradWaves), 0, stream, dyt, dht, ht, rows, (int)N, wt, eps, dxt, part);

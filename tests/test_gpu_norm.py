@@ -228,6 +228,13 @@ def test_gradients(T, N, kind, with_dh, with_w):
     m.check()
 
 
+# the rows up to which one block writes the weight's gradient itself, and one more
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("T,N", [(16, 500), (17, 500), (8, 2048), (9, 2048), (4, 4000), (5, 4000), (2, 16384), (3, 16384), (2, 8192), (3, 8192)])
+def test_gradients_of_few_rows(T, N, kind):
+    test_gradients(T, N, kind, 1, 1)
+
+
 @pytest.mark.parametrize("T,N", [(3, 24), (2, 33)])
 def test_gradients_against_differences(T, N):
     """Of L = sum(y dy) + sum(h dh) by the formulas in 64 bits: central differences with a step of 2^-12 are off by

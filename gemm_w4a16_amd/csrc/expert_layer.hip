@@ -393,7 +393,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void layer_down_kernel(const int8_
             const int k = (it.kt * KW + (KW == 2 ? j : 0)) * 128 + 16 * copied_chunk(8 * j + lane / 8);
             return (uint32_t)min(k, I - 16);
         };
-        const int8_t* w = there ? it.w : down;
+        const int8_t* w = there ? it.w : hq;  // (no weights of experts that no token chose)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const uint32_t row = KW == 2 ? lane / 8 : 8 * j + lane / 8;

@@ -8,9 +8,9 @@
 //     o_n = s_n sum_groups b (sum_{i in group} hq_i down[e][n][i])            (integer sums exact, the rest fp32)
 //     y[t][n] = sum_j weights[t][j] o_n          (in order of j, rounded once)
 // The used experts' weights, read once, are what it costs: one token through two of eight experts of H = 4096, I = 14336
-// takes 38 us up (6.2 TB/s) and 22 down (5.4); eight tokens, 6.3 experts, 111 (6.7) and 61 (6.1); 32 tokens x 8 of 64
-// experts of 2048 x 1024 41 and 28 (5.6, 4.1).  Small layers: each launch's start, sort and finish, 5 us (five tokens x 3
-// of 20 experts of 1008 x 496 7.8 and 6.5).
+// takes 38 us up (6.2 TB/s) and 21 down (5.5); eight tokens, 6.3 experts, 111 (6.7) and 61 (6.1); 32 tokens x 8 of 64
+// experts of 2048 x 1024 41 and 28 (5.6, 4.1).  Small layers: each launch's start, sort and finish, 4-5 us (five tokens x 3
+// of 20 experts of 1008 x 496 8.0 and 5.6).
 // A scale for 64 columns instead of one for the row: the first launch then finishes its codes by itself (a row's
 // largest magnitude would need all of its blocks), and small values keep more bits.
 #include <algorithm>

@@ -18,7 +18,7 @@ namespace {
 // Bytes bound both directions.  A block takes 32 rows of a k-tile, so that its scales, one group of 256 bytes, pass through
 // LDS and are whole lines of memory (written byte by byte they cost as much as the codes); a lane takes 16 bytes
 // of a row, so a wave two rows of 16-bit values or one of 32-bit ones.  14336 x 4096 fp32
-// 43-44 us (6.1 TB/s; a copy moves 5.1), bf16 28; back to bf16 24-31; 333 x 2080 3.2.  (32 bytes a lane of fp32: 50-53.)
+// 43-44 us (6.1 TB/s; a copy moves 5.1), bf16 28; back to bf16 24-31; 333 x 2080 fp16 3.0.  (32 bytes a lane of fp32: 50-53.)
 
 // Tile `tile`: k-tile kt of rows 32 g ..
 struct Tile {

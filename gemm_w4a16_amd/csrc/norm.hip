@@ -11,7 +11,7 @@
 // Bytes bound all of these for many rows, and a row's chain of loads and reductions for few.  A row stays in registers
 // between its passes (kKeep units of 16 bytes a thread); what a long row has beyond that is read again, from the
 // caches.  8192 x 4096 bf16 with a residual: in 8 bits 42 us (5.6 TB/s; a copy moves 5.1), in bf16 48, gradients 55 (4.9
-// TB/s); one row in 8 bits 3.7 us, 1024 rows 10.  With a row's loads behind the row before instead of beside it, 59, 59
+// TB/s); one row in 8 bits 3.2 us, 1024 rows 10.  With a row's loads behind the row before instead of beside it, 59, 59
 // and 89.
 #include <algorithm>
 #include <type_traits>

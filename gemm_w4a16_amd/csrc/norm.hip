@@ -63,12 +63,12 @@ __device__ __forceinline__ void add(const Pack<T, V>& u, float (&f)[V]) {
     for (int j = 0; j < V; ++j) f[j] += to_f32(u.v[j]);
 }
 
-// A sum or maximum over the threads of a row, the same in each: lanes, then waves in order.  red: a word per wave.
+// A sum or maximum over the threads of a row, the same in each: lanes, then waves in order.  red: a word per wave, of
+// two arrays in turn: who writes one has passed the other's barrier, behind which nobody reads the first any more.
 template <int kWaves>
 __device__ __forceinline__ float row_sum(float v, float* red) {
     v = wave_sum(v);
     if constexpr (kWaves > 1) {
-        __syncthreads();  // red may still be read
         if (lane_id() == 0) red[wave_id()] = v;
         __syncthreads();
         v = red[0];
@@ -83,7 +83,6 @@ __device__ __forceinline__ void row_sums(float& a, float& b, float2* red) {
     a = wave_sum(a);
     b = wave_sum(b);
     if constexpr (kWaves > 1) {
-        __syncthreads();
         if (lane_id() == 0) red[wave_id() % kWaves] = make_float2(a, b);
         __syncthreads();
         a = red[0].x, b = red[0].y;
@@ -97,7 +96,6 @@ __device__ __forceinline__ uint32_t row_max(uint32_t m, float* red) {
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off));
     if constexpr (kWaves > 1) {
-        __syncthreads();
         if (lane_id() == 0) red[wave_id()] = __uint_as_float(m);
         __syncthreads();
 #pragma unroll
@@ -141,7 +139,8 @@ __global__ __launch_bounds__(kWaves == 1 ? 256 : 64 * kWaves) void add_rmsnorm_k
                                                                                       T* h, T* y, int8_t* __restrict__ xq,
                                                                                       float* __restrict__ ascale) {
     constexpr int V = kUnit<T>, kThreads = 64 * kWaves, kRows = kWaves == 1 ? 4 : 1;
-    __shared__ float red[kWaves];
+    __shared__ float red[2][kWaves];
+    int turn = 0;
     const int tid = kWaves == 1 ? lane_id() : (int)threadIdx.x;
     const int units = (N + V - 1) / V;
     const int64_t step = (int64_t)gridDim.x * kRows;
@@ -187,7 +186,8 @@ __global__ __launch_bounds__(kWaves == 1 ? 256 : 64 * kWaves) void add_rmsnorm_k
 #pragma unroll
             for (int j = 0; j < V; ++j) ss = __builtin_fmaf(s[j], s[j], ss);
         }
-        ss = row_sum<kWaves>(ss, red);
+        ss = row_sum<kWaves>(ss, red[turn]);
+        if constexpr (!kI8) turn ^= 1;
         const float r = 1.0f / sqrtf(ss / (float)N + eps);
         // s -> v
         auto scaled = [&](const Pack<T, V>& w, float (&s)[V]) __attribute__((always_inline)) {
@@ -234,7 +234,7 @@ __global__ __launch_bounds__(kWaves == 1 ? 256 : 64 * kWaves) void add_rmsnorm_k
                 scaled(weight_unit(c), s);
                 widest(s);
             }
-            const float a = scale_i8(__uint_as_float(row_max<kWaves>(top, red))), inv = 1.0f / a;
+            const float a = scale_i8(__uint_as_float(row_max<kWaves>(top, red[1]))), inv = 1.0f / a;
             auto codes = [&](int c, const float (&v)[V]) __attribute__((always_inline)) {
                 uint32_t w[V / 4];
                 codes_i8(v, a, inv, w);
@@ -272,7 +272,8 @@ __global__ __launch_bounds__(64 * grad_waves(kWaves)) void add_rmsnorm_backward_
                                                                                int64_t rows, int N, const T* __restrict__ weight,
                                                                                float eps, T* dx, float* __restrict__ part) {
     constexpr int V = kUnit<T>, kThreads = 64 * kWaves, kGradWaves = grad_waves(kWaves), kRows = kGradWaves / kWaves;
-    __shared__ float2 red[kGradWaves];
+    __shared__ float2 red[2][kGradWaves];
+    int turn = 0;
     __shared__ float sums[kRows > 1 ? kRows * kThreads * kUnits * V : 1];
     const int tid = threadIdx.x % kThreads, group = wave_id() / kWaves, units = (N + V - 1) / V;
     Pack<T, V> w[kUnits];
@@ -315,7 +316,8 @@ __global__ __launch_bounds__(64 * grad_waves(kWaves)) void add_rmsnorm_backward_
                 ss = __builtin_fmaf(hv, hv, ss);
                 gh = __builtin_fmaf(g, hv, gh);
             }
-        row_sums<kWaves>(ss, gh, red + group * kWaves);
+        row_sums<kWaves>(ss, gh, red[turn] + group * kWaves);
+        turn ^= 1;
         const float r = 1.0f / sqrtf(ss / (float)N + eps), c0 = gh / (float)N * (r * r);
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
@@ -365,7 +367,8 @@ __global__ __launch_bounds__(64 * kWaves) void add_rmsnorm_backward_long_kernel(
                                                                                 int64_t rows, int N, const T* __restrict__ weight,
                                                                                 float eps, T* dx, float* __restrict__ rstd) {
     constexpr int V = kUnit<T>, kThreads = 64 * kWaves;
-    __shared__ float2 red[kWaves];
+    __shared__ float2 red[2][kWaves];
+    int turn = 0;
     const int units = (N + V - 1) / V;
     for (int64_t m = blockIdx.x; m < rows; m += gridDim.x) {
         float ss = 0.0f, gh = 0.0f;
@@ -380,7 +383,8 @@ __global__ __launch_bounds__(64 * kWaves) void add_rmsnorm_backward_long_kernel(
                 gh = __builtin_fmaf(weight ? g[j] * w[j] : g[j], hv[j], gh);
             }
         }
-        row_sums<kWaves>(ss, gh, red);
+        row_sums<kWaves>(ss, gh, red[turn]);
+        turn ^= 1;
         const float r = 1.0f / sqrtf(ss / (float)N + eps), c0 = gh / (float)N * (r * r);
         if (rstd && threadIdx.x == 0) rstd[m] = r;
         if (!dx) continue;

@@ -10,7 +10,7 @@
 //
 // Bytes bound all of these for many rows, and a row's chain of loads and reductions for few.  A row stays in registers
 // between its passes (kKeep units of 16 bytes a thread); what a long row has beyond that is read again, from the
-// caches.  8192 x 4096 bf16 with a residual: in 8 bits 42 us (5.6 TB/s; a copy moves 5.1), in bf16 48, gradients 55 (4.9
+// caches.  8192 x 4096 bf16 with a residual: in 8 bits 42 us (5.6 TB/s; a copy moves 5.1), in bf16 48, gradients 51 (5.3
 // TB/s); one row in 8 bits 3.2 us, 1024 rows 10.  With a row's loads behind the row before instead of beside it, 59, 59
 // and 89.
 #include <algorithm>
@@ -267,7 +267,7 @@ __global__ __launch_bounds__(kWaves == 1 ? 256 : 64 * kWaves) void add_rmsnorm_k
 // add theirs in LDS at the end, in order.  A block's part leaves once, to part [blocks][N].  The order of additions
 // does not depend on timing.
 constexpr int grad_waves(int row_waves) { return row_waves > 8 ? row_waves : 8; }  // of a block
-template <typename T, int kWaves, int kUnits, bool kAny>
+template <typename T, int kWaves, int kUnits, bool kAny, bool kStream>
 __global__ __launch_bounds__(64 * grad_waves(kWaves)) void add_rmsnorm_backward_kernel(const T* dy, const T* dh, const T* __restrict__ h,
                                                                                int64_t rows, int N, const T* __restrict__ weight,
                                                                                float eps, T* dx, float* __restrict__ part) {
@@ -294,9 +294,9 @@ __global__ __launch_bounds__(64 * grad_waves(kWaves)) void add_rmsnorm_backward_
         for (int i = 0; i < kUnits; ++i) {
             const int c = tid + kThreads * i;
             const bool there = c < units && row < rows;
-            next_h[i] = there ? load_row_unit<false, kAny>(h + row * N, c, N) : Pack<T, V>{};
-            next_g[i] = there ? load_row_unit<false, kAny>(dy + row * N, c, N) : Pack<T, V>{};
-            if (dx && dh && there) next_a[i] = load_row_unit<false, kAny>(dh + row * N, c, N);
+            next_h[i] = there ? load_row_unit<kStream, kAny>(h + row * N, c, N) : Pack<T, V>{};
+            next_g[i] = there ? load_row_unit<kStream, kAny>(dy + row * N, c, N) : Pack<T, V>{};
+            if (dx && dh && there) next_a[i] = load_row_unit<kStream, kAny>(dh + row * N, c, N);
         }
     };
     constexpr bool kAhead = kWaves <= 8;  // (sixteen waves a block have 128 registers a thread: they spill)
@@ -331,7 +331,7 @@ __global__ __launch_bounds__(64 * grad_waves(kWaves)) void add_rmsnorm_backward_
                 o[j] = r * (g * to_f32(w[i].v[j]) - hv * c0);
             }
             if (dx && dh) add(au[i], o);
-            if (dx) store_row_unit<false, kAny>(dx + m * N, c, N, o);
+            if (dx) store_row_unit<kStream, kAny>(dx + m * N, c, N, o);
         }
     }
     if (!part) return;
@@ -446,7 +446,8 @@ int64_t grad_parts(int64_t rows) { return std::min(rows, kGradBlocks); }
 
 // Waves of a launch: as many as run at once, each with rows in turn.
 constexpr int64_t kNormWaves = 4096;
-// Arrays from this many bytes on are read and written past the caches' usual order.
+// Arrays from this many bytes on are read and written past the caches' usual order (gradients 16384 x 4096 bf16 92 us against
+// 101, 8192 x 2048, 32 MiB, 28.4 against 30.3; of 16 MiB 17.6 against 17.2).
 constexpr int64_t kNormStreamBytes = 32 << 20;
 
 }  // namespace
@@ -499,24 +500,28 @@ hipError_t launch_add_rmsnorm_backward(int dtype, const void* dy, const void* dh
         T* dxt = static_cast<T*>(dx);
         int parts = (int)grad_parts(rows);
         if (N <= kGradKept<T>) {
-            auto run = [&](auto waves, auto keep, auto any) {
+            const bool stream_past = rows * N * (int64_t)sizeof(T) >= kNormStreamBytes;
+            auto run = [&](auto waves, auto keep, auto any, auto past) {
                 constexpr int kWaves = decltype(waves)::value, kUnits = decltype(keep)::value, kGradWaves = grad_waves(kWaves), kRows = kGradWaves / kWaves;
                 // Up to two rows for each group one block and no join (16 x 1024 bf16 5.6 us against 6.4, 16 x 500 fp32
                 // 4.1 against 5.6; at four rows each 8.0 against 6.5 and 5.7 against 5.6).
                 parts = rows <= 2 * kRows ? 1 : (int)std::min((rows + kRows - 1) / kRows, kGradBlocks);
                 float* part = parts == 1 ? dweight : dweight ? ws : nullptr;
-                hipLaunchKernelGGL((add_rmsnorm_backward_kernel<T, kWaves, kUnits, decltype(any)::value>), dim3((unsigned)parts),
+                hipLaunchKernelGGL((add_rmsnorm_backward_kernel<T, kWaves, kUnits, decltype(any)::value, decltype(past)::value>), dim3((unsigned)parts),
                                    dim3(64 * kGradWaves), 0, stream, dyt, dht, ht, rows, (int)N, wt, eps, dxt, part);
                 return hipGetLastError();
             };
-            auto pick = [&](auto any) {
+            auto pick_waves = [&](auto any, auto past) {
                 const int64_t units = (N + kUnit<T> - 1) / kUnit<T>;
                 using I2 = std::integral_constant<int, 2>;
-                if (units <= 128) return run(std::integral_constant<int, 1>{}, I2{}, any);
-                if (units <= 256) return run(I2{}, I2{}, any);
-                if (units <= 512) return run(std::integral_constant<int, 4>{}, I2{}, any);
-                if (units <= 1024) return run(std::integral_constant<int, 8>{}, I2{}, any);
-                return run(std::integral_constant<int, 16>{}, I2{}, any);
+                if (units <= 128) return run(std::integral_constant<int, 1>{}, I2{}, any, past);
+                if (units <= 256) return run(I2{}, I2{}, any, past);
+                if (units <= 512) return run(std::integral_constant<int, 4>{}, I2{}, any, past);
+                if (units <= 1024) return run(std::integral_constant<int, 8>{}, I2{}, any, past);
+                return run(std::integral_constant<int, 16>{}, I2{}, any, past);
+            };
+            auto pick = [&](auto any) {
+                return stream_past ? pick_waves(any, std::true_type{}) : pick_waves(any, std::false_type{});
             };
             const hipError_t e = N % kUnit<T> == 0 ? pick(std::false_type{}) : pick(std::true_type{});
             if (e != hipSuccess || !dweight || parts == 1) return e;

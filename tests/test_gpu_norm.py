@@ -235,6 +235,15 @@ def test_gradients_of_few_rows(T, N, kind):
     test_gradients(T, N, kind, 1, 1)
 
 
+# arrays from 32 MiB on, which pass the caches by: a wave a row up to sixteen, whole units and ragged rows
+@pytest.mark.parametrize("T,N", [(35000, 496), (17000, 1001), (4300, 4000), (4200, 4097), (2100, 8176), (1100, 15600), (1101, 15601)])
+def test_large_arrays(T, N):
+    test_norm(T, N, "bf16", 1, 1, 1)
+    test_gradients(T, N, "bf16", 1, 1)
+    if N % 16 == 0:
+        test_norm_i8(T, N, "bf16", 1, 1)
+
+
 @pytest.mark.parametrize("T,N", [(3, 24), (2, 33)])
 def test_gradients_against_differences(T, N):
     """Of L = sum(y dy) + sum(h dh) by the formulas in 64 bits: central differences with a step of 2^-12 are off by

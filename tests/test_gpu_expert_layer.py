@@ -118,6 +118,13 @@ def test_every_token_to_the_same_experts(T, topk, E):
     check(run(d, "f32"), d, "f32")
 
 
+# weights from 64 MiB on, which pass the caches by: of 16 columns a block, of 8, and tiles of 16 pairs
+@pytest.mark.parametrize("T,topk,E,H,I", [(2, 2, 3, 4112, 2064), (3, 2, 4, 2064, 2832), (12, 2, 3, 2064, 4112)])
+def test_large_weights(T, topk, E, H, I):
+    d = data(T, topk, E, H, I, 10)
+    check(run(d, "bf16"), d, "bf16")
+
+
 # 63 to 65 pairs: one wave's, and the first that are not; some with no expert, some experts with one pair, some with many
 @pytest.mark.parametrize("T,topk", [(9, 7), (8, 8), (32, 2), (13, 5), (1, 64), (1, 65)])
 @pytest.mark.parametrize("E", [2, 7, 512])

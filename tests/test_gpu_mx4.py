@@ -115,6 +115,28 @@ def test_rows_bit_exact(M, K, kind):
     m.check()
 
 
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("M,K", [(2000, 4128), (4200, 4128), (8300, 4128)])
+def test_many_rows_as_in_pieces(M, K, kind):
+    """The kernels of many rows, and of arrays that pass the caches by: bit for bit those of few."""
+    act, dt = TYPES[kind][:2]
+    x = rows(M, K, dt, 2).cuda()
+    xq, xs, _ = w.alloc_packed(MX4, M, K)
+    w.w4a16_quantize_rows_mx4(act, x, M, K, xq, xs)
+    v = torch.empty((M, K), dtype=dt, device="cuda")
+    w.w4a16_dequant(MX4, xq, xs, None, M, K, act, v)
+    scales = xs.reshape((K + 255) // 256, -1, 256)
+    for r in range(0, M, 640):
+        n = min(640, M - r)
+        pq, ps, _ = w.alloc_packed(MX4, n, K)
+        w.w4a16_quantize_rows_mx4(act, x[r:r + n].contiguous(), n, K, pq, ps)
+        assert torch.equal(pq.reshape(n, -1), xq.reshape(M, -1)[r:r + n])
+        assert torch.equal(ps.reshape(scales.shape[0], -1, 256), scales[:, r // 32:(r + n + 31) // 32])
+        pv = torch.empty((n, K), dtype=dt, device="cuda")
+        w.w4a16_dequant(MX4, pq, ps, None, n, K, act, pv)
+        assert torch.equal(pv.nan_to_num(7.0), v[r:r + n].nan_to_num(7.0))
+
+
 def test_smallest_and_largest_numbers():
     """fp32 from the subnormal numbers to the largest: exponents of blocks over the whole range of their byte."""
     g = torch.Generator().manual_seed(3)
@@ -204,6 +226,21 @@ def test_whole_numbers_are_exact(M, N, K):
     w.w4a16_gemm_w4a4(MX4, w.W4A16_FP32, xq, xs, M, wq, ws, None, N, K, y)
     assert (xv.abs() @ wv.abs().t().contiguous()).max() < 2 ** 24
     assert torch.equal(y.double(), xv @ wv.t().contiguous())
+
+
+# weights from 64 MiB on, which few rows read past the caches' usual order
+@pytest.mark.parametrize("M,N,K", [(1, 33005, 4096), (2, 20001, 7200), (5, 17008, 8192), (16, 70000, 2080)])
+def test_few_rows_of_large_weights(M, N, K):
+    test_whole_numbers_are_exact(M, N, K)
+    if M < 5:  # quantized in the product
+        g = torch.Generator().manual_seed(30)
+        x = (torch.randint(-3, 4, (M, K), generator=g) * 2).to(torch.bfloat16)
+        code = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8).cuda() & 0x22  # zeros and ones
+        scales = torch.full(w.alloc_packed(MX4, N, K)[1].shape, 127, dtype=torch.uint8, device="cuda")
+        wv = torch.stack([code & 0x0F, code >> 4], -1).reshape(N, K).double() / 2
+        y, (ws, nb) = torch.empty((M, N), dtype=torch.bfloat16, device="cuda"), w.alloc_w4a4_workspace(MX4, M, N, K)
+        w.w4a16_matmul_w4a4(MX4, w.W4A16_BF16, x.cuda(), M, code, scales, None, N, K, y, ws, nb)
+        assert torch.equal(y, (x.cuda().double() @ wv.t().contiguous()).to(torch.bfloat16))
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 100, 512), (20, 200, 288), (300, 300, 1056)])

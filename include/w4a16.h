@@ -491,10 +491,10 @@ size_t w4a16_w4a4_workspace_bytes(w4a16_format_t fmt, int64_t M, int64_t N, int6
  *   h [T][N]  s rounded to `act`: the sum that goes on past the layer; NULL where it is not wanted
  *   v = s r w in fp32 with r = 1 / sqrt(sum_n s^2 / N + eps), weight w [N] of type `act` (NULL: ones)
  * The norm is of s before it is rounded.  Sums are fp32 in a fixed order: bitwise reproducible.  eps finite
- * and not negative (with 0, a row of zeros is divided by zero: NaN); N at most 2^22 (ERR_UNSUPPORTED above).  A row whose sum of squares passes fp32's
- * range gets zeros, one with an infinity or NaN gets NaN where it has one (and zeros or NaN besides); other rows
- * are not touched by it.  h and y may each be x's or residual's own array (the same address), but not one
- * array for both; other overlaps are not allowed. */
+ * and not negative (with 0, a row of zeros is divided by zero: NaN); N at most 2^22 (ERR_UNSUPPORTED above).  A row whose
+ * sum of squares passes fp32's range gets zeros, one with an infinity or NaN gets NaN where it has one (and zeros or NaN
+ * besides); other rows are not touched by it.  h and y may each be x's or residual's own array (the same address),
+ * but not one array for both; other overlaps are not allowed. */
 
 /* y [T][N] = v rounded to `act`. */
 w4a16_status_t w4a16_add_rmsnorm(w4a16_dtype_t act, const void* x, const void* residual, int64_t T, int64_t N,

@@ -189,20 +189,23 @@ __device__ __forceinline__ T* uniform(T* p) {
 
 // A block: one tile of pairs, one group of 64 columns of v; a wave 16 of the columns (their gate rows and up rows, 32
 // weight rows).  Two stages a wave, so that four blocks share a CU: while one sorts or finishes, the others stream
-// (three stages, two blocks a CU: 49 us against 43 for 32 tokens x 8 of 64 experts, H = 2048, I = 1024).
-template <int XR>
+// (three stages, two blocks a CU: 49 us against 43 for 32 tokens x 8 of 64 experts, H = 2048, I = 1024).  Three where
+// all blocks run at once, two on a CU (4 of 32 experts of 2048 x 768 for one token 8.2 us against 8.8, 20 tokens x 2 of 16 of
+// 2048 x 1024 22.0 against 23.1 in all).
+constexpr int64_t kUpDeepBlocks = 512;
+template <int XR, int R_>
 struct UpShape {
-    static constexpr int R = 2, kStage = 4096 + 128 * XR, kCopies = 4 + XR / 8;
+    static constexpr int R = R_, kStage = 4096 + 128 * XR, kCopies = 4 + XR / 8;
     static constexpr size_t kLds = 4 * R * kStage;
     static_assert(kLds >= sizeof(PairTiles<XR>), "the lists fit in the ring");
 };
 
-template <typename TI, int XR, bool kOnce>
+template <typename TI, int XR, int kStages, bool kOnce>
 __global__ __launch_bounds__(256) void layer_up_kernel(const int8_t* __restrict__ xq, const float* __restrict__ ascale,
                                                             const TI* __restrict__ ids, int P, int topk, int E,
                                                             const int8_t* __restrict__ up, const float* __restrict__ up_scales, int H,
                                                             int I, int groups, int8_t* __restrict__ hq, float* __restrict__ hscale) {
-    using S = UpShape<XR>;
+    using S = UpShape<XR, kStages>;
     constexpr int R = S::R, C = S::kCopies;
     __shared__ __attribute__((aligned(1024))) char smem[S::kLds];
     const int tile = blockIdx.x / groups, group = blockIdx.x - tile * groups;
@@ -484,8 +487,15 @@ hipError_t launch_expert_layer_w8a8(int dtype, const int8_t* xq, const float* as
         constexpr int XR = decltype(xr)::value, kCols = decltype(cols)::value;
         constexpr bool kOnce = decltype(once)::value;
         const TI* idt = static_cast<const TI*>(ids);
-        hipLaunchKernelGGL((layer_up_kernel<TI, XR, kOnce>), dim3((unsigned)(expert_tiles(P, E, XR) * groups)), dim3(256), 0,
-                           stream, xq, ascale, idt, (int)P, (int)topk, (int)E, up, up_scales, (int)H, (int)I, (int)groups, hq, hscale);
+        const int64_t blocks = expert_tiles(P, E, XR) * groups;
+        auto launch_up = [&](auto stages) {
+            hipLaunchKernelGGL((layer_up_kernel<TI, XR, decltype(stages)::value, kOnce>), dim3((unsigned)blocks), dim3(256), 0, stream, xq,
+                               ascale, idt, (int)P, (int)topk, (int)E, up, up_scales, (int)H, (int)I, (int)groups, hq, hscale);
+        };
+        if (blocks <= kUpDeepBlocks)
+            launch_up(std::integral_constant<int, 3>{});
+        else
+            launch_up(std::integral_constant<int, 2>{});
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
         return with_act_type(dtype, [&](auto t) {
             using TO = decltype(t);

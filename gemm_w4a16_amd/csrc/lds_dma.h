@@ -14,40 +14,42 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 // them to LDS byte m0 + 16 l (or 4 l), with m0 = lds + kImm.  They are issued from inline
 // assembly so that the compiler does not track them: it cannot tell LDS stages apart and would
 // wait for every copy in flight before any LDS access.  The only waits for them are explicit
-// wait_vm<n>() calls, placed by count.
+// wait_vm<n>() calls, placed by count.  A copy needs a wait state behind a scalar write of m0, which
+// the compiler does not put inside inline assembly: the s_nop (tests/test_lds_copy_waits_cpu.py
+// looks for it, and for the five between a vector instruction's write of sbase and the copy, in the built code).
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 template <int kImm = 0>
 __device__ __forceinline__ void dma16(uint32_t voff, const void* sbase, uint32_t lds) {
     if constexpr (kImm == 0)
-        asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(sbase), "s"(lds)
+        asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(sbase), "s"(lds)
                      : "memory", "m0");
     else
-        asm volatile("s_add_u32 m0, %2, %3\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(sbase), "s"(lds),
+        asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(sbase), "s"(lds),
                      "n"(kImm)
                      : "memory", "m0", "scc");
 }
 // The same, non-temporal: data read once.
 __device__ __forceinline__ void dma16_once(uint32_t voff, const void* sbase, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(voff), "s"(sbase), "s"(lds) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(voff), "s"(sbase), "s"(lds) : "memory", "m0");
 }
 template <int kImm = 0>
 __device__ __forceinline__ void dma4(uint32_t voff, const void* sbase, uint32_t lds) {
     if constexpr (kImm == 0)
-        asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(sbase), "s"(lds)
+        asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(sbase), "s"(lds)
                      : "memory", "m0");
     else
-        asm volatile("s_add_u32 m0, %2, %3\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(sbase), "s"(lds),
+        asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(sbase), "s"(lds),
                      "n"(kImm)
                      : "memory", "m0", "scc");
 }
 // Lane l's 16 bytes at an address of its own to LDS byte lds + 16 l.
 __device__ __forceinline__ void dma16_at(const void* p, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(lds) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(lds) : "memory", "m0");
 }
 // Lane l's dword at an address of its own to LDS byte lds + 4 l.
 __device__ __forceinline__ void dma4_at(const void* p, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(p), "s"(lds) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(p), "s"(lds) : "memory", "m0");
 }
 #pragma clang diagnostic pop
 

@@ -135,14 +135,14 @@ __device__ __forceinline__ void dma16_pol(uint32_t voff, const void* sbase, uint
     if constexpr (kPol == 0) {
         w4a16::dma16<kImm>(voff, sbase, lds);
     } else if constexpr (kPol == 1) {
-        asm volatile("s_add_u32 m0, %2, %3\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(voff), "s"(sbase), "s"(lds), "n"(kImm)
+        asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(voff), "s"(sbase), "s"(lds), "n"(kImm)
                      : "memory", "m0", "scc");
     } else if constexpr (kPol == 2) {
-        asm volatile("s_add_u32 m0, %2, %3\n\tglobal_load_lds_dwordx4 %0, %1 sc0 sc1" ::"v"(voff), "s"(sbase), "s"(lds),
+        asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 sc0 sc1" ::"v"(voff), "s"(sbase), "s"(lds),
                      "n"(kImm)
                      : "memory", "m0", "scc");
     } else {
-        asm volatile("s_add_u32 m0, %2, %3\n\tglobal_load_lds_dwordx4 %0, %1 sc1" ::"v"(voff), "s"(sbase), "s"(lds), "n"(kImm)
+        asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 sc1" ::"v"(voff), "s"(sbase), "s"(lds), "n"(kImm)
                      : "memory", "m0", "scc");
     }
 }

@@ -5,8 +5,9 @@
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
+#include <memory>
 #include <mutex>
-#include <vector>
+#include <new>
 
 #include "../../include/w4a16.h"
 #include "launch.h"
@@ -286,6 +287,21 @@ w4a16_status_t w4a16_check_weights(w4a16_format_t fmt, const float* W, int64_t N
     return W4A16_OK;
 }
 
+// Debug only: W copied to the host, some rows at a time (a copy of all could be more memory than there is, and an
+// exception must not leave a C entry point).
+static w4a16_status_t check_device_weights(w4a16_format_t fmt, const float* W, int64_t N, int64_t K, hipStream_t stream) {
+    const int64_t rows = std::min(N, std::max<int64_t>(1, ((int64_t)16 << 20) / K));
+    const std::unique_ptr<float[]> host(new (std::nothrow) float[(size_t)rows * (size_t)K]);
+    if (!host || hipStreamSynchronize(stream) != hipSuccess) return W4A16_ERR_DEVICE;
+    for (int64_t n = 0; n < N; n += rows) {
+        const int64_t here = std::min(rows, N - n);
+        if (hipMemcpy(host.get(), W + n * K, (size_t)here * (size_t)K * sizeof(float), hipMemcpyDeviceToHost) != hipSuccess)
+            return W4A16_ERR_DEVICE;
+        if (const w4a16_status_t st = w4a16_check_weights(fmt, host.get(), here, K); st != W4A16_OK) return st;
+    }
+    return W4A16_OK;
+}
+
 w4a16_status_t w4a16_quantize_pack(w4a16_format_t fmt, const float* W, int64_t N, int64_t K, void* codes,
                                    void* scales, void* mins, hipStream_t stream) {
     w4a16_status_t st = check_shape(fmt, N, K);
@@ -294,12 +310,8 @@ w4a16_status_t w4a16_quantize_pack(w4a16_format_t fmt, const float* W, int64_t N
     st = check_packed(fmt, codes, scales, mins);
     if (st != W4A16_OK) return st;
     w4a16::clear_stale_error();
-    if (debug_checks_enabled()) {  // debug only: a synchronous copy of W to the host
-        std::vector<float> host((size_t)N * (size_t)K);
-        if (hipStreamSynchronize(stream) != hipSuccess ||
-            hipMemcpy(host.data(), W, host.size() * sizeof(float), hipMemcpyDeviceToHost) != hipSuccess)
-            return W4A16_ERR_DEVICE;
-        st = w4a16_check_weights(fmt, host.data(), N, K);
+    if (debug_checks_enabled()) {
+        st = check_device_weights(fmt, W, N, K, stream);
         if (st != W4A16_OK) return st;
     }
     if (fmt == W4A16_FMT_G128_ASYM_BF16)

@@ -136,8 +136,9 @@ w4a16_status_t w4a16_packed_sizes(w4a16_format_t fmt, int64_t N, int64_t K,
  * bytes differently" (Q4: per (n, block) absmax/7 fp16 scale, codes + 8).
  * Output arrays as described by w4a16_format_t, all written in full (mins: G128 only; NULL
  * for Q4).  The result is bit-identical to the CPU definition.  With W4A16_DEBUG_CHECKS set, the
- * call first synchronizes `stream`, copies W to host memory it allocates and frees, and returns
- * the status of w4a16_check_weights on it (ERR_INVALID before any launch). */
+ * call first synchronizes `stream`, copies W to host memory it allocates and frees (at most 64 MiB,
+ * some rows at a time; ERR_DEVICE where there is none), and returns the status of
+ * w4a16_check_weights on it (ERR_INVALID before any launch). */
 w4a16_status_t w4a16_quantize_pack(w4a16_format_t fmt, const float* W, int64_t N, int64_t K,
                                    void* codes, void* scales, void* mins, hipStream_t stream);
 

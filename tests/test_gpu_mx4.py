@@ -228,6 +228,62 @@ def test_whole_numbers_are_exact(M, N, K):
     assert torch.equal(y.double(), xv @ wv.t().contiguous())
 
 
+# Shapes of the tilings that the shapes above leave out, and of K that ends in the first or second half of a k-tile of 256
+# or with it, for each tiling (tests/test_w4a4_plan_cpu.py works out which takes which).
+WIDE_SHAPES = [(1043, 7365, 1056), (1201, 6501, 672), (1546, 5061, 768), (520, 7245, 1056), (535, 7241, 928), (645, 6001, 768),
+               (3655, 1037, 288), (515, 4100, 1056), (530, 4103, 672), (900, 1501, 1024), (300, 2051, 1024), (301, 2050, 416),
+               (205, 1031, 2208)]
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("M,N,K", WIDE_SHAPES)
+def test_tilings(M, N, K, kind):
+    """Random elements of every kind with random scales against 64 bits; then whole numbers, exactly: every sum is one
+    below 2^24, rounded once to the output type."""
+    act, dt, u, tiny = TYPES[kind]
+    rng = np.random.default_rng(M + N + K)
+    m = Arena()
+
+    def arrays(R, codes, scales):
+        code, scale = rng.choice(codes, (R, K)).astype(np.uint8), rng.choice(scales, (R, K // 32)).astype(np.uint8)
+        q, s = packed(code, scale)
+        s[s == 0] = 0xFF  # (what pads the scales is of no effect)
+        return m.put(torch.from_numpy(q)), m.put(torch.from_numpy(s)), values(code, scale).cuda()
+
+    for codes, scales in ((np.arange(16), np.arange(119, 127)), ([0, 2, 4, 10, 12], [127, 128])):
+        xq, xs, xv = arrays(M, codes, scales)
+        wq, ws, wv = arrays(N, codes, scales)
+        y = m.out((M, N), dt)
+        w.w4a16_gemm_w4a4(MX4, act, xq, xs, M, wq, ws, None, N, K, y)
+        wv = wv.t().contiguous()
+        ref, mag = xv @ wv, xv.abs() @ wv.abs()
+        if len(codes) == 16:
+            err = (y.double() - ref).abs() - (u * ref.abs() + (1 + u) * K * 2 * F * mag + tiny)
+            assert not y.isnan().any() and err.max().item() <= 0
+        else:
+            assert mag.max() < 2 ** 24 and torch.equal(y, ref.to(dt))
+        m.check()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 61, 96), (9, 300, 288), (37, 130, 544), (300, 2051, 160)])
+def test_scales_far_from_one(M, N, K):
+    """Scales over the whole range of their byte, whose products are near one, exactly; and products below fp32's
+    normal numbers, which may be taken as zero."""
+    rng = np.random.default_rng(17)
+    code = [rng.choice([0, 2, 4, 10], (R, K)).astype(np.uint8) for R in (M, N)]
+    for sx, sw in ((0, 252), (252, 0), (2, 252), (252, 2), (27, 227), (227, 27), (57, 57), (1, 1)):
+        a, b = (packed(c, np.full((c.shape[0], K // 32), s, np.uint8)) for c, s in zip(code, (sx, sw)))
+        (xq, xs), (wq, ws) = ((torch.from_numpy(q).cuda(), torch.from_numpy(s).cuda()) for q, s in (a, b))
+        y = torch.empty((M, N), device="cuda")
+        w.w4a16_gemm_w4a4(MX4, w.W4A16_FP32, xq, xs, M, wq, ws, None, N, K, y)
+        ones = [values(c, np.full((c.shape[0], K // 32), 127, np.uint8)).cuda() for c in code]
+        ref = (ones[0] @ ones[1].t().contiguous()) * 2.0 ** (sx + sw - 254)
+        if sx + sw > 200:
+            assert torch.equal(y.double(), ref)
+        else:
+            assert ((y.double() - ref).abs() <= 2.0 ** -126).all()
+
+
 # weights from 64 MiB on, which few rows read past the caches' usual order
 @pytest.mark.parametrize("M,N,K", [(1, 33005, 4096), (2, 20001, 7200), (5, 17008, 8192), (16, 70000, 2080)])
 def test_few_rows_of_large_weights(M, N, K):

@@ -125,6 +125,21 @@ def test_large_weights(T, topk, E, H, I):
     check(run(d, "bf16"), d, "bf16")
 
 
+# Up products of 512 blocks, which run with three stages a wave, and of more, with two: tiles of 8 pairs and of 16, weights
+# below 64 MiB and from there on, which pass the caches by
+@pytest.mark.parametrize("bits", [32, 64])
+@pytest.mark.parametrize("T,topk,E,H,I", [(8, 1, 8, 144, 4096), (8, 1, 8, 144, 4112), (8, 2, 8, 144, 4112), (32, 8, 64, 512, 1040), (32, 8, 3, 2064, 4112),
+                                          (32, 4, 4, 96, 4112)])
+def test_many_blocks(T, topk, E, H, I, bits):
+    d = data(T, topk, E, H, I, 11, 0.0)
+    if topk == 1:
+        d["ids"][:, 0] = torch.arange(T)  # a tile each
+    check(run(d, "bf16", bits=bits), d, "bf16")
+    if E == 64:  # the same eight experts for all
+        d["ids"][:] = torch.arange(8) * 7 + 3
+        check(run(d, "f32", bits=bits), d, "f32")
+
+
 # 63 to 65 pairs: one wave's, and the first that are not; some with no expert, some experts with one pair, some with many
 @pytest.mark.parametrize("T,topk", [(9, 7), (8, 8), (32, 2), (13, 5), (1, 64), (1, 65)])
 @pytest.mark.parametrize("E", [2, 7, 512])

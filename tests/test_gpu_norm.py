@@ -244,6 +244,34 @@ def test_large_arrays(T, N):
         test_norm_i8(T, N, "bf16", 1, 1)
 
 
+# one to sixteen waves a row and longer rows; one block, many, and arrays from 32 MiB on, in whole units and ragged rows
+@pytest.mark.parametrize("kind,T,N", [
+    ("bf16", 8, 496), ("f16", 17, 1001), ("f32", 77, 500), ("f32", 300, 17000), ("bf16", 2100, 20000), ("f16", 333, 33333),
+    ("bf16", 35000, 496), ("f16", 17000, 1001), ("bf16", 4300, 4000), ("f16", 4200, 4097), ("bf16", 2100, 8176), ("f16", 1101, 15601),
+    ("f32", 33000, 500), ("f32", 17000, 501), ("f32", 9001, 1000), ("f32", 4200, 2001), ("f32", 2300, 4000), ("f32", 1100, 8190)])
+def test_gradient_of_the_weight_exactly(kind, T, N):
+    """Rows of +-1 have the factor 1 with eps = 0, and whole numbers dy make each column's sum a whole number below 2^24,
+    which any order of additions gives: a row lost or taken twice, in a block's rows or among the parts, shows."""
+    act, dt = TYPES[kind][:2]
+    g = torch.Generator(device="cuda").manual_seed(T + N)
+    h = torch.randint(0, 2, (T, N), generator=g, device="cuda", dtype=torch.int8) * 2 - 1
+    dy = torch.randint(-7, 8, (T, N), generator=g, device="cuda", dtype=torch.int8)
+    ref = (h * dy).sum(0, dtype=torch.int64)
+    dx, dw = torch.empty((T, N), dtype=dt, device="cuda"), torch.full((N,), float("nan"), device="cuda")
+    ws, nb = w.alloc_add_rmsnorm_backward_workspace(T, N)
+    w.w4a16_add_rmsnorm_backward(act, dy.to(dt), None, h.to(dt), T, N, None, 0.0, dx, dw, ws, nb)
+    assert torch.equal(dw.double(), ref.double())
+
+
+def test_gradient_of_the_weight_past_32_bit_offsets():
+    N = 4096
+    T = (1 << 31) // N + 5
+    h = torch.ones((T, N), dtype=torch.bfloat16, device="cuda")
+    dw, (ws, nb) = torch.empty(N, device="cuda"), w.alloc_add_rmsnorm_backward_workspace(T, N)
+    w.w4a16_add_rmsnorm_backward(w.W4A16_BF16, h, None, h, T, N, None, 0.0, None, dw, ws, nb)
+    assert (dw == T).all()
+
+
 @pytest.mark.parametrize("T,N", [(3, 24), (2, 33)])
 def test_gradients_against_differences(T, N):
     """Of L = sum(y dy) + sum(h dh) by the formulas in 64 bits: central differences with a step of 2^-12 are off by

@@ -310,7 +310,7 @@ w4a16_status_t w4a16_quantize_pack(w4a16_format_t fmt, const float* W, int64_t N
     st = check_packed(fmt, codes, scales, mins);
     if (st != W4A16_OK) return st;
     w4a16::clear_stale_error();
-    if (debug_checks_enabled()) {
+    if (fmt != W4A16_FMT_MX4_B32_E8M0 && debug_checks_enabled()) {  // (MX4 defines what any weights give)
         st = check_device_weights(fmt, W, N, K, stream);
         if (st != W4A16_OK) return st;
     }

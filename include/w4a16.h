@@ -38,7 +38,8 @@
  *    N needs no particular multiple.  N above 2^26 or K above 2^22 returns
  *    W4A16_ERR_UNSUPPORTED: the kernels address operands as a 64-bit base plus a 32-bit
  *    per-lane byte offset.
- *  - Weights given to the quantizers must be finite (non-finite input is undefined).
+ *  - Weights given to the quantizers must be finite (non-finite input is undefined), but for MX4, which
+ *    defines what they give.
  */
 #ifndef W4A16_H
 #define W4A16_H
@@ -136,7 +137,7 @@ w4a16_status_t w4a16_packed_sizes(w4a16_format_t fmt, int64_t N, int64_t K,
  * bytes differently" (Q4: per (n, block) absmax/7 fp16 scale, codes + 8).
  * Output arrays as described by w4a16_format_t, all written in full (mins: G128 only; NULL
  * for Q4).  The result is bit-identical to the CPU definition.  With W4A16_DEBUG_CHECKS set, the
- * call first synchronizes `stream`, copies W to host memory it allocates and frees (at most 64 MiB,
+ * call (but for MX4, which takes any weights) first synchronizes `stream`, copies W to host memory it allocates and frees (at most 64 MiB,
  * some rows at a time; ERR_DEVICE where there is none), and returns the status of
  * w4a16_check_weights on it (ERR_INVALID before any launch). */
 w4a16_status_t w4a16_quantize_pack(w4a16_format_t fmt, const float* W, int64_t N, int64_t K,
@@ -153,7 +154,9 @@ w4a16_status_t w4a16_quantize_pack(w4a16_format_t fmt, const float* W, int64_t N
  * otherwise.  Pure host code: no HIP call, no allocation.  Shape checks as w4a16_packed_sizes.
  * w4a16_quantize_pack runs this check itself (on a host copy of W, after synchronizing `stream`)
  * when the environment variable W4A16_DEBUG_CHECKS is set to a value other than "0"; without it
- * the quantizers do not check, and non-finite or overflowing weights give undefined codes. */
+ * the quantizers do not check, and non-finite or overflowing weights give undefined codes.  For MX4
+ * too it says whether every weight is finite, for callers that want to know; the quantizer does not run it
+ * there, since the format defines blocks that are not. */
 w4a16_status_t w4a16_check_weights(w4a16_format_t fmt, const float* W_host, int64_t N, int64_t K);
 
 /* Reference dequant: W_hat [N][K] (row-major) in `out_dtype` (BF16, FP16 or FP32), each value

@@ -284,6 +284,19 @@ def test_scales_far_from_one(M, N, K):
             assert ((y.double() - ref).abs() <= 2.0 ** -126).all()
 
 
+def test_debug_checks_take_what_the_format_defines(monkeypatch):
+    """Weights that are not finite have codes in this format: the quantizer's debug check does not refuse them."""
+    N, K = 40, 288
+    wt = rows(N, K, torch.float32, 31)
+    wt[3, 40], wt[39, 287] = float("inf"), float("nan")
+    monkeypatch.setenv("W4A16_DEBUG_CHECKS", "1")
+    codes, scales, _ = w.alloc_packed(MX4, N, K)
+    w.w4a16_quantize_pack(MX4, wt.cuda(), N, K, codes, scales, None)
+    ref = packed(*quantized(wt))
+    np.testing.assert_array_equal(codes.cpu().numpy(), ref[0])
+    np.testing.assert_array_equal(scales.cpu().numpy(), ref[1])
+
+
 # weights from 64 MiB on, which few rows read past the caches' usual order
 @pytest.mark.parametrize("M,N,K", [(1, 33005, 4096), (2, 20001, 7200), (5, 17008, 8192), (16, 70000, 2080)])
 def test_few_rows_of_large_weights(M, N, K):

@@ -6,7 +6,8 @@
 // in 8 bits a = max|v| / 127, q = clamp(rint(v / a), -127, 127).  The norm is of the sum as it is in fp32, not of
 // the rounded h: h is what goes on, and one rounding of y is enough.
 // Gradients, of y = norm(h) for the h that was stored (g = dy w, r from h):
-//     dx = r (g - h r^2 sum_n(g h) / N) + dh,   dw_n = sum_t dy h r.
+//     dx = r (g - u sum_n(g u) / N) + dh,   dw_n = sum_t dy u,   u = h r:
+// with u and not h r^2, whose factor leaves fp32's range long before dx does (r of 2^64 on).
 //
 // Bytes bound all of these for many rows, and a row's chain of loads and reductions for few.  A row stays in registers
 // between its passes (kKeep units of 16 bytes a thread); what a long row has beyond that is read again, from the
@@ -318,20 +319,20 @@ __global__ __launch_bounds__(64 * grad_waves(kWaves)) void add_rmsnorm_backward_
             }
         row_sums<kWaves>(ss, gh, red[turn] + group * kWaves);
         turn ^= 1;
-        const float r = 1.0f / sqrtf(ss / (float)N + eps), c0 = gh / (float)N * (r * r);
+        const float r = 1.0f / sqrtf(ss / (float)N + eps), c = gh * r / (float)N;  // (the mean of g u)
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
-            const int c = tid + kThreads * i;
-            if (c >= units || m >= rows) continue;
+            const int at = tid + kThreads * i;
+            if (at >= units || m >= rows) continue;
             float o[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float hv = to_f32(hu[i].v[j]), g = to_f32(gu[i].v[j]);
-                dw[i][j] = __builtin_fmaf(g, hv * r, dw[i][j]);
-                o[j] = r * (g * to_f32(w[i].v[j]) - hv * c0);
+                const float u = to_f32(hu[i].v[j]) * r, g = to_f32(gu[i].v[j]);
+                dw[i][j] = __builtin_fmaf(g, u, dw[i][j]);
+                o[j] = r * (g * to_f32(w[i].v[j]) - u * c);
             }
             if (dx && dh) add(au[i], o);
-            if (dx) store_row_unit<kStream, kAny>(dx + m * N, c, N, o);
+            if (dx) store_row_unit<kStream, kAny>(dx + m * N, at, N, o);
         }
     }
     if (!part) return;
@@ -385,18 +386,18 @@ __global__ __launch_bounds__(64 * kWaves) void add_rmsnorm_backward_long_kernel(
         }
         row_sums<kWaves>(ss, gh, red[turn]);
         turn ^= 1;
-        const float r = 1.0f / sqrtf(ss / (float)N + eps), c0 = gh / (float)N * (r * r);
+        const float r = 1.0f / sqrtf(ss / (float)N + eps), c = gh * r / (float)N;  // (the mean of g u)
         if (rstd && threadIdx.x == 0) rstd[m] = r;
         if (!dx) continue;
-        for (int c = threadIdx.x; c < units; c += kThreads) {
+        for (int at = threadIdx.x; at < units; at += kThreads) {
             float hv[V], g[V], w[V];
-            widen(load_row_unit<false, true>(h + m * N, c, N), hv);
-            widen(load_row_unit<false, true>(dy + m * N, c, N), g);
-            if (weight) widen(load_row_unit<false, true>(weight, c, N), w);
+            widen(load_row_unit<false, true>(h + m * N, at, N), hv);
+            widen(load_row_unit<false, true>(dy + m * N, at, N), g);
+            if (weight) widen(load_row_unit<false, true>(weight, at, N), w);
 #pragma unroll
-            for (int j = 0; j < V; ++j) g[j] = r * ((weight ? g[j] * w[j] : g[j]) - hv[j] * c0);
-            if (dh) add(load_row_unit<false, true>(dh + m * N, c, N), g);
-            store_row_unit<false, true>(dx + m * N, c, N, g);
+            for (int j = 0; j < V; ++j) g[j] = r * ((weight ? g[j] * w[j] : g[j]) - hv[j] * r * c);
+            if (dh) add(load_row_unit<false, true>(dh + m * N, at, N), g);
+            store_row_unit<false, true>(dx + m * N, at, N, g);
         }
     }
 }

@@ -272,6 +272,33 @@ def test_gradient_of_the_weight_past_32_bit_offsets():
     assert (dw == T).all()
 
 
+def check_gradients(kind, dy, h, wt, eps):
+    act, dt, u, tiny = TYPES[kind]
+    T, N = h.shape
+    dx, dw = torch.empty((T, N), dtype=dt, device="cuda"), torch.empty(N, device="cuda")
+    ws, nb = w.alloc_add_rmsnorm_backward_workspace(T, N)
+    w.w4a16_add_rmsnorm_backward(act, dy.cuda(), None, h.cuda(), T, N, wt.cuda(), eps, dx, dw, ws, nb)
+    ref, ref_w, mag, mag_w = gradients(dy, None, h, wt, eps)
+    err = (dx.cpu().double() - ref).abs() - (u * ref.abs() + (1 + u) * (3 * REL(N) + 8 * F) * mag + tiny)
+    assert not dx.isnan().any() and err.max().item() <= 0
+    err = (dw.cpu().double() - ref_w).abs() - (REL(N) + (T + 64) * F) * mag_w
+    assert not dw.isnan().any() and err.max().item() <= 0
+
+
+SMALL = [("bf16", 512), ("f32", 500), ("bf16", 2048), ("f32", 8000), ("bf16", 15000), ("bf16", 20000), ("f32", 9001)]
+
+
+@pytest.mark.parametrize("kind,N", SMALL)
+def test_gradients_of_rows_whose_factor_is_large(kind, N):
+    """Rows of +-2^-65: their squares and the sum of these are exact, their factor is 2^65 with eps = 0, and its square
+    is past fp32's range."""
+    dt = TYPES[kind][1]
+    g = torch.Generator().manual_seed(41)
+    h = (torch.randint(0, 2, (5, N), generator=g) * 2 - 1).float() * 2.0 ** -65
+    dy, wt = torch.randn((5, N), generator=g), 1 + 0.3 * torch.randn(N, generator=g)
+    check_gradients(kind, dy.to(dt), h.to(dt), wt.to(dt), 0.0)
+
+
 @pytest.mark.parametrize("T,N", [(3, 24), (2, 33)])
 def test_gradients_against_differences(T, N):
     """Of L = sum(y dy) + sum(h dh) by the formulas in 64 bits: central differences with a step of 2^-12 are off by

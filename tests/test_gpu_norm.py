@@ -118,6 +118,23 @@ def test_codes_next_to_a_border():
     np.testing.assert_array_equal(xq.cpu().numpy(), np.clip(np.rint(yn / an[:, None]), -127, 127).astype(np.int8))
 
 
+def test_codes_next_to_a_border_with_a_small_eps():
+    """The same rows with an eps that is lost beside their mean square, which other kernels take than eps = 0: as many of the
+    values lie on borders."""
+    N, T, eps = 256, 64, 2.0 ** -60
+    q = np.arange(N) % 127 + 0.5
+    x = np.stack([(q / 127 * (1 + (t - 32) * 2.0 ** -24)).astype(np.float32) for t in range(T)])
+    x[:, 0] = 1.0
+    x = torch.from_numpy(x).cuda()
+    xq, a, y = torch.empty((T, N), dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda"), torch.empty((T, N), device="cuda")
+    w.w4a16_add_rmsnorm_i8(w.W4A16_FP32, x, None, T, N, None, eps, None, xq, a)
+    w.w4a16_add_rmsnorm(w.W4A16_FP32, x, None, T, N, None, eps, None, y)
+    yn = y.cpu().numpy()
+    an = np.abs(yn).max(1) / np.float32(127)
+    np.testing.assert_array_equal(a.cpu().numpy(), an)
+    np.testing.assert_array_equal(xq.cpu().numpy(), np.clip(np.rint(yn / an[:, None]), -127, 127).astype(np.int8))
+
+
 @pytest.mark.parametrize("kind", list(TYPES))
 @pytest.mark.parametrize("N", [512, 1001, 9000])
 def test_in_place(kind, N):
@@ -244,13 +261,15 @@ def test_large_arrays(T, N):
         test_norm_i8(T, N, "bf16", 1, 1)
 
 
-# one to sixteen waves a row and longer rows; one block, many, and arrays from 32 MiB on, in whole units and ragged rows
+# one to sixteen waves a row and longer rows; one block, many, and arrays from 32 MiB on, in whole units and ragged rows; with
+# eps = 0 and one that leaves a factor of 1 as it is (kernels of their own)
+@pytest.mark.parametrize("eps", [0.0, 2.0 ** -60])
 @pytest.mark.parametrize("kind,T,N", [
     ("bf16", 8, 496), ("f16", 17, 1001), ("f32", 77, 500), ("f32", 300, 17000), ("bf16", 2100, 20000), ("f16", 333, 33333),
     ("bf16", 35000, 496), ("f16", 17000, 1001), ("bf16", 4300, 4000), ("f16", 4200, 4097), ("bf16", 2100, 8176), ("f16", 1101, 15601),
     ("f32", 33000, 500), ("f32", 17000, 501), ("f32", 9001, 1000), ("f32", 4200, 2001), ("f32", 2300, 4000), ("f32", 1100, 8190)])
-def test_gradient_of_the_weight_exactly(kind, T, N):
-    """Rows of +-1 have the factor 1 with eps = 0, and whole numbers dy make each column's sum a whole number below 2^24,
+def test_gradient_of_the_weight_exactly(kind, T, N, eps):
+    """Rows of +-1 have the factor 1, and whole numbers dy make each column's sum a whole number below 2^24,
     which any order of additions gives: a row lost or taken twice, in a block's rows or among the parts, shows."""
     act, dt = TYPES[kind][:2]
     g = torch.Generator(device="cuda").manual_seed(T + N)
@@ -259,16 +278,17 @@ def test_gradient_of_the_weight_exactly(kind, T, N):
     ref = (h * dy).sum(0, dtype=torch.int64)
     dx, dw = torch.empty((T, N), dtype=dt, device="cuda"), torch.full((N,), float("nan"), device="cuda")
     ws, nb = w.alloc_add_rmsnorm_backward_workspace(T, N)
-    w.w4a16_add_rmsnorm_backward(act, dy.to(dt), None, h.to(dt), T, N, None, 0.0, dx, dw, ws, nb)
+    w.w4a16_add_rmsnorm_backward(act, dy.to(dt), None, h.to(dt), T, N, None, eps, dx, dw, ws, nb)
     assert torch.equal(dw.double(), ref.double())
 
 
-def test_gradient_of_the_weight_past_32_bit_offsets():
+@pytest.mark.parametrize("eps", [0.0, 2.0 ** -60])
+def test_gradient_of_the_weight_past_32_bit_offsets(eps):
     N = 4096
     T = (1 << 31) // N + 5
     h = torch.ones((T, N), dtype=torch.bfloat16, device="cuda")
     dw, (ws, nb) = torch.empty(N, device="cuda"), w.alloc_add_rmsnorm_backward_workspace(T, N)
-    w.w4a16_add_rmsnorm_backward(w.W4A16_BF16, h, None, h, T, N, None, 0.0, None, dw, ws, nb)
+    w.w4a16_add_rmsnorm_backward(w.W4A16_BF16, h, None, h, T, N, None, eps, None, dw, ws, nb)
     assert (dw == T).all()
 
 
@@ -289,14 +309,61 @@ SMALL = [("bf16", 512), ("f32", 500), ("bf16", 2048), ("f32", 8000), ("bf16", 15
 
 
 @pytest.mark.parametrize("kind,N", SMALL)
-def test_gradients_of_rows_whose_factor_is_large(kind, N):
+@pytest.mark.parametrize("eps", [0.0, 2.0 ** -109])
+def test_gradients_of_rows_whose_factor_is_large(kind, N, eps):
     """Rows of +-2^-65: their squares and the sum of these are exact, their factor is 2^65 with eps = 0, and its square
     is past fp32's range."""
     dt = TYPES[kind][1]
     g = torch.Generator().manual_seed(41)
     h = (torch.randint(0, 2, (5, N), generator=g) * 2 - 1).float() * 2.0 ** -65
     dy, wt = torch.randn((5, N), generator=g), 1 + 0.3 * torch.randn(N, generator=g)
-    check_gradients(kind, dy.to(dt), h.to(dt), wt.to(dt), 0.0)
+    check_gradients(kind, dy.to(dt), h.to(dt), wt.to(dt), eps)
+
+
+def small_rows(kind, N):
+    """Rows of magnitudes down to the type's smallest numbers."""
+    e = torch.arange(-36, -128 if kind == "bf16" else -144, -4).double()
+    x = torch.randn((len(e), N), generator=torch.Generator().manual_seed(42), dtype=torch.float64)
+    return (x * torch.exp2(e)[:, None]).to(TYPES[kind][1])
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-42, 1e-30])
+@pytest.mark.parametrize("kind,N", SMALL)
+def test_gradients_of_rows_whose_squares_vanish(kind, N, eps):
+    dt = TYPES[kind][1]
+    h = small_rows(kind, N)
+    g = torch.Generator().manual_seed(43)
+    dy, wt = torch.randn(h.shape, generator=g) * 2.0 ** -20, 1 + 0.3 * torch.randn(N, generator=g)
+    check_gradients(kind, dy.to(dt), h, wt.to(dt), float(np.float32(eps)))
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-42, 1e-30])
+@pytest.mark.parametrize("kind,N", [("bf16", 16), ("f32", 496), ("bf16", 2048), ("f32", 8000), ("bf16", 20000), ("f32", 9001)])
+def test_rows_whose_squares_vanish(kind, N, eps):
+    """Squares below fp32's smallest numbers enter the sum all the same."""
+    act, dt, u, _ = TYPES[kind]
+    x, eps = small_rows(kind, N), float(np.float32(eps))
+    T = x.shape[0]
+    wt = (1 + 0.3 * torch.randn(N, generator=torch.Generator().manual_seed(44))).to(dt)
+    _, v = reference(x, None, wt, eps)
+    small = 2.0 ** -149  # (values below fp32's normal numbers: half a step of these, and of the type's)
+    y = x.cuda()
+    h = torch.empty_like(y)
+    w.w4a16_add_rmsnorm(act, y, None, T, N, wt.cuda(), eps, h, y)
+    assert torch.equal(h.cpu(), x)
+    least = torch.finfo(dt).smallest_normal * 2 * u + small
+    assert not y.isnan().any() and ((y.cpu().double() - v).abs() <= (u + (1 + u) * REL(N)) * v.abs() + least).all()
+    if N % 16:
+        return
+    xq, a = torch.empty((T, N), dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    h = x.cuda()
+    w.w4a16_add_rmsnorm_i8(act, h, None, T, N, wt.cuda(), eps, h, xq, a)
+    assert torch.equal(h.cpu(), x)
+    top, a64 = v.abs().amax(1), a.cpu().double()
+    normal = top > 2.0 ** -110
+    assert ((a64 - top / 127).abs() <= (REL(N) + 2 * F) * top / 127)[normal].all()
+    err = (xq.cpu().double() * a64[:, None] - v).abs() - (a64[:, None] * (0.5 + 128 * 2 * F) + REL(N) * v.abs())
+    assert err[normal].max().item() <= 0
 
 
 @pytest.mark.parametrize("T,N", [(3, 24), (2, 33)])

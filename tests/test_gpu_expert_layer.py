@@ -140,6 +140,16 @@ def test_many_blocks(T, topk, E, H, I, bits):
         check(run(d, "f32", bits=bits), d, "f32")
 
 
+# the widest layers that a call takes, in either direction, with codes of the largest magnitude: sums next to 2^31
+@pytest.mark.parametrize("T,topk,E,H,I", [(32, 8, 3, 131056, 16), (3, 2, 2, 131056, 16), (32, 1, 2, 16, 131056), (2, 2, 2, 32, 131056)])
+def test_widest_layers(T, topk, E, H, I):
+    d = data(T, topk, E, H, I, 12, 0.0)
+    d["xq"][0] = 127
+    d["up"][0] = 127
+    d["up"][0, 1] = -127
+    check(run(d, "f32"), d, "f32")
+
+
 # 63 to 65 pairs: one wave's, and the first that are not; some with no expert, some experts with one pair, some with many
 @pytest.mark.parametrize("T,topk", [(9, 7), (8, 8), (32, 2), (13, 5), (1, 64), (1, 65)])
 @pytest.mark.parametrize("E", [2, 7, 512])

@@ -265,6 +265,46 @@ def test_tilings(M, N, K, kind):
         m.check()
 
 
+@pytest.mark.parametrize("M,N,K", WIDE_SHAPES)
+def test_blocks_that_are_not_numbers_in_every_tiling(M, N, K):
+    """A row's last block and a column's first: NaN in that row and column, whole numbers elsewhere."""
+    rng = np.random.default_rng(5)
+    code, scale = [rng.choice([0, 2, 4, 10], (R, K)).astype(np.uint8) for R in (M, N)], [np.full((R, K // 32), 127, np.uint8) for R in (M, N)]
+    scale[0][M // 2, -1] = scale[0][M - 1, 3] = scale[1][N // 3, 0] = 255
+    (xq, xs), (wq, ws) = ([torch.from_numpy(a).cuda() for a in packed(c, s)] for c, s in zip(code, scale))
+    xv, wv = (values(c, s).cuda() for c, s in zip(code, scale))
+    y = torch.empty((M, N), device="cuda")
+    w.w4a16_gemm_w4a4(MX4, w.W4A16_FP32, xq, xs, M, wq, ws, None, N, K, y)
+    bad = torch.zeros((M, N), dtype=torch.bool, device="cuda")
+    bad[[M // 2, M - 1]], bad[:, N // 3] = True, True
+    ref = xv.nan_to_num() @ wv.nan_to_num().t().contiguous()
+    assert y[bad].isnan().all() and torch.equal(y[~bad].double(), ref[~bad])
+
+
+@pytest.mark.parametrize("M,N", [(1, 17), (2, 40), (7, 33), (20, 70), (130, 50)])
+def test_longest_rows(M, N):
+    """K of 2^22, the most that a call takes: ones and zeros with scales of one, exactly, and x quantized on the way."""
+    K = 1 << 22
+    g = torch.Generator(device="cuda").manual_seed(M)
+    def ones(R):
+        t = torch.rand((R, K // 2), generator=g, device="cuda")  # of each pair of elements the first, the second, or none
+        return (t < 0.2).to(torch.uint8) * 2 + (t > 0.9).to(torch.uint8) * 0x20
+    def value(q):
+        return torch.stack([(q & 15) / 2, (q >> 4) / 2], -1).reshape(q.shape[0], K).float()
+    xq, wq = ones(M), ones(N)
+    xs, ws = (torch.full(w.alloc_packed(MX4, R, K)[1].shape, 127, dtype=torch.uint8, device="cuda") for R in (M, N))
+    y = torch.empty((M, N), device="cuda")
+    w.w4a16_gemm_w4a4(MX4, w.W4A16_FP32, xq, xs, M, wq, ws, None, N, K, y)
+    xv, wv = value(xq), value(wq)
+    ref = torch.zeros((M, N), dtype=torch.float64, device="cuda")
+    for k in range(0, K, 1 << 18):
+        ref += xv[:, k:k + (1 << 18)].double() @ wv[:, k:k + (1 << 18)].double().t().contiguous()
+    assert ref.max() < 2 ** 24 and torch.equal(y.double(), ref)
+    z, (room, nb) = torch.empty((M, N), device="cuda"), w.alloc_w4a4_workspace(MX4, M, N, K)
+    w.w4a16_matmul_w4a4(MX4, w.W4A16_FP32, xv * 4, M, wq, ws, None, N, K, z, room, nb)
+    assert torch.equal(z, y * 4)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 61, 96), (9, 300, 288), (37, 130, 544), (300, 2051, 160)])
 def test_scales_far_from_one(M, N, K):
     """Scales over the whole range of their byte, whose products are near one, exactly; and products below fp32's

@@ -159,6 +159,32 @@ def test_in_place(kind, N):
         assert torch.equal(xq, xq2) and torch.equal(a, a2) and torch.equal(r2, h)
 
 
+# rows in turn, the next asked for before one is written
+@pytest.mark.parametrize("kind,T,N", [("bf16", 9000, 512), ("f32", 700, 16000), ("f16", 1100, 4001), ("bf16", 300, 40000)])
+def test_many_rows_in_place(kind, T, N):
+    act = TYPES[kind][0]
+    x, res, wt = (t.cuda() for t in data(T, N, kind, 17))
+    h, y = torch.empty_like(x), torch.empty_like(x)
+    w.w4a16_add_rmsnorm(act, x, res, T, N, wt, EPS, h, y)
+    x2, r2 = x.clone(), res.clone()
+    w.w4a16_add_rmsnorm(act, x2, r2, T, N, wt, EPS, r2, x2)
+    assert torch.equal(r2, h) and torch.equal(x2, y)
+    dy, dh = torch.randn_like(x), torch.randn_like(x)
+    ws, nb = w.alloc_add_rmsnorm_backward_workspace(T, N)
+    dx, dw, dw2 = torch.empty_like(x), torch.empty(N, device="cuda"), torch.empty(N, device="cuda")
+    w.w4a16_add_rmsnorm_backward(act, dy, dh, h, T, N, wt, EPS, dx, dw, ws, nb)
+    w.w4a16_add_rmsnorm_backward(act, dy, dh, h, T, N, wt, EPS, dh, dw2, ws, nb)
+    assert torch.equal(dx, dh) and torch.equal(dw, dw2)
+
+
+def test_longest_rows():
+    """Of 2^22 elements, the most that a call takes."""
+    T, N = 3, 1 << 22
+    test_norm(T, N, "bf16", 1, 1, 1)
+    test_norm_i8(T, N, "f16", 1, 1)
+    test_gradients(T, N, "bf16", 1, 1)
+
+
 def test_in_place_long_i8():
     T, N = 3, 16 * 1600
     x, res, wt = (t.cuda() for t in data(T, N, "bf16", 8))

@@ -5,7 +5,7 @@
 //     r = 1 / sqrt(sum_n s_n^2 / N + eps),   v_n = (s_n r) w_n   (fp32),   y = v rounded once;
 // in 8 bits a = max|v| / 127, q = clamp(rint(v / a), -127, 127).  The norm is of the sum as it is in fp32, not of
 // the rounded h: h is what goes on, and one rounding of y is enough.
-// Gradients, of y = norm(h) for the h that was stored (g = dy w, r from h):
+// Gradients, of y = norm(h) for the h that was stored, which is all that a backward pass has of s (g = dy w, r from h):
 //     dx = r (g - u sum_n(g u) / N) + dh,   dw_n = sum_t dy u,   u = h r:
 // with u and not h r^2, whose factor leaves fp32's range long before dx does (r of 2^64 on).
 //

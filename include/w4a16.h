@@ -494,8 +494,11 @@ size_t w4a16_w4a4_workspace_bytes(w4a16_format_t fmt, int64_t M, int64_t N, int6
  * Row t of x and residual [T][N] (type `act`): s = x + residual in fp32 (residual NULL: s = x), and
  *   h [T][N]  s rounded to `act`: the sum that goes on past the layer; NULL where it is not wanted
  *   v = s r w in fp32 with r = 1 / sqrt(sum_n s^2 / N + eps), weight w [N] of type `act` (NULL: ones)
- * The norm is of s before it is rounded.  Sums are fp32 in a fixed order: bitwise reproducible.  eps finite
- * and not negative (with 0, a row of zeros is divided by zero: NaN); N at most 2^22 (ERR_UNSUPPORTED above).  A row whose
+ * The norm is of s before it is rounded, and w4a16_add_rmsnorm_backward's gradients are of the norm of h, which is s
+ * rounded: the two functions are one with fp32 activations and differ by a rounding of each element of s with 16-bit
+ * ones.  Where y is to be the norm of the stored sum, pass that sum as x, with no residual.  Sums are fp32 in a fixed order: bitwise reproducible.  eps finite
+ * and not negative (with 0, a row of zeros is divided by zero: NaN; rows whose squares vanish in fp32 are normed
+ * all the same); N at most 2^22 (ERR_UNSUPPORTED above).  A row whose
  * sum of squares passes fp32's range gets zeros, one with an infinity or NaN gets NaN where it has one (and zeros or NaN
  * besides); other rows are not touched by it.  h and y may each be x's or residual's own array (the same address),
  * but not one array for both; other overlaps are not allowed. */
@@ -510,7 +513,8 @@ w4a16_status_t w4a16_add_rmsnorm(w4a16_dtype_t act, const void* x, const void* r
 w4a16_status_t w4a16_add_rmsnorm_i8(w4a16_dtype_t act, const void* x, const void* residual, int64_t T, int64_t N,
                                     const void* weight, float eps, void* h, int8_t* xq, float* ascale, hipStream_t stream);
 
-/* Gradients of y = h r w, r = 1 / sqrt(sum_n h^2 / N + eps), for h [T][N] as w4a16_add_rmsnorm stored it: with
+/* Gradients of y = h r w, r = 1 / sqrt(sum_n h^2 / N + eps), for h [T][N] as w4a16_add_rmsnorm stored it (not of the
+ * unrounded sum that it normed, see there): with
  * g = dy w,
  *   dx [T][N]    r (g - h r^2 sum_n(g h) / N) + dh, of x and of residual alike (type `act`, rounded once); dh [T][N]
  *                is the gradient that reaches h itself (NULL: none)

@@ -47,8 +47,9 @@ constexpr int kOnes = 0x7F7F7F7F;  // scales of one, for blocks past K (their el
 // of R stages.  kX = false: x is not in the ring (which holds weights alone) but whole in LDS behind it, quantized by
 // the block from activations.
 //
-// What bounds it.  1024 x 14336 x 4096 takes 32-33 us in 256 x 256 tiles (3.7 PFLOP/s), 8192 rows 240 (4.0), 8192 cubed
-// 245 (4.5; hipBLASLt's product of this format 314).  A k-tile is 2048 cycles of matrix instructions a SIMD
+// What bounds it.  1024 x 14336 x 4096 takes 32-35 us in 256 x 256 tiles (3.4-3.7 PFLOP/s; the instructions alone reach 9.0 on
+// zeros and 6.3-6.9 on random bits), 8192 rows 240-257 (3.7-4.0), 8192 cubed 245-265 (4.15-4.5; hipBLASLt's product of this format
+// 314-327).  A k-tile is 2048 cycles of matrix instructions a SIMD
 // beside 2080 of LDS reads and writes a CU, so neither hides all of the other: 1.3 us a k-tile without copies, 1.7 with
 // (timing-only copies; 0.9 by the products alone).  The outputs, which all blocks write at once, are 5 us of the 32,
 // scale copies 1.  Four waves of 128 x 128, one a SIMD, read a third less from LDS and take 40.  Few rows: the weights'
